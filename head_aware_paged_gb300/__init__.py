@@ -12,6 +12,12 @@ supplies device memory and streams, the library's kernels do all the work.
     cache.append_kv(layer, [seq], [0, T], k, v)
     cache.append_kv(layer, [seq], [0, 1], k1, v1)
     out, lse = cache.decode(layer, [seq], q1)
+
+or, with unrotated projections (rotary embedding on the way into the pages)
+and scores capped by a tanh:
+
+    q1 = cache.append_kv_rope(layer, [seq], [0, 1], q1, k1, v1)
+    out, lse = cache.decode(layer, [seq], q1, score_cap=50.0)
 """
 from __future__ import annotations
 
@@ -23,11 +29,11 @@ from typing import List, Optional, Sequence
 import numpy as np
 import torch
 
-from ._lib import (EXPORTS, GLOBAL, KV_BF16, KV_FP8, LOCAL, RETRIEVAL, SegPagedError, SpConfig, SpHeadPolicy,
+from ._lib import (EXPORTS, GLOBAL, KV_BF16, KV_FP4, KV_FP8, LOCAL, RETRIEVAL, SegPagedError, SpConfig, SpHeadPolicy,
                    check, i32_array, i64_array, load)
 
 __all__ = ["Config", "Policy", "SegPagedCache", "SegPagedError", "GLOBAL", "LOCAL",
-           "RETRIEVAL", "KV_BF16", "KV_FP8", "load", "EXPORTS"] + list(EXPORTS)
+           "RETRIEVAL", "KV_BF16", "KV_FP8", "KV_FP4", "load", "EXPORTS"] + list(EXPORTS)
 
 
 @dataclass
@@ -43,7 +49,7 @@ class Config:
     max_idx_per_seq: int = 0
     max_tokens: int = 8192
     max_batch: int = 1
-    kv_dtype: int = 0          # KV_BF16, or KV_FP8 (e4m3 pages with per-channel scales)
+    kv_dtype: int = 0          # KV_BF16, KV_FP8 (e4m3 pages with per-channel scales) or KV_FP4 (4-bit pages)
 
     def to_c(self) -> SpConfig:
         return SpConfig(self.num_layers, self.num_q_heads, self.num_kv_heads, self.head_dim,
@@ -132,6 +138,39 @@ def sp_attention_decode(handle, layer: int, seq_ids: Sequence[int], q: torch.Ten
                         stream=None) -> None:
     check(load().sp_attention_decode(handle, layer, i32_array(seq_ids), len(seq_ids), _ptr(q),
                                      _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def sp_attention_prefill_capped(handle, layer: int, seq_ids: Sequence[int], cu_q: Sequence[int],
+                                q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, score_cap: float,
+                                out: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """sp_attention_prefill over scores capped by score_cap * tanh(s / score_cap)."""
+    check(load().sp_attention_prefill_capped(handle, layer, i32_array(seq_ids), len(seq_ids),
+                                             i32_array(cu_q), _ptr(q), _ptr(k), _ptr(v),
+                                             float(score_cap), _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def sp_attention_decode_capped(handle, layer: int, seq_ids: Sequence[int], q: torch.Tensor,
+                               score_cap: float, out: torch.Tensor,
+                               lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """sp_attention_decode over scores capped by score_cap * tanh(s / score_cap)."""
+    check(load().sp_attention_decode_capped(handle, layer, i32_array(seq_ids), len(seq_ids), _ptr(q),
+                                            float(score_cap), _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def sp_append_kv_rope(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequence[int],
+                      q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                      q_out: Optional[torch.Tensor] = None, pos: Optional[Sequence[int]] = None,
+                      rope_theta: float = 10000.0, inv_freq: Optional[Sequence[float]] = None,
+                      stream=None) -> None:
+    """Rotate q into q_out and k on its way into the pages (see the C header).
+    q, k, v [rows, heads, head_dim] with any row stride the header allows."""
+    fr = None
+    if inv_freq is not None:
+        fr = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
+    check(load().sp_append_kv_rope(handle, layer, i32_array(seq_ids), len(seq_ids), i32_array(cu_new),
+                                   None if pos is None else i64_array(pos), _ptr(q),
+                                   0 if q is None else q.stride(0), _ptr(k), k.stride(0), _ptr(v),
+                                   v.stride(0), _ptr(q_out), float(rope_theta), fr, _stream(stream)))
 
 
 def sp_attention_decode_static_scratch(handle, layer: int, seq_ids: Sequence[int],
@@ -335,18 +374,22 @@ class SegPagedCache:
             pass
 
     # views of the page pool: [num_pages, page_size, head_dim] bf16 each
-    def k_pool(self) -> torch.Tensor:
-        """K pages [num_pages][page_size][head_dim]: bf16, or uint8 e4m3 codes."""
+    def _half_pool(self, i: int) -> torch.Tensor:
         c = self.cfg
+        if c.kv_dtype == KV_FP4:
+            half = c.num_pages * (c.page_size // 16) * 1152
+            return self.pool[i * half:(i + 1) * half].view(c.num_pages, c.page_size // 16, 1152)
         half = c.num_pages * c.page_size * c.head_dim
         dt = torch.uint8 if c.kv_dtype == KV_FP8 else torch.bfloat16
-        return self.pool.view(dt)[:half].view(c.num_pages, c.page_size, c.head_dim)
+        return self.pool.view(dt)[i * half:(i + 1) * half].view(c.num_pages, c.page_size, c.head_dim)
+
+    def k_pool(self) -> torch.Tensor:
+        """K pages [num_pages][page_size][head_dim]: bf16, or uint8 e4m3 codes;
+        4-bit pages: [num_pages][page_size / 16][1152] bytes."""
+        return self._half_pool(0)
 
     def v_pool(self) -> torch.Tensor:
-        c = self.cfg
-        half = c.num_pages * c.page_size * c.head_dim
-        dt = torch.uint8 if c.kv_dtype == KV_FP8 else torch.bfloat16
-        return self.pool.view(dt)[half:2 * half].view(c.num_pages, c.page_size, c.head_dim)
+        return self._half_pool(1)
 
     def set_policy(self, seq: int, policies, stream=None) -> None:
         flat = []
@@ -364,23 +407,56 @@ class SegPagedCache:
         assert k.is_contiguous() and v.is_contiguous()
         sp_append_kv(self.handle, layer, seq_ids, cu_new, k, v, stream)
 
+    def append_kv_rope(self, layer: int, seq_ids, cu_new, q, k, v, pos=None, q_out=None,
+                       rope_theta: float = 10000.0, inv_freq=None, stream=None):
+        """Rotate the new tokens' q and k to their positions and write k and v
+        into the pages (sp_append_kv_rope): the positions after what each
+        sequence holds, or from pos[b] on (held ones are overwritten in place).
+        q (or None), k, v [rows, heads, head_dim] bf16, rows any stride apart
+        (views of one fused projection).  Returns the rotated queries."""
+        c = self.cfg
+        for x, heads in ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
+            assert x is None or (x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 3
+                                 and x.shape[1:] == (heads, c.head_dim) and x.shape[0] >= cu_new[-1]
+                                 and x.stride(2) == 1 and x.stride(1) == c.head_dim), \
+                "q, k, v: bf16 [rows, heads, head_dim] on the device, heads contiguous"
+        assert len(cu_new) == len(seq_ids) + 1 and (pos is None or len(pos) == len(seq_ids))
+        assert inv_freq is None or len(inv_freq) == c.head_dim // 2
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        assert q is None or (q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype == q.dtype)
+        sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out if q is not None else None,
+                          pos, rope_theta, inv_freq, stream)
+        return q_out
+
     def prefill(self, layer: int, seq_ids, cu_q, q, k, v, out=None, lse=None, want_lse=True,
-                stream=None):
+                score_cap: Optional[float] = None, stream=None):
+        """Causal attention of a chunk over its history and itself; with
+        score_cap the scores are capped by score_cap * tanh(s / score_cap)."""
         assert q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-        sp_attention_prefill(self.handle, layer, seq_ids, cu_q, q, k, v, out, lse, stream)
+        if score_cap is None:
+            sp_attention_prefill(self.handle, layer, seq_ids, cu_q, q, k, v, out, lse, stream)
+        else:
+            sp_attention_prefill_capped(self.handle, layer, seq_ids, cu_q, q, k, v, score_cap, out, lse,
+                                        stream)
         return out, lse
 
-    def decode(self, layer: int, seq_ids, q, out=None, lse=None, want_lse=True, stream=None):
+    def decode(self, layer: int, seq_ids, q, out=None, lse=None, want_lse=True,
+               score_cap: Optional[float] = None, stream=None):
+        """One query per sequence over its visible keys; score_cap as for prefill."""
         assert q.is_contiguous()
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-        sp_attention_decode(self.handle, layer, seq_ids, q, out, lse, stream)
+        if score_cap is None:
+            sp_attention_decode(self.handle, layer, seq_ids, q, out, lse, stream)
+        else:
+            sp_attention_decode_capped(self.handle, layer, seq_ids, q, score_cap, out, lse, stream)
         return out, lse
 
     def rope_realign(self, layer: int, seq_ids, delta: int, kv_head: int = -1, pos_lo: int = 0,

@@ -16,11 +16,12 @@ STATUS_NAMES = {0: "SP_OK", 1: "SP_ERR_INVALID_ARG", 2: "SP_ERR_OUT_OF_PAGES",
                 3: "SP_ERR_UNSUPPORTED", 4: "SP_ERR_CUDA", 5: "SP_ERR_DEVICE_STATUS",
                 6: "SP_ERR_TIMEOUT"}
 GLOBAL, LOCAL, RETRIEVAL = 0, 1, 2
-KV_BF16, KV_FP8 = 0, 1
+KV_BF16, KV_FP8, KV_FP4 = 0, 1, 4
 
 # Every symbol include/segpaged.h declares.
 EXPORTS = ("sp_required_bytes", "sp_cache_create", "sp_cache_destroy", "sp_set_policy",
            "sp_build_cache", "sp_append_kv", "sp_attention_prefill", "sp_attention_decode",
+           "sp_attention_prefill_capped", "sp_attention_decode_capped", "sp_append_kv_rope",
            "sp_attention_decode_static_scratch", "sp_rope_realign", "sp_pack_seq",
            "sp_unpack_seq", "sp_select_workspace_bytes", "sp_select_heavy_hitters",
            "sp_select_heavy_hitters_top_p", "sp_set_kv_scales",
@@ -70,6 +71,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sp_append_kv": [P, c_int32, I32P, c_int32, I32P, P, P, P],
         "sp_attention_prefill": [P, c_int32, I32P, c_int32, I32P, P, P, P, P, P, P],
         "sp_attention_decode": [P, c_int32, I32P, c_int32, P, P, P, P],
+        "sp_attention_prefill_capped": [P, c_int32, I32P, c_int32, I32P, P, P, P, ctypes.c_float, P, P, P],
+        "sp_attention_decode_capped": [P, c_int32, I32P, c_int32, P, ctypes.c_float, P, P, P],
+        "sp_append_kv_rope": [P, c_int32, I32P, c_int32, I32P, I64P, P, c_int64, P, c_int64, P, c_int64, P,
+                              c_double, POINTER(c_double), P],
         "sp_attention_decode_static_scratch": [P, c_int32, I32P, c_int32, P, P, P, P],
         "sp_rope_realign": [P, c_int32, I32P, c_int32, c_int32, c_int64, c_int64, c_int64,
                             c_double, P],

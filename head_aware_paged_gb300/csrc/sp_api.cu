@@ -31,6 +31,12 @@ struct Layout {
     size_t pool_total = 0;
 };
 
+// Bytes of one stored K or V row.
+size_t config_row_bytes(const sp_config* c) {
+    return c->kv_dtype == SP_KV_FP4_E2M1 ? (size_t)kFp4RowBytes
+                                         : (size_t)c->head_dim * (c->kv_dtype == SP_KV_FP8_E4M3 ? 1 : 2);
+}
+
 sp_status check_config(const sp_config* c) {
     if (!c) return fail(SP_ERR_INVALID_ARG, "config is null");
     if (c->num_layers < 1 || c->num_q_heads < 1 || c->num_kv_heads < 1)
@@ -54,10 +60,12 @@ sp_status check_config(const sp_config* c) {
         return fail(SP_ERR_UNSUPPORTED, "max_batch * num_kv_heads above 4096");
     if ((int64_t)c->num_layers * c->num_kv_heads > kMaxPolicyUnits)
         return fail(SP_ERR_UNSUPPORTED, "num_layers * num_kv_heads above 8192");
-    if (c->kv_dtype != SP_KV_BF16 && c->kv_dtype != SP_KV_FP8_E4M3)
+    if (c->kv_dtype != SP_KV_BF16 && c->kv_dtype != SP_KV_FP8_E4M3 && c->kv_dtype != SP_KV_FP4_E2M1)
         return fail(SP_ERR_INVALID_ARG, "unknown kv_dtype");
     if (c->kv_dtype == SP_KV_FP8_E4M3 && c->head_dim != 128)
         return fail(SP_ERR_UNSUPPORTED, "FP8 pages need head_dim 128");
+    if (c->kv_dtype == SP_KV_FP4_E2M1 && c->head_dim != 128)
+        return fail(SP_ERR_UNSUPPORTED, "FP4 pages need head_dim 128");
     return SP_OK;
 }
 
@@ -92,8 +100,7 @@ Layout make_layout(const sp_config* c) {
     L.split_o = o;  o = align_up(o + (size_t)kPrefillSplitSlots * 2 * 128 * c->head_dim * 4, 256);
     L.split_ml = o; o = align_up(o + (size_t)kPrefillSplitSlots * 2 * 128 * 2 * 4, 256);
     L.ws_total = o;
-    L.pool_total = 2 * (size_t)c->num_pages * c->page_size * c->head_dim *
-                   (c->kv_dtype == SP_KV_FP8_E4M3 ? 1 : 2);
+    L.pool_total = 2 * (size_t)c->num_pages * c->page_size * config_row_bytes(c);
     return L;
 }
 
@@ -222,6 +229,20 @@ size_t align_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
+bool valid_cap(float score_cap) { return score_cap >= kMinScoreCap && score_cap <= kMaxScoreCap; }
+
+Cap make_cap(float score_cap, int head_dim) {
+    const double log2e = 1.4426950408889634;
+    Cap r;
+    r.on = 1;
+    const double a = (double)score_cap * log2e;
+    r.k1 = (float)(2.0 * log2e / ((double)score_cap * std::sqrt((double)head_dim)));
+    r.a = (float)a;
+    r.b = (float)(2.0 * a);
+    r.ref = (float)std::min(a, 118.0 - a);
+    return r;
+}
+
 bool valid_layer(const sp_cache* c, int32_t l) { return l >= 0 && l < c->cfg.num_layers; }
 
 sp_status check_seq_list(const sp_cache* c, const int32_t* seq_ids, int32_t n_seqs) {
@@ -339,15 +360,16 @@ sp_status sp_cache_create(const sp_config* cfg, void* pool, void* meta, void* ws
     g.max_seqs = cfg->max_seqs; g.max_pages_unit = L.max_pages_unit;
     g.max_idx_per_seq = std::max(cfg->max_idx_per_seq, 1); g.num_pages = cfg->num_pages;
     g.fp8 = cfg->kv_dtype == SP_KV_FP8_E4M3 ? 1 : 0;
+    g.fp4 = cfg->kv_dtype == SP_KV_FP4_E2M1 ? 1 : 0;
     cudaError_t e = cudaGetDevice(&c->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
     if (e != cudaSuccess) { delete c; return cuda_fail(e, "device query"); }
-    // FP8 decode runs two CTAs per SM
-    c->decode_ctas = std::min(c->num_sms * (g.fp8 ? 2 : 1), kMaxDecodeCtas);
-    const size_t pool_half = (size_t)cfg->num_pages * cfg->page_size * cfg->head_dim;
-    // (FP8 pages: the same pointers address bytes; kernels cast them)
+    // FP8 decode runs two CTAs per SM, 4-bit decode two for up to 8 query heads per KV head
+    c->decode_ctas = std::min(c->num_sms * (g.fp8 || (g.fp4 && g.group <= 8) ? 2 : 1), kMaxDecodeCtas);
+    const size_t pool_half = (size_t)cfg->num_pages * cfg->page_size * config_row_bytes(cfg);
+    // (FP8 and 4-bit pages: the same pointers address bytes; kernels cast them)
     c->kpool = static_cast<__nv_bfloat16*>(pool);
-    c->vpool = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(pool) + pool_half * (g.fp8 ? 1 : 2));
+    c->vpool = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(pool) + pool_half);
     uint8_t* mb = static_cast<uint8_t*>(meta);
     c->meta.pol = reinterpret_cast<UnitPol*>(mb + L.pol);
     c->meta.npages = reinterpret_cast<int32_t*>(mb + L.npages);
@@ -383,10 +405,12 @@ sp_status sp_cache_create(const sp_config* cfg, void* pool, void* meta, void* ws
     // row is 128 bytes, one swizzle row
     const uint32_t box = g.fp8 ? (uint32_t)cfg->head_dim : 64u;
     const uint64_t rowb = (uint64_t)cfg->head_dim * (g.fp8 ? 1 : 2);
-    if (!encode_tmap_2d(&c->tm_kpool, c->kpool, cfg->head_dim, rows, rowb, box,
-                        cfg->page_size, true, &err, g.fp8) ||
-        !encode_tmap_2d(&c->tm_vpool, c->vpool, cfg->head_dim, rows, rowb, box,
-                        cfg->page_size, true, &err, g.fp8)) {
+    // (4-bit pages are read with untiled bulk copies: no map)
+    if (!g.fp4 &&
+        (!encode_tmap_2d(&c->tm_kpool, c->kpool, cfg->head_dim, rows, rowb, box,
+                         cfg->page_size, true, &err, g.fp8) ||
+         !encode_tmap_2d(&c->tm_vpool, c->vpool, cfg->head_dim, rows, rowb, box,
+                         cfg->page_size, true, &err, g.fp8))) {
         delete c;
         return fail(SP_ERR_CUDA, err);
     }
@@ -555,10 +579,10 @@ sp_status sp_append_kv(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
                         static_cast<cudaStream_t>(stream));
 }
 
-sp_status sp_attention_prefill(sp_cache* c, int32_t layer, const int32_t* seq_ids,
-                               int32_t n_seqs, const int32_t* cu_q, const void* q,
-                               const void* k, const void* v, void* out, float* lse,
-                               void* stream) {
+static sp_status attention_prefill(sp_cache* c, int32_t layer, const int32_t* seq_ids,
+                                   int32_t n_seqs, const int32_t* cu_q, const void* q,
+                                   const void* k, const void* v, void* out, float* lse,
+                                   const Cap& cap, void* stream) {
     if (!c || !cu_q || !q || !k || !v || !out) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     sp_status s = check_seq_list(c, seq_ids, n_seqs);
@@ -578,11 +602,12 @@ sp_status sp_attention_prefill(sp_cache* c, int32_t layer, const int32_t* seq_id
     if (cu_q[n_seqs] > c->cfg.max_tokens) return fail(SP_ERR_INVALID_ARG, "more rows than max_tokens");
     return prefill_impl(c, layer, seq_ids, n_seqs, cu_q, static_cast<const __nv_bfloat16*>(q),
                         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
-                        static_cast<__nv_bfloat16*>(out), lse, static_cast<cudaStream_t>(stream));
+                        static_cast<__nv_bfloat16*>(out), lse, cap, static_cast<cudaStream_t>(stream));
 }
 
-sp_status sp_attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
-                              const void* q, void* out, float* lse, void* stream) {
+static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                                  const void* q, void* out, float* lse, const Cap& cap,
+                                  void* stream) {
     if (!c || !q || !out) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     sp_status s = check_seq_list(c, seq_ids, n_seqs);
@@ -598,7 +623,8 @@ sp_status sp_attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids
     p->n_units = n_seqs * c->cfg.num_kv_heads;
     p->item_off[0] = 0;
     int64_t total = 0;
-    const int P = c->cfg.page_size;
+    p->cap = cap;
+    const int P = c->cfg.page_size, slots = decode_item_slots(c->geo);
     for (int b = 0; b < n_seqs; ++b) {
         const int seq = seq_ids[b];
         const int64_t n = c->h_seqlen[(size_t)seq * c->cfg.num_layers + layer];
@@ -607,7 +633,7 @@ sp_status sp_attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids
         p->tq[b] = (int32_t)(n - 1);
         for (int h = 0; h < c->cfg.num_kv_heads; ++h) {
             const UnitPol& u = c->h_pol[unit_index(c, seq, layer, h)];
-            total += decode_items(decode_ranges(u, host_idx(c, seq, u), n - 1, P), P);
+            total += decode_items(decode_ranges(u, host_idx(c, seq, u), n - 1, P), slots);
             p->item_off[b * c->cfg.num_kv_heads + h + 1] = (int32_t)total;
         }
     }
@@ -625,6 +651,37 @@ sp_status sp_attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     launch_mark_end(c, static_cast<cudaStream_t>(stream));
     return SP_OK;
+}
+
+sp_status sp_attention_prefill(sp_cache* c, int32_t layer, const int32_t* seq_ids,
+                               int32_t n_seqs, const int32_t* cu_q, const void* q,
+                               const void* k, const void* v, void* out, float* lse,
+                               void* stream) {
+    return attention_prefill(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse, Cap{}, stream);
+}
+
+sp_status sp_attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                              const void* q, void* out, float* lse, void* stream) {
+    return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse, Cap{}, stream);
+}
+
+sp_status sp_attention_prefill_capped(sp_cache* c, int32_t layer, const int32_t* seq_ids,
+                                      int32_t n_seqs, const int32_t* cu_q, const void* q,
+                                      const void* k, const void* v, float score_cap, void* out,
+                                      float* lse, void* stream) {
+    if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
+    if (!valid_cap(score_cap)) return fail(SP_ERR_INVALID_ARG, "score_cap must lie in [1/64, 64]");
+    return attention_prefill(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse,
+                             make_cap(score_cap, c->cfg.head_dim), stream);
+}
+
+sp_status sp_attention_decode_capped(sp_cache* c, int32_t layer, const int32_t* seq_ids,
+                                     int32_t n_seqs, const void* q, float score_cap, void* out,
+                                     float* lse, void* stream) {
+    if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
+    if (!valid_cap(score_cap)) return fail(SP_ERR_INVALID_ARG, "score_cap must lie in [1/64, 64]");
+    return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
+                            make_cap(score_cap, c->cfg.head_dim), stream);
 }
 
 sp_status sp_set_launch_events(sp_cache* c, void* start_event, void* end_event) {
@@ -654,7 +711,8 @@ sp_status sp_release_seq(sp_cache* c, int32_t seq, void* stream) {
 sp_status sp_set_kv_scales(sp_cache* c, int32_t layer, const float* k_scale, const float* v_scale,
                            void* stream) {
     if (!c || !k_scale || !v_scale) return fail(SP_ERR_INVALID_ARG, "null argument");
-    if (!c->geo.fp8) return fail(SP_ERR_INVALID_ARG, "scales apply to FP8 pages only");
+    if (!c->geo.fp8 && !c->geo.fp4)
+        return fail(SP_ERR_INVALID_ARG, "scales apply to FP8 and FP4 pages only");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     for (int s = 0; s < c->cfg.max_seqs; ++s)
         if (c->h_seqlen[(size_t)s * c->cfg.num_layers + layer] != 0)
@@ -785,7 +843,7 @@ sp_status sp_pack_seq(sp_cache* c, int32_t seq, void* dst, size_t dst_bytes, siz
         row_off += rows;
         blk_off += (rows + kTransferRows - 1) / kTransferRows;
     }
-    const size_t payload_bytes = (size_t)row_off * 2 * d * (c->geo.fp8 ? 1 : 2);
+    const size_t payload_bytes = (size_t)row_off * 2 * c->geo.row_bytes();
     *ph = PackHeader{kPackMagic, 1, L, H, d, P, U, idx_total, (int64_t)payload_off,
                      (int64_t)payload_bytes, (int64_t)(payload_off + payload_bytes),
                      (int64_t)c->cfg.kv_dtype};
@@ -870,7 +928,7 @@ sp_status sp_unpack_seq(sp_cache* c, int32_t seq, const void* src, size_t src_by
         blocks += (x.rows + kTransferRows - 1) / kTransferRows;
         io += x.n_idx;
     }
-    if (ph.payload_bytes != rows_total * 2 * c->cfg.head_dim * (c->geo.fp8 ? 1 : 2))
+    if (ph.payload_bytes != rows_total * 2 * c->geo.row_bytes())
         return fail(SP_ERR_INVALID_ARG, "packed payload size does not match its units");
     if (demand > c->h_free)
         return fail(SP_ERR_OUT_OF_PAGES, "unpack needs " + std::to_string(demand) + " pages, " +
@@ -996,7 +1054,7 @@ sp_status sp_count_decode_bytes(const sp_cache* c, int32_t layer, const int32_t*
             total += visible_count(u, host_idx(c, seq_ids[b], u), t[b]);
         }
     }
-    *bytes = total * 2 * c->cfg.head_dim * (c->geo.fp8 ? 1 : 2);   // K + V rows of the page type
+    *bytes = total * 2 * c->geo.row_bytes();   // K + V rows of the page type
     return SP_OK;
 }
 

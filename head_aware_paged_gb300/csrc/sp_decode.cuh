@@ -1,4 +1,6 @@
-// sp_decode.cu -- split-KV decode over each head's own visible pages.
+// sp_decode.cuh -- split-KV decode over each head's own visible pages (bf16 and
+// FP8 pages; 4-bit pages: sp_decode4.cuh).  The kernel and its launcher; one
+// source file instantiates them for scores as they are, one for capped scores.
 //
 // One query per sequence reads, for every (sequence, KV head) unit, only the
 // pages holding that head's visible tokens (RedKnot SegPagedAttention runtime
@@ -23,6 +25,9 @@
 //     unnormalised partial (o, m, l); the last CTA to finish the unit (atomic
 //     ticket, no waiting) merges them: m* = max m_s, l* = sum 2^(m_s-m*) l_s,
 //     O = sum 2^(m_s-m*) o_s / l*.
+#pragma once
+#include <algorithm>
+
 #include "sp_internal.h"
 #include "sp_device.cuh"
 
@@ -65,7 +70,14 @@ __device__ __forceinline__ int64_t cta_of_item(int64_t x, int64_t T, int G) {
     return (x * G + G - 1) / T;
 }
 
-template <int D, int P, bool F8>
+// A raw product q . k in log2 units of the softmax, capped by a tanh
+// (Cap, sp_internal.h): two MUFU operations on top of the exponential's one,
+// hidden behind the page stream.
+__device__ __forceinline__ float capped_log2(float x, const Cap& cap) {
+    return cap.a - __fdividef(cap.b, 1.f + fast_exp2(x * cap.k1));
+}
+
+template <int D, int P, bool F8, bool CAP>
 __global__ void __launch_bounds__(kDecodeThreads, F8 ? 2 : 1)
 k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmK,
          const __grid_constant__ CUtensorMap tmV) {
@@ -345,7 +357,8 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                 for (int nt = 0; nt < NT; ++nt)
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[nt][e] *= p.scale_log2;
+                        if constexpr (CAP) sc[nt][e] = capped_log2(sc[nt][e], p.cap);
+                        else sc[nt][e] *= p.scale_log2;
                         mx[e >> 1] = fmaxf(mx[e >> 1], sc[nt][e]);
                     }
             } else {
@@ -354,7 +367,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = key0 + nt * 8 + qc + (e & 1);
-                        float v = sc[nt][e] * p.scale_log2;
+                        float v = CAP ? capped_log2(sc[nt][e], p.cap) : sc[nt][e] * p.scale_log2;
                         if (key < lo || key >= hi) v = -INFINITY;
                         sc[nt][e] = v;
                         mx[e >> 1] = fmaxf(mx[e >> 1], v);
@@ -590,7 +603,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
     }
 }
 
-template <int D, int P, bool F8 = false>
+template <int D, int P, bool F8, bool CAP>
 cudaError_t launch_decode_t(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s) {
     using Sh = DecodeShape<D, P, F8>;
     // merge buffer: the four warps' [group][D] partials, or two [grid][group]
@@ -609,45 +622,40 @@ cudaError_t launch_decode_t(const sp_cache* c, DecodeParams& p, int grid, cudaSt
     }
     if (p.nst < 2) return cudaErrorInvalidConfiguration;
     const int smem = p.nst * Sh::kStageBytes + merge_bytes + Sh::kMiscBytes;
-    cudaError_t e = cudaFuncSetAttribute(k_decode<D, P, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(k_decode<D, P, F8, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Sh::kSmemCap);
     if (e != cudaSuccess) return e;
     if (Sh::kCtasPerSm > 1) {
-        e = cudaFuncSetAttribute(k_decode<D, P, F8>, cudaFuncAttributePreferredSharedMemoryCarveout,
+        e = cudaFuncSetAttribute(k_decode<D, P, F8, CAP>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  (int)cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
     }
     // the tensor maps' box is one stage's keys: a whole page, or half a page
     const CUtensorMap& tk = Sh::kSub == 2 ? c->tm_kpool_half : c->tm_kpool;
     const CUtensorMap& tv = Sh::kSub == 2 ? c->tm_vpool_half : c->tm_vpool;
-    k_decode<D, P, F8><<<grid, kDecodeThreads, smem, s>>>(p, tk, tv);
+    k_decode<D, P, F8, CAP><<<grid, kDecodeThreads, smem, s>>>(p, tk, tv);
     return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_decode(const sp_cache* c, DecodeParams& p, cudaStream_t s) {
-    // Persistent grid, but at least kMinItemsPerCta pages per CTA: a small batch
-    // then spreads one head over a few CTAs instead of dozens (fewer partials
-    // to merge).
-    constexpr int64_t kMinItemsPerCta = 8;
-    int grid = c->decode_ctas;
-    const int64_t want = (p.total_items + kMinItemsPerCta - 1) / kMinItemsPerCta;
-    if (want < grid) grid = (int)(want > 0 ? want : 1);
+// The instance for the cache's page type, head_dim and page size.
+template <bool CAP>
+cudaError_t launch_decode_any(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s) {
     const int D = c->geo.d, P = c->geo.page;
     if (c->geo.fp8) {   // FP8 pages: head_dim 128 only (checked at create)
         if (D != 128) return cudaErrorInvalidValue;
-        if (P == 16) return launch_decode_t<128, 16, true>(c, p, grid, s);
-        if (P == 32) return launch_decode_t<128, 32, true>(c, p, grid, s);
-        if (P == 64) return launch_decode_t<128, 64, true>(c, p, grid, s);
-        if (P == 128) return launch_decode_t<128, 128, true>(c, p, grid, s);
+        if (P == 16) return launch_decode_t<128, 16, true, CAP>(c, p, grid, s);
+        if (P == 32) return launch_decode_t<128, 32, true, CAP>(c, p, grid, s);
+        if (P == 64) return launch_decode_t<128, 64, true, CAP>(c, p, grid, s);
+        if (P == 128) return launch_decode_t<128, 128, true, CAP>(c, p, grid, s);
         return cudaErrorInvalidValue;
     }
-#define SP_DEC(DD, PP) if (D == DD && P == PP) return launch_decode_t<DD, PP>(c, p, grid, s);
+#define SP_DEC(DD, PP) if (D == DD && P == PP) return launch_decode_t<DD, PP, false, CAP>(c, p, grid, s);
     SP_DEC(64, 16) SP_DEC(64, 32) SP_DEC(64, 64) SP_DEC(64, 128)
     SP_DEC(128, 16) SP_DEC(128, 32) SP_DEC(128, 64) SP_DEC(128, 128)
 #undef SP_DEC
     return cudaErrorInvalidValue;
 }
+
+}  // namespace
 
 }  // namespace sp

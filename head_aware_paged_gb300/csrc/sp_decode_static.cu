@@ -95,7 +95,8 @@ extern "C" sp_status sp_attention_decode_static_scratch(sp_cache* c, int32_t lay
     p.n_units = (int32_t)n_units;
     p.item_off[0] = 0;
     int64_t total = 0;
-    const int P = c->cfg.page_size;
+    p.cap = Cap{};
+    const int P = c->cfg.page_size, slots = decode_item_slots(c->geo);
     for (int b = 0; b < n_seqs; ++b) {
         const int seq = seq_ids[b];
         const int64_t n = c->h_seqlen[(size_t)seq * c->cfg.num_layers + layer];
@@ -103,7 +104,7 @@ extern "C" sp_status sp_attention_decode_static_scratch(sp_cache* c, int32_t lay
         p.tq[b] = (int32_t)(n - 1);
         for (int h = 0; h < hkv; ++h) {
             const UnitPol& u = c->h_pol[((size_t)seq * c->cfg.num_layers + layer) * hkv + h];
-            total += decode_items(decode_ranges(u, c->h_idx[seq].data() + u.idx_off, n - 1, P), P);
+            total += decode_items(decode_ranges(u, c->h_idx[seq].data() + u.idx_off, n - 1, P), slots);
             p.item_off[b * hkv + h + 1] = (int32_t)total;
         }
     }

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "segpaged.h"
+#include "sp_fp4.cuh"
 #include "sp_rules.h"
 
 namespace sp {
@@ -38,6 +39,9 @@ struct Geo {
     int32_t layers, hq, hkv, group, d, page, max_seqs, max_pages_unit,
             max_idx_per_seq, num_pages;
     int32_t fp8;         // pages hold e4m3 codes (1 byte) instead of bf16
+    int32_t fp4;         // pages hold e2m1 codes and block scales (sp_fp4.cuh)
+    // bytes of one stored K or V row
+    __host__ __device__ int32_t row_bytes() const { return fp4 ? kFp4RowBytes : d * (fp8 ? 1 : 2); }
     __host__ __device__ int64_t unit_row(int seq, int layer, int h) const {
         return ((int64_t)seq * layers + layer) * hkv + h;
     }
@@ -51,6 +55,25 @@ struct CallSeqs {
     int32_t cnt[kMaxCallSeqs];   // new tokens / query rows
     int32_t row0[kMaxCallSeqs];  // first row in the call's packed tensors
 };
+
+// Scores capped by a tanh, s' = cap * tanh(s / cap), in log2 units of the raw
+// product x = q . k:  tanh(y) = 1 - 2 / (1 + e^2y), so
+//     s' log2(e) = a - b / (1 + 2^(k1 x)),
+// a = cap log2(e), b = 2 a, k1 = 2 log2(e) / (cap sqrt(d)).  2^(k1 x) may
+// overflow to infinity or underflow to 0: the quotient is then 0 or b, the
+// limits of tanh.
+struct Cap {
+    int32_t on;
+    float k1, a, b;
+    float ref;                   // prefill: fixed reference of the exponentials
+};
+Cap make_cap(float score_cap, int head_dim);
+constexpr float kMinScoreCap = 1.f / 64.f, kMaxScoreCap = 64.f;
+
+// Slots of one decode work item: a page, or for 4-bit pages a run of 64 slots
+// whatever the page size.
+constexpr int kFp4ItemSlots = 64;
+inline int decode_item_slots(const Geo& g) { return g.fp4 ? kFp4ItemSlots : g.page; }
 
 struct DecodeParams {
     Meta meta;
@@ -69,6 +92,7 @@ struct DecodeParams {
     float* part_ml;              // [(n_units + grid)][group][2]
     int32_t* counters;           // [n_units], zero between calls
     float scale_log2;            // log2(e) / sqrt(d)
+    Cap cap;                     // capped scores (cap.on = 0: as they are)
     int32_t nst;                 // pipeline stages (set by the launcher)
     int32_t owners;              // consumer warps that own stages (divides nst)
     int32_t merge_floats;        // merge buffer floats (set by the launcher)
@@ -161,7 +185,8 @@ struct sp_cache {
     cudaEvent_t stage_ev[kStaging] = {};
     size_t stage_bytes = 0;                       // size of each buffer
     int stage_next = 0;
-    bool prefill_checked[5][4] = {};             // [speculative ? 4 : two issuers ? 3 : FP8 ? 2 : D == 128][log2(P) - 4]: attributes set
+    // [capped ? 6 : 0 + (speculative ? 4 : two issuers ? 3 : 4-bit ? 5 : FP8 ? 2 : D == 128)][log2(P) - 4, or 0]: attributes set
+    bool prefill_checked[12][4] = {};
     // Caller's event pair armed by sp_set_launch_events for the next
     // attention call (both null when not armed).
     cudaEvent_t launch_ev[2] = {};
@@ -180,6 +205,7 @@ cudaError_t stage_copy(sp_cache* c, int slot, void* dst, size_t bytes, cudaStrea
 // nothing.  check_seq_list: 1..max_batch ids, each in range, with a policy,
 // none listed twice.
 bool valid_layer(const sp_cache* c, int32_t layer);
+bool valid_cap(float score_cap);
 sp_status check_seq_list(const sp_cache* c, const int32_t* seq_ids, int32_t n_seqs);
 
 // Armed launch events (sp_set_launch_events): the start is recorded right
@@ -213,6 +239,11 @@ cudaError_t launch_export(const sp_cache* c, int seq, int layer, int h, int32_t*
 cudaError_t launch_decode_counts(const sp_cache* c, int seq, int layer, int h,
                                  const int64_t* pos, int n, int32_t* out, cudaStream_t s);
 cudaError_t launch_decode(const sp_cache* c, DecodeParams& p, cudaStream_t s);
+// Instances for capped scores (sp_decode_capped.cu) and for 4-bit pages
+// (sp_decode4.cu, sp_decode4_capped.cu); launch_decode chooses.
+cudaError_t launch_decode_capped(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
+cudaError_t launch_decode4(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
+cudaError_t launch_decode4_capped(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
 cudaError_t launch_rope(const sp_cache* c, const RopeParams& p, cudaStream_t s);
 cudaError_t launch_transfer(const sp_cache* c, const TransferParams& p, cudaStream_t s);
 

@@ -15,7 +15,7 @@ constexpr int kPrefillSplitSlots = 256;
 sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
                        const int32_t* cu_q, const __nv_bfloat16* q, const __nv_bfloat16* k,
                        const __nv_bfloat16* v, __nv_bfloat16* out, float* lse,
-                       cudaStream_t stream);
+                       const Cap& cap, cudaStream_t stream);
 
 // For positions i >= held: |V(i)| as the prefill kernel's tile plan and mask
 // see it, for a chunk starting at the unit's current length (entries with

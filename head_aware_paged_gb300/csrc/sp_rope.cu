@@ -98,16 +98,45 @@ __device__ __forceinline__ void rotate16_fp8(uint4& xa, uint4& yb, const float* 
     yb = make_uint4(yw[0], yw[1], yw[2], yw[3]);
 }
 
+// 4-bit pages: the pair blocks b and b + 4 (dimensions i0 .. i0+15 and
+// i0+64 .. i0+79) of one row.  Dequantised with its block and channel scales,
+// rotated in fp32 with every product and sum rounded separately, and both
+// blocks quantised again like a write (new block scales from the new values).
+__device__ __forceinline__ void rotate_fp4(uint8_t* group, int s, int b, const float* cs, const float* sn,
+                                           const float* sx, const float* sy, const float* ix,
+                                           const float* iy) {
+    uint2* cx = reinterpret_cast<uint2*>(group + fp4_k_code(s, b));
+    uint2* cy = reinterpret_cast<uint2*>(group + fp4_k_code(s, b + 4));
+    uint8_t* scx = group + fp4_k_scale(s, b);
+    uint8_t* scy = group + fp4_k_scale(s, b + 4);
+    float x[16], y[16];
+    fp4_value16(*cx, *scx, x);
+    fp4_value16(*cy, *scy, y);
+    #pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float xv = __fmul_rn(x[k], sx[k]), yv = __fmul_rn(y[k], sy[k]);
+        x[k] = __fmul_rn(__fsub_rn(__fmul_rn(xv, cs[k]), __fmul_rn(yv, sn[k])), ix[k]);
+        y[k] = __fmul_rn(__fadd_rn(__fmul_rn(yv, cs[k]), __fmul_rn(xv, sn[k])), iy[k]);
+    }
+    uint32_t sc;
+    *cx = fp4_quant16(x, sc);
+    *scx = (uint8_t)sc;
+    *cy = fp4_quant16(y, sc);
+    *scy = (uint8_t)sc;
+}
+
+enum PageType { kPageBf16, kPageFp8, kPageFp4 };
+
 // One block per (unit, page) of the call, grid-strided: the unit comes from
 // a binary search of the page offsets.  A work item is 8 frequency pairs of
-// one row (16 for FP8 pages): a 16-byte load from each half of the row, the
-// rotation, two 16-byte stores.
-template <bool F8>
+// one row (16 for FP8 and 4-bit pages): a 16-byte (4-bit: 8-byte) load from
+// each half of the row, the rotation, two stores.
+template <PageType KV>
 __global__ void __launch_bounds__(256)
 k_rope(const __grid_constant__ RopeParams p, void* kpool_) {
     const Geo& g = p.geo;
     const int P = g.page, D = g.d, half = D / 2;
-    constexpr int kPairs = F8 ? 16 : 8;              // frequency pairs per work item
+    constexpr int kPairs = KV == kPageBf16 ? 8 : 16;              // frequency pairs per work item
     const int chunks = half / kPairs;                // work items per row
     const int items = P * chunks;
     const int32_t lo = (int32_t)min64(p.pos_lo, (int64_t)INT32_MAX);
@@ -137,7 +166,13 @@ k_rope(const __grid_constant__ RopeParams p, void* kpool_) {
             const int32_t pos = slot_pos32(pol, idx, pg * P + row, n, held_idx, P);
             if (pos < 0 || pos < lo || pos >= hi) continue;
             const int i0 = c * kPairs;
-            if constexpr (F8) {
+            if constexpr (KV == kPageFp4) {
+                uint8_t* group = static_cast<uint8_t*>(kpool_) + fp4_group_off(phys, row, P);
+                const int64_t so = ((int64_t)p.layer * g.hkv + h) * D;
+                rotate_fp4(group, row & 15, c, p.cs + i0, p.sn + i0, p.meta.kscale + so + i0,
+                           p.meta.kscale + so + half + i0, p.meta.kinv + so + i0,
+                           p.meta.kinv + so + half + i0);
+            } else if constexpr (KV == kPageFp8) {
                 uint8_t* r = static_cast<uint8_t*>(kpool_) + ((int64_t)phys * P + row) * D;
                 uint4* px = reinterpret_cast<uint4*>(r + i0);
                 uint4* py = reinterpret_cast<uint4*>(r + half + i0);
@@ -169,8 +204,9 @@ cudaError_t launch_rope(const sp_cache* c, const RopeParams& p, cudaStream_t s) 
     const int32_t total = p.page_off[p.n_units];
     if (total <= 0) return cudaSuccess;
     const int grid = total < 16 * c->num_sms ? total : 16 * c->num_sms;
-    if (c->geo.fp8) k_rope<true><<<grid, 256, 0, s>>>(p, c->kpool);
-    else k_rope<false><<<grid, 256, 0, s>>>(p, c->kpool);
+    if (c->geo.fp4) k_rope<kPageFp4><<<grid, 256, 0, s>>>(p, c->kpool);
+    else if (c->geo.fp8) k_rope<kPageFp8><<<grid, 256, 0, s>>>(p, c->kpool);
+    else k_rope<kPageBf16><<<grid, 256, 0, s>>>(p, c->kpool);
     return cudaGetLastError();
 }
 

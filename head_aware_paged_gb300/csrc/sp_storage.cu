@@ -119,7 +119,24 @@ __device__ __forceinline__ uint2 quant_e4m3x8(int4 x, const float* inv) {
     return make_uint2(out[0], out[1]);
 }
 
-// Copy the retained rows of each unit into its pages (16-byte vectors).
+// 16 bf16 values times their channels' reciprocal scales, in fp32.
+__device__ __forceinline__ void scaled16(const __nv_bfloat16* src, const float* inv, float (&x)[16]) {
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int4 r = __ldg(reinterpret_cast<const int4*>(src) + h);
+        const uint32_t w[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 p2 = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+            x[8 * h + 2 * e] = __low2float(p2) * __ldg(inv + 8 * h + 2 * e);
+            x[8 * h + 2 * e + 1] = __high2float(p2) * __ldg(inv + 8 * h + 2 * e + 1);
+        }
+    }
+}
+
+// Copy the retained rows of each unit into its pages (16-byte vectors; 4-bit
+// pages: one block of 16 dimensions a thread).
+template <bool F4>
 __global__ void __launch_bounds__(256)
 k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict__ k,
           const __nv_bfloat16* __restrict__ v, int64_t row_stride,
@@ -133,7 +150,7 @@ k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict
     const int32_t* idx = m.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off;
     const ItemRanges r = retained_items(pol, idx, n_old, n_new, g.page);
     const int64_t n0 = r.hi[0] - r.lo[0], n1 = r.hi[1] - r.lo[1];
-    const int vecs = g.d / 8;
+    const int vecs = g.d / (F4 ? 16 : 8);
     const int64_t total = (n0 + n1) * vecs;
     const int32_t* tab = m.ptab + row * g.max_pages_unit;
     for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < total;
@@ -146,6 +163,23 @@ k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict
         else { t = item; us = unit_slot(pol, idx, t, g.page); }
         const int32_t page = tab[us / g.page];
         if (page < 0 || page >= g.num_pages) { atomicOr(m.status, kStatusBadPage); continue; }
+        if constexpr (F4) {
+            const int64_t from = (cs.row0[b] + (t - n_old)) * row_stride + (int64_t)h * g.d + c * 16;
+            const int64_t so = ((int64_t)layer * g.hkv + h) * g.d + c * 16;
+            const int s16 = (int)(us % g.page) & 15;
+            const int64_t go = fp4_group_off(page, (int)(us % g.page), g.page);
+            uint8_t* kg = reinterpret_cast<uint8_t*>(kpool) + go;
+            uint8_t* vg = reinterpret_cast<uint8_t*>(vpool) + go;
+            float x[16];
+            uint32_t sc;
+            scaled16(k + from, m.kinv + so, x);
+            *reinterpret_cast<uint2*>(kg + fp4_k_code(s16, c)) = fp4_quant16(x, sc);
+            kg[fp4_k_scale(s16, c)] = (uint8_t)sc;
+            scaled16(v + from, m.vinv + so, x);
+            *reinterpret_cast<uint2*>(vg + fp4_v_code(s16, c)) = fp4_quant16(x, sc);
+            vg[fp4_v_scale(s16, c)] = (uint8_t)sc;
+            continue;
+        }
         const int64_t src = (cs.row0[b] + (t - n_old)) * row_stride + (int64_t)h * g.d + c * 8;
         const int64_t dst = ((int64_t)page * g.page + us % g.page) * g.d + c * 8;
         const int4 kv = __ldg(reinterpret_cast<const int4*>(k + src));
@@ -261,8 +295,12 @@ cudaError_t launch_scatter(const sp_cache* c, const CallSeqs& cs, int layer,
     int64_t gx = (work + 255) / 256;
     if (gx > 4096) gx = 4096;
     dim3 grid((unsigned)gx, (unsigned)(cs.n * c->geo.hkv));
-    k_scatter<<<grid, 256, 0, s>>>(c->meta, c->geo, cs, layer, k, v, row_stride,
-                                   c->kpool, c->vpool);
+    if (c->geo.fp4)
+        k_scatter<true><<<grid, 256, 0, s>>>(c->meta, c->geo, cs, layer, k, v, row_stride,
+                                             c->kpool, c->vpool);
+    else
+        k_scatter<false><<<grid, 256, 0, s>>>(c->meta, c->geo, cs, layer, k, v, row_stride,
+                                              c->kpool, c->vpool);
     return cudaGetLastError();
 }
 

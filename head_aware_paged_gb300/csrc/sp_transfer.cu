@@ -35,12 +35,35 @@ __device__ __forceinline__ void row_slot(const UnitPol& u, const int32_t* idx, i
     }
 }
 
+// A 4-bit row travels as its 64 code bytes in dimension order, then its 8
+// scales: nine 8-byte words, copied one by one between the page's order
+// (sp_fp4.cuh) and the payload.
+__device__ __forceinline__ void copy_fp4_word(uint8_t* group, int s, int w, bool v, uint8_t* pay,
+                                              bool unpack) {
+    uint2* word = reinterpret_cast<uint2*>(pay + w * 8);
+    if (w < 8) {
+        uint2* code = reinterpret_cast<uint2*>(group + (v ? fp4_v_code(s, w) : fp4_k_code(s, w)));
+        if (unpack) *code = *word;
+        else *word = *code;
+        return;
+    }
+    uint32_t x[2] = {0u, 0u};
+    if (unpack) { const uint2 t = *word; x[0] = t.x; x[1] = t.y; }
+    #pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        uint8_t* sc = group + (v ? fp4_v_scale(s, b) : fp4_k_scale(s, b));
+        if (unpack) *sc = (uint8_t)(x[b >> 2] >> (8 * (b & 3)));
+        else x[b >> 2] |= (uint32_t)*sc << (8 * (b & 3));
+    }
+    if (!unpack) *word = make_uint2(x[0], x[1]);
+}
+
 __global__ void __launch_bounds__(256)
 k_transfer(const __grid_constant__ TransferParams p, uint8_t* kpool, uint8_t* vpool) {
     const Geo& g = p.geo;
     const int P = g.page;
-    const int row_bytes = g.d * (g.fp8 ? 1 : 2);
-    const int vec = row_bytes / 16;                    // 16-byte chunks per row
+    const int row_bytes = g.row_bytes();
+    const int vec = g.fp4 ? 9 : row_bytes / 16;        // 16-byte chunks (4-bit: 8-byte words) per row
     for (int64_t blk = blockIdx.x; blk < p.total_blocks; blk += gridDim.x) {
         int a = 0, z = p.n_units - 1;                  // unit with blk_off[u] <= blk < blk_off[u+1]
         while (a < z) {
@@ -69,6 +92,11 @@ k_transfer(const __grid_constant__ TransferParams p, uint8_t* kpool, uint8_t* vp
             const int32_t phys = ptab[slot / P];
             if (phys < 0 || phys >= g.num_pages) {
                 atomicOr(p.meta.status, kStatusBadPage);
+                continue;
+            }
+            if (g.fp4) {
+                copy_fp4_word((kv ? vpool : kpool) + fp4_group_off(phys, slot % P, P), slot & 15, c, kv != 0,
+                              (kv ? vblk : kblk) + (int64_t)r * row_bytes, p.unpack != 0);
                 continue;
             }
             uint8_t* pool = (kv ? vpool : kpool) + ((int64_t)phys * P + slot % P) * row_bytes + c * 16;

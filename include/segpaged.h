@@ -103,14 +103,30 @@ typedef struct sp_config {
  * own rows enter its attention as the caller's bf16 values).
  * sp_rope_realign on FP8 pages dequantises each key with its channel
  * scales, rotates in fp32 (every product and sum rounded once) and writes
- * the codes again as a write would. */
-typedef enum { SP_KV_BF16 = 0, SP_KV_FP8_E4M3 = 1 } sp_kv_dtype;
+ * the codes again as a write would.
+ *
+ * SP_KV_FP4_E2M1 stores 72 bytes a row instead of 256 (head_dim 128 only):
+ * every 16 neighbouring dimensions share one scale, an unsigned float of 5
+ * exponent and 3 mantissa bits (0, 2^-17 .. 10240), the value nearest
+ * amax / 6; an element is the e2m1 value (0, .5, 1, 1.5, 2, 3, 4, 6, signed)
+ * nearest x / scale.  Both round to nearest, ties to even, and saturate; an
+ * element that is NaN is stored as 6 * scale and does not count in amax.  The
+ * channel scales of sp_set_kv_scales (1.0 until set) apply first, as for FP8:
+ * x * (1 / channel scale) is what the block quantises, and the stored value is
+ * code * scale * channel scale.  Every call that takes a cache takes such a
+ * one: decode multiplies code * scale (exact in f16) with q * channel scale
+ * in f16, prefill reads bf16(code * scale * channel scale), sp_rope_realign
+ * dequantises, rotates and quantises again with new block scales, and a packed
+ * row is its 64 code bytes (two dimensions a byte, the even one low), then its
+ * 8 scales. */
+typedef enum { SP_KV_BF16 = 0, SP_KV_FP8_E4M3 = 1, SP_KV_FP4_E2M1 = 4 } sp_kv_dtype;
 
 typedef struct sp_cache sp_cache;  /* opaque host handle */
 
 /* Bytes of the three caller-owned device buffers for cfg (host only, no GPU).
  *   pool: K pages then V pages, each [num_pages][page_size][head_dim] elements
- *         of kv_dtype (bf16, or one byte for FP8).
+ *         of kv_dtype (bf16, or one byte for FP8); FP4: [num_pages]
+ *         [page_size / 16][1152] bytes, 16 rows' codes and their scales.
  *   meta: page tables, policies, retrieval lists, free-page stack, status.
  *   ws:   per-call scratch (prefill work list, decode split partials). */
 sp_status sp_required_bytes(const sp_config* cfg, size_t* pool_bytes,
@@ -155,6 +171,38 @@ sp_status sp_append_kv(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
                        int32_t n_seqs, const int32_t* cu_new, const void* k,
                        const void* v, void* stream);
 
+/* Append with the rotary embedding applied on the way: new queries and keys
+ * arrive unrotated, as a fused projection leaves them.  For the c_b =
+ * cu_new[b+1] - cu_new[b] tokens of sequence seq_ids[b], whose positions are
+ * pos[b], pos[b] + 1, ...:
+ *   - q_out[row] = q[row] rotated to its position (bf16);
+ *   - k[row] rotated and v[row] go into the pages as sp_append_kv would write
+ *     them (the rotated key enters the page type with one rounding: no bf16
+ *     in between for FP8 and FP4 pages).
+ * The rotation is that of sp_rope_realign with delta = position: pair
+ * (i, i + head_dim/2) turns by position * w_i, w_i = rope_theta^(-2i/head_dim),
+ * or inv_freq[i] where inv_freq (host, [head_dim / 2], |w| <= 2^16) is given
+ * (rope_theta is then not read).  Frequencies are double, angles are reduced
+ * in 64-bit fixed point, cos, sin and the rotation are fp32.
+ *   pos: host array of first positions, 0 <= pos[b] <= tokens held, or null =
+ *     append at the end.  Positions below what the sequence holds are
+ *     overwritten in place wherever the head keeps them (recomputed tokens of
+ *     a reused segment), the rest is appended; no token is dropped, and the
+ *     length becomes max(held, pos[b] + c_b).
+ *   q [cu_new[n_seqs]] rows of num_q_heads * head_dim elements q_stride apart,
+ *     k and v likewise with num_kv_heads (strides in elements, multiples of 8,
+ *     at least a row); all 16-byte aligned.  q and q_out may both be null: keys
+ *     and values only.  q_out is contiguous; it may be q itself if q is.
+ * One launch, pages included; works for every page type and head class.  The
+ * current device must be the cache's.  Captured into a graph, a replay writes
+ * the same positions and pages again. */
+sp_status sp_append_kv_rope(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
+                            int32_t n_seqs, const int32_t* cu_new, const int64_t* pos,
+                            const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride,
+                            void* q_out, double rope_theta, const double* inv_freq,
+                            void* stream);
+
 /* EXECUTE, prefill (runtime article section 4): causal attention of a chunk.
  * Rows cu_q[b] .. cu_q[b+1]-1 of q belong to sequence seq_ids[b] and sit at
  * absolute positions n_b .. n_b + c_b - 1, where n_b is what (seq, layer)
@@ -179,6 +227,21 @@ sp_status sp_attention_prefill(sp_cache* cache, int32_t layer,
 sp_status sp_attention_decode(sp_cache* cache, int32_t layer,
                               const int32_t* seq_ids, int32_t n_seqs,
                               const void* q, void* out, float* lse, void* stream);
+
+/* The two attention calls with scores capped by a tanh: the softmax is taken
+ * of score_cap * tanh(s / score_cap), s = q . k / sqrt(head_dim), over each
+ * head's visible keys.  score_cap in [1/64, 64] (SP_ERR_INVALID_ARG
+ * otherwise); everything else is as for sp_attention_prefill and
+ * sp_attention_decode (lse is that of the capped scores). */
+sp_status sp_attention_prefill_capped(sp_cache* cache, int32_t layer,
+                                      const int32_t* seq_ids, int32_t n_seqs,
+                                      const int32_t* cu_q, const void* q,
+                                      const void* k, const void* v, float score_cap,
+                                      void* out, float* lse, void* stream);
+sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
+                                     const int32_t* seq_ids, int32_t n_seqs,
+                                     const void* q, float score_cap, void* out,
+                                     float* lse, void* stream);
 
 /* Decode without any device allocation by the caller for scratch: the same
  * computation as sp_attention_decode, but the split-KV scratch (partial
@@ -207,9 +270,10 @@ sp_status sp_attention_decode_static_scratch(sp_cache* cache, int32_t layer,
                                              const void* q, void* out, float* lse,
                                              void* stream);
 
-/* FP8 pages: the per-channel scales of `layer`.  k_scale, v_scale are host
+/* FP8 and FP4 pages: the per-channel scales of `layer`.  k_scale, v_scale are host
  * arrays [num_kv_heads][head_dim] of floats in [2^-14, 128]; the pages store
- * e4m3(x * (1 / scale)) with the reciprocal taken in fp32.  Decode rebuilds
+ * e4m3(x * (1 / scale)) with the reciprocal taken in fp32 (FP4: the block
+ * format of x * (1 / scale), see sp_kv_dtype).  Decode rebuilds
  * each element as code * scale in f16 (the scale rounded to f16 first), so the
  * range keeps scales normal in f16 and 448 * scale below the f16 maximum;
  * q and P enter the decode MMAs as f16 as well.  Only while no sequence holds
@@ -231,7 +295,8 @@ sp_status sp_set_kv_scales(sp_cache* cache, int32_t layer, const float* k_scale,
  * from the exact rotation of the stored value).  FP8 pages: each code is
  * dequantised with its channel's K scale, the pair rotated in fp32 with
  * every product and sum rounded once, and the results written as new codes
- * like a write (e4m3(v * fp32(1 / scale)), saturating).  V and the recorded positions
+ * like a write (e4m3(v * fp32(1 / scale)), saturating); FP4 pages likewise,
+ * with new block scales.  V and the recorded positions
  * are not changed: a caller reusing KV computed at other positions stores it
  * at its new positions and calls this with delta = new - old.  Rows outside
  * [pos_lo, pos_hi), rows a policy does not store, and other heads are left
