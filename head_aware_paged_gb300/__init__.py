@@ -65,14 +65,15 @@ class Policy:
     idx: Optional[Sequence[int]] = None
 
 
-def _stream(stream=None) -> c_void_p:
+def _stream(stream=None) -> int:
+    """The CUDA stream handle (torch's current stream by default)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ptr(t: Optional[torch.Tensor]) -> c_void_p:
-    return c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 # ---------------------------------------------------------------- C-ABI names
@@ -354,6 +355,7 @@ class SegPagedCache:
         self._pool_raw, self.pool = self._aligned(pool_b, device)
         self._meta_raw, self.meta = self._aligned(meta_b, device)
         self._ws_raw, self.ws = self._aligned(ws_b, device)
+        self._halves = None          # K and V views of the pool
         self.handle = sp_cache_create(cfg, self.pool, self.meta, self.ws)
 
     @staticmethod
@@ -375,13 +377,16 @@ class SegPagedCache:
 
     # views of the page pool: [num_pages, page_size, head_dim] bf16 each
     def _half_pool(self, i: int) -> torch.Tensor:
-        c = self.cfg
-        if c.kv_dtype == KV_FP4:
-            half = c.num_pages * (c.page_size // 16) * 1152
-            return self.pool[i * half:(i + 1) * half].view(c.num_pages, c.page_size // 16, 1152)
-        half = c.num_pages * c.page_size * c.head_dim
-        dt = torch.uint8 if c.kv_dtype == KV_FP8 else torch.bfloat16
-        return self.pool.view(dt)[i * half:(i + 1) * half].view(c.num_pages, c.page_size, c.head_dim)
+        if self._halves is None:
+            c = self.cfg
+            if c.kv_dtype == KV_FP4:
+                shape, pool = (c.num_pages, c.page_size // 16, 1152), self.pool
+            else:
+                shape = (c.num_pages, c.page_size, c.head_dim)
+                pool = self.pool.view(torch.uint8 if c.kv_dtype == KV_FP8 else torch.bfloat16)
+            n = shape[0] * shape[1] * shape[2]
+            self._halves = pool[:n].view(shape), pool[n:2 * n].view(shape)
+        return self._halves[i]
 
     def k_pool(self) -> torch.Tensor:
         """K pages [num_pages][page_size][head_dim]: bf16, or uint8 e4m3 codes;
@@ -415,18 +420,22 @@ class SegPagedCache:
         q (or None), k, v [rows, heads, head_dim] bf16, rows any stride apart
         (views of one fused projection).  Returns the rotated queries."""
         c = self.cfg
-        for x, heads in ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
-            assert x is None or (x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 3
-                                 and x.shape[1:] == (heads, c.head_dim) and x.shape[0] >= cu_new[-1]
-                                 and x.stride(2) == 1 and x.stride(1) == c.head_dim), \
+        for x, heads in ((k, c.num_kv_heads), (v, c.num_kv_heads)) if q is None else \
+                ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
+            n, h, d = x.shape
+            assert x.dtype is torch.bfloat16 and x.is_cuda and h == heads and d == c.head_dim and \
+                n >= cu_new[-1] and x.stride()[1:] == (d, 1), \
                 "q, k, v: bf16 [rows, heads, head_dim] on the device, heads contiguous"
         assert len(cu_new) == len(seq_ids) + 1 and (pos is None or len(pos) == len(seq_ids))
         assert inv_freq is None or len(inv_freq) == c.head_dim // 2
-        if q is not None and q_out is None:
+        if q is None:
+            q_out = None
+        elif q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        assert q is None or (q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype == q.dtype)
-        sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out if q is not None else None,
-                          pos, rope_theta, inv_freq, stream)
+        else:
+            assert q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype is q.dtype
+        sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out, pos, rope_theta, inv_freq,
+                          stream)
         return q_out
 
     def prefill(self, layer: int, seq_ids, cu_q, q, k, v, out=None, lse=None, want_lse=True,

@@ -4,6 +4,7 @@ library's CUDA kernels).  No fallback: if the library is missing, loading
 raises."""
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_double, c_int32, c_int64, c_size_t, c_void_p
@@ -114,11 +115,22 @@ def check(status: int) -> None:
         raise SegPagedError(status, msg)
 
 
+def _host_array(ctype, code, values):
+    # one pass in C for sequences of integers; anything else (floats with
+    # integer values, numbers that wrap) one by one
+    try:
+        buf = array.array(code, values)
+    except (TypeError, OverflowError):
+        values = [int(x) for x in values]
+        return (ctype * max(1, len(values)))(*values)
+    if not buf:
+        buf.append(0)
+    return (ctype * len(buf)).from_buffer(buf)
+
+
 def i32_array(values):
-    values = [int(x) for x in values]
-    return (c_int32 * max(1, len(values)))(*values)
+    return _host_array(c_int32, "i", values)
 
 
 def i64_array(values):
-    values = [int(x) for x in values]
-    return (c_int64 * max(1, len(values)))(*values)
+    return _host_array(c_int64, "q", values)

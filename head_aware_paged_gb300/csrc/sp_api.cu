@@ -301,6 +301,7 @@ sp_status fail(sp_status s, const std::string& msg) {
 
 sp_status cuda_fail(cudaError_t e, const char* what) {
     g_last_error = std::string(what) + ": " + cudaGetErrorString(e);
+    cudaGetLastError();      // a refused launch or attribute must not fail the next call's check
     return SP_ERR_CUDA;
 }
 

@@ -1,21 +1,26 @@
 // sp_decode4.cuh -- split-KV decode over 4-bit pages (format: sp_fp4.cuh).
 //
-// The same stream as k_decode (sp_decode.cuh): all visible slots of the call
-// are one list of work items, split evenly over a persistent grid; a producer
-// warp copies them into a ring of shared-memory stages, consumer warps own the
-// stages round robin, and a unit spread over several CTAs is merged by the
-// last of them.  What 4 bits change:
+// All visible slots of the call are one list of work items, split evenly over
+// a persistent grid, and a unit spread over several CTAs is merged by the last
+// of them, as in k_decode (sp_decode.cuh).  What 4 bits change:
 //
-//   * An item is a run of 64 slots of a unit whatever the page size, two
-//     stages of 32; a stage is one or two groups of 16 slots, each a 1152-byte
-//     bulk copy of K and one of V, and groups that no query sees are not read.
-//   * 144 bytes a key instead of 512, so the arithmetic decides.  Keys are the
-//     M side of the matrix instructions and the query heads the N side (8 of
-//     them, or 16 in two steps), so no row is padding:
+//   * 144 bytes a key instead of 512, so arithmetic and latency decide.  Keys
+//     are the M side of the matrix instructions and the query heads the N side
+//     (8 of them, or 16 in two steps), so no row is padding:
 //         S^T = K Q^T      16 keys x 8 heads, 8 steps of 16 dimensions
 //         O^T = V^T P^T    16 dimensions x 8 heads, 8 tiles, K = 16 keys
 //     P^T goes from the accumulator to the operand layout by two 8 x 8
 //     register transposes (movmatrix).
+//   * An item is a run of 64 slots of a unit whatever the page size (four groups
+//     of 16; a group that no query sees is loaded too, or a neighbour in its
+//     place).
+//   * There is no producer and no barrier in the stream: each warp takes a run
+//     of neighbouring items (mostly of one unit), owns one stage and refills
+//     its K half as soon as the scores are taken and its V half after the
+//     products.  The lanes look up the pages of the warp's next 32 items at once
+//     and hand them out by shuffle.  A unit that lies inside a warp's run is
+//     finished by that warp; a run's first and last units leave a partial (o, m,
+//     l) in shared memory, merged once when the CTA's warps are done.
 //   * Codes become f16 by the hardware's conversion, one instruction per two,
 //     and times their block's scale exactly (6 significant bits); a lane's
 //     codes of a K fragment lie in two blocks and of a V fragment in one, so
@@ -34,13 +39,21 @@ namespace sp {
 
 namespace {
 
-constexpr int kD4Warps = 8;                          // consumer warps
-constexpr int kD4Threads = (kD4Warps + 1) * 32;
-constexpr int kD4StageKeys = 32;
-constexpr int kD4Sub = kFp4ItemSlots / kD4StageKeys; // stages per item
-constexpr int kD4TileBytes = kD4StageKeys * kFp4RowBytes;
+constexpr int kD4Warps = 8;
+constexpr int kD4Threads = kD4Warps * 32;
+constexpr int kD4Depth = 1;                          // stages of a warp
+constexpr int kD4Stages = kD4Warps * kD4Depth;
+constexpr int kD4TileBytes = kFp4ItemSlots * kFp4RowBytes;
 constexpr int kD4StageBytes = 2 * kD4TileBytes;      // K, then V
 constexpr int kD4Dim = 128;
+constexpr float kLazyLog2 = 8.f;
+// A partial's head in shared memory: dimension 16 gl + 2 mt + i at 16 mt + 2 gl +
+// i, heads 132 floats apart (a half warp's 8-byte stores then meet no bank twice).
+constexpr int kD4HeadFloats = 132;
+__device__ __forceinline__ int d4_dim(int at) { return ((at >> 1) & 7) * 16 + (at >> 4) * 2 + (at & 1); }
+static_assert(16 * kD4HeadFloats * 4 <= kD4Depth * kD4StageBytes, "16 heads fit a warp's stages");
+constexpr int kD4Groups = kFp4ItemSlots / kFp4Group;
+static_assert(kD4Groups == 4, "an item is four groups of 16 slots");
 
 // Transpose of an 8x8 f16 matrix held as one pair a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -54,136 +67,104 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// NH: 8-head steps (group <= 8 * NH).  Two CTAs of 9 warps share an SM at
-// NH = 1 (at most 112 registers a thread); NH = 2 holds twice the output and
+// A work item: its groups' places in the pool (in groups), and its visible
+// slots [lo, hi) as lo | hi << 8.
+struct Item4 { uint32_t g[kD4Groups], visible; };
+
+// Item j of unit u (positions and slots are below 2^31).
+__device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_t j) {
+    const Geo& g = p.geo;
+    const uint32_t P = (uint32_t)g.page, lp = 31 - __clz(P);
+    const int b = u / g.hkv, h = u - b * g.hkv;
+    const int seq = p.seq[b];
+    const int32_t t = p.tq[b];
+    const int64_t row = g.unit_row(seq, p.layer, h);
+    const UnitPol pol = p.meta.pol[row];
+    // the visible ranges of decode_ranges (sp_rules.h), in 32 bits
+    int32_t lo[3] = {0, 0, 0}, hi[3] = {0, 0, 0};
+    if (pol.kind == kGlobal) {
+        hi[0] = t + 1;
+    } else if (pol.kind == kLocal) {
+        const int32_t sink_end = min(pol.sink, t + 1);
+        hi[0] = sink_end;
+        const int32_t w0 = max(max(t - pol.window + 1, 0), sink_end);
+        if (w0 <= t) {
+            const int32_t base = pol.sink_pages << lp, ring = pol.ring << lp, len = t - w0 + 1;
+            const int32_t q0 = (int32_t)((uint32_t)(w0 - pol.sink) % (uint32_t)ring);
+            lo[1] = base + q0;
+            hi[1] = base + min(q0 + len, ring);
+            lo[2] = base;
+            hi[2] = base + max(q0 + len - ring, 0);
+        }
+    } else {
+        const int32_t* idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off;
+        hi[0] = (int32_t)count_below(idx, pol.n_idx, (int64_t)t + 1);
+    }
+    int32_t w = 0, l = 0, e = 1;                      // window, visible slots [l, e) in it
+    #pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        if (hi[q] <= lo[q]) continue;
+        const int32_t first = lo[q] / kFp4ItemSlots, n = (hi[q] - 1) / kFp4ItemSlots - first + 1;
+        if (j >= 0 && j < n) {
+            w = (first + j) * kFp4ItemSlots;
+            l = max(lo[q] - w, 0);
+            e = min(hi[q] - w, kFp4ItemSlots);
+        }
+        j -= n;
+    }
+    // a group without a visible slot may have no page: its nearest neighbour
+    // that has one is read in its place
+    Item4 it;
+    it.visible = (uint32_t)l | ((uint32_t)e << 8);
+    const int32_t* tab = p.meta.ptab + row * g.max_pages_unit;
+    #pragma unroll
+    for (int k = 0; k < kD4Groups; ++k) {
+        if (P >= kFp4ItemSlots && k > 0) { it.g[k] = it.g[0] + k; continue; }   // one page holds the item
+        const int near = P >= kFp4ItemSlots ? 0 : min(max(k, l >> 4), (e - 1) >> 4);
+        const uint32_t slot = (uint32_t)w + 16 * near;
+        const int32_t page = tab[slot >> lp];
+        it.g[k] = 0;                                  // a bad page: load something harmless
+        if (page < 0 || page >= g.num_pages) atomicOr(p.meta.status, kStatusBadPage);
+        else it.g[k] = (((uint32_t)page << lp) + (slot & (P - 1))) >> 4;
+    }
+    return it;
+}
+
+// NH: 8-head steps (group <= 8 * NH).  Two CTAs of 8 warps share an SM at
+// NH = 1 (at most 128 registers a thread); NH = 2 holds twice the output and
 // runs one.
 template <int NH, bool CAP>
 __global__ void __launch_bounds__(kD4Threads, NH == 1 ? 2 : 1)
 k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kpool,
           const uint8_t* __restrict__ vpool) {
     constexpr int D = kD4Dim;
-    const int NST = p.nst;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* stages = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    float* merge_o = reinterpret_cast<float*>(stages + NST * kD4StageBytes);   // [warps][group][D]
-    float* merge_ml = merge_o + p.merge_floats;                               // [warps][group][2]
-    uint64_t* full = reinterpret_cast<uint64_t*>(
-        (reinterpret_cast<uintptr_t>(merge_ml + kD4Warps * p.geo.group * 2) + 15) & ~uintptr_t(15));
-    uint64_t* empty = full + NST;
-    int2* desc = reinterpret_cast<int2*>(empty + NST);          // {unit, lo | hi << 16} of a stage
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(desc + NST);
-    int* flag_last = const_cast<int*>(abort_flag) + 1;
-    int4* batch = reinterpret_cast<int4*>(const_cast<int*>(abort_flag) + 4);  // [32][2] producer batch
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t* stages = smem_raw;
+    // A warp's first and last partials are entries 2 w and 2 w + 1: (m, l) and
+    // unit here, outputs in its slot and in its stages.
+    float* slots = reinterpret_cast<float*>(stages + kD4Stages * kD4StageBytes);     // [warps][group][kD4HeadFloats]
+    float2* entry_ml = reinterpret_cast<float2*>(slots + p.merge_floats);           // [2 warps][group]
+    __shared__ uint64_t full[2 * kD4Stages];         // K and V of each stage landed
+    __shared__ int abort_word, flag_last[2], entry_unit[2 * kD4Warps];
+    volatile int* abort_flag = &abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, c = blockIdx.x;
     const int64_t T = p.total_items;
     const int64_t x0 = T * c / G, x1 = T * (c + 1) / G;
     const Geo& g = p.geo;
-    const int group = g.group, P = g.page;
+    const int group = g.group;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NST; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        *abort_flag = 0;
+        for (int s = 0; s < 2 * kD4Stages; ++s) mbar_init(&full[s], 1);
+        for (int e = 0; e < 2 * kD4Warps; ++e) entry_unit[e] = -1;
+        abort_word = 0;
         fence_mbar_init();
     }
     __syncthreads();
 
-    if (warp == kD4Warps) {
-        // ---------------- producer: stream this CTA's items ----------------
-        if (x0 < x1) {
-            int issued = 0, ps = 0;
-            uint32_t pk = 0;
-            bool stop = false;
-            for (int64_t base = x0; base < x1 && !stop; base += 32) {
-                const int64_t x = base + lane;
-                if (x < x1) {
-                    int lo_u = 0, hi_u = p.n_units - 1;      // unit holding item x
-                    while (lo_u < hi_u) {
-                        const int mid = (lo_u + hi_u) >> 1;
-                        if (p.item_off[mid + 1] <= x) lo_u = mid + 1; else hi_u = mid;
-                    }
-                    const int u = lo_u;
-                    const int b = u / g.hkv, h = u % g.hkv;
-                    const int seq = p.seq[b];
-                    const int64_t row = g.unit_row(seq, p.layer, h);
-                    const UnitPol pol = p.meta.pol[row];
-                    const int32_t* idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off;
-                    const SlotRanges rg = decode_ranges(pol, idx, p.tq[b], P);
-                    int64_t j = x - p.item_off[u];
-                    int64_t w = 0, lo = 0, hi = 0;           // 64-slot window, visible slots in it
-                    for (int q = 0; q < rg.count; ++q) {
-                        const int64_t np = range_pages(rg.lo[q], rg.hi[q], kFp4ItemSlots);
-                        if (j < np) {
-                            w = rg.lo[q] / kFp4ItemSlots + j;
-                            lo = max64(rg.lo[q], w * kFp4ItemSlots) - w * kFp4ItemSlots;
-                            hi = min64(rg.hi[q], (w + 1) * kFp4ItemSlots) - w * kFp4ItemSlots;
-                            break;
-                        }
-                        j -= np;
-                    }
-                    // first group row (in groups of the pool) of each group of 16 slots
-                    int32_t gr[4];
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        gr[q] = 0;
-                        if (16 * q + 16 <= lo || 16 * q >= hi) continue;
-                        const int64_t slot = w * kFp4ItemSlots + 16 * q;
-                        const int32_t page = p.meta.ptab[row * g.max_pages_unit + slot / P];
-                        if (page < 0 || page >= g.num_pages) {
-                            atomicOr(p.meta.status, kStatusBadPage);
-                            continue;                        // load something harmless
-                        }
-                        gr[q] = (int32_t)(((int64_t)page * P + slot % P) >> 4);
-                    }
-                    batch[2 * lane] = make_int4(u, (int)lo | ((int)hi << 16), 0, 0);
-                    batch[2 * lane + 1] = make_int4(gr[0], gr[1], gr[2], gr[3]);
-                }
-                __syncwarp();
-                const int n = (int)min64(32, x1 - base);
-                for (int i = 0; i < n && !stop; ++i) {
-                    const int4 bi = batch[2 * i];
-                    const int lo = bi.y & 0xFFFF, hi = bi.y >> 16;
-                    #pragma unroll
-                    for (int sub = 0; sub < kD4Sub; ++sub) {
-                        if (stop) break;
-                        const bool ok = pk == 0 || mbar_wait(&empty[ps], (pk - 1) & 1, abort_flag, p.meta.status);
-                        if (__any_sync(0xffffffffu, !ok)) { stop = true; break; }
-                        const int k0 = sub * kD4StageKeys;
-                        const int slo = max(lo - k0, 0), shi = min(hi - k0, kD4StageKeys);
-                        const int g0 = slo >> 4, ng = slo < shi ? ((shi + 15) >> 4) - g0 : 0;
-                        if (lane == 0) {
-                            desc[ps] = make_int2(bi.x, slo < shi ? slo | (shi << 16) : 0);
-                            if (ng > 0) mbar_arrive_expect_tx(&full[ps], 2 * ng * kFp4GroupBytes);
-                            else mbar_arrive(&full[ps]);
-                        }
-                        __syncwarp();
-                        // lanes 0..3: (group, K or V) of the stage
-                        const int q = lane & 1, kv = lane >> 1;
-                        if (lane < 4 && q >= g0 && q < g0 + ng) {
-                            const int32_t gr = reinterpret_cast<const int32_t*>(&batch[2 * i + 1])[2 * sub + q];
-                            bulk_load(stages + ps * kD4StageBytes + kv * kD4TileBytes + q * kFp4GroupBytes,
-                                      (kv ? vpool : kpool) + (int64_t)gr * kFp4GroupBytes, kFp4GroupBytes,
-                                      &full[ps]);
-                        }
-                        ++issued;
-                        if (++ps == NST) { ps = 0; ++pk; }
-                    }
-                }
-                __syncwarp();
-            }
-            // leave only after every load this CTA issued has landed (bounded)
-            if (lane == 0)
-                for (int s = 0; s < NST && s < issued; ++s)
-                    mbar_wait(&full[s], (uint32_t)(((issued - 1 - s) / NST) & 1), nullptr, nullptr);
-        }
-        return;
-    }
-
-    // ------------------------------ consumers ------------------------------
     const int ctid = threadIdx.x;
-    constexpr int CT = kD4Warps * 32;
+    constexpr int CT = kD4Threads;
     // Units with no visible token: O = 0, LSE = -inf (one CTA each).
     for (int u = c; u < p.n_units; u += G) {
         if (p.item_off[u + 1] != p.item_off[u]) continue;
@@ -196,22 +177,75 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
     }
     if (x0 >= x1) return;
 
+    // This warp's items [wx0, wx1) of the CTA's.  The lanes hold 32 of them,
+    // [batch, batch + 32).
+    const int32_t wx0 = (int32_t)(x0 + (x1 - x0) * warp / kD4Warps);
+    const int32_t wx1 = (int32_t)(x0 + (x1 - x0) * (warp + 1) / kD4Warps);
+    const int mine = wx1 - wx0;
+    uint8_t* my_stages = stages + warp * kD4Depth * kD4StageBytes;
+    uint64_t* my_full = full + warp * kD4Depth * 2;
+    int u_first = 0;                                 // first unit with an item >= wx0
+    for (int u_hi = p.n_units - 1; u_first < u_hi;) {
+        const int mid = (u_first + u_hi) >> 1;
+        if (p.item_off[mid + 1] <= wx0) u_first = mid + 1; else u_hi = mid;
+    }
+    Item4 held{}, next{};
+    int batch = -32, u_batch = u_first;
+    uint32_t visible = 0;                            // slots of the item in the stage
+    const bool one_page = g.page >= kFp4ItemSlots;
+    int issued[2] = {0, 0};                          // K and V loads
+    // take(i): item i's description into `next`
+    auto take = [&](int i) {
+        if (i >= batch + 32) {
+            // the units of 32 items: walk their ends together (each end is one
+            // uniform load), every lane stepping over those before its item
+            batch += 32;
+            const int32_t x = wx0 + batch + lane, last = min(wx0 + batch + 31, wx1 - 1);
+            int u = u_batch;
+            int32_t start = p.item_off[u_batch];
+            for (; u_batch + 1 < p.n_units; ++u_batch) {
+                const int32_t end = p.item_off[u_batch + 1];
+                if (end > last) break;
+                if (end <= x) { u = u_batch + 1; start = end; }
+            }
+            if (batch + lane < mine) held = find_item4(p, u, x - start);
+        }
+        next.visible = __shfl_sync(0xffffffffu, held.visible, i - batch);
+        next.g[0] = __shfl_sync(0xffffffffu, held.g[0], i - batch);
+        if (!one_page) {
+            #pragma unroll
+            for (int k = 1; k < kD4Groups; ++k) next.g[k] = __shfl_sync(0xffffffffu, held.g[k], i - batch);
+        }
+    };
+    // lane 0: K (kv = 0) or V of the taken item into the stage
+    auto load = [&](int kv) {
+        ++issued[kv];
+        if (lane != 0) return;
+        uint64_t* bar = &my_full[kv];
+        uint8_t* dst = my_stages + kv * kD4TileBytes;
+        const uint8_t* pool = kv ? vpool : kpool;
+        mbar_arrive_expect_tx(bar, kD4TileBytes);
+        if (one_page) {
+            bulk_load(dst, pool + (int64_t)next.g[0] * kFp4GroupBytes, kD4TileBytes, bar);
+            return;
+        }
+        #pragma unroll
+        for (int k = 0; k < kD4Groups; ++k)
+            bulk_load(dst + k * kFp4GroupBytes, pool + (int64_t)next.g[k] * kFp4GroupBytes, kFp4GroupBytes, bar);
+    };
+    if (mine > 0) { take(0); load(0); load(1); }
+
     const int gl = lane >> 2, j = lane & 3;          // fragment row, column pair
     // slots of this lane's rows of S^T in a group (positions gl and gl + 8)
     const int slot_a = (gl >> 1) + 4 * (gl & 1), slot_b = slot_a + 8;
     uint32_t qb[NH][8][2];
     float m_run[NH][2], l_run[NH][2], o[NH][8][4];
-    int xi = warp, s = warp;                         // next stage fill of this warp, its stage
-    uint32_t rounds = 0;
+    int it = 0;                                      // next item of this warp
     bool dead = false;
-    int u_lo = 0, u_hi = p.n_units - 1;              // first unit with an item >= x0
-    while (u_lo < u_hi) {
-        const int mid = (u_lo + u_hi) >> 1;
-        if (p.item_off[mid + 1] <= x0) u_lo = mid + 1; else u_hi = mid;
-    }
-    for (int u = u_lo; u < p.n_units && p.item_off[u] < x1; ++u) {
-        const int64_t ua = max64(p.item_off[u], x0), ub = min64(p.item_off[u + 1], x1);
-        if (ua >= ub) continue;
+    for (int u = u_first; it < mine; ++u) {
+        const int32_t u_begin = p.item_off[u], u_end = p.item_off[u + 1];
+        if (u_end <= wx0 + it) continue;             // no items, or before this run
+        const int stop = min(mine, u_end - wx0);
         const int b = u / g.hkv, h = u - b * g.hkv;
         const float* ks = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
         const float* vs = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
@@ -237,148 +271,171 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nh][mt][e] = 0.f;
         }
-        for (; x0 * kD4Sub + xi < ub * kD4Sub; xi += kD4Warps) {
-            if (!dead && !mbar_wait(&full[s], rounds & 1, abort_flag, p.meta.status)) dead = true;
+        for (; it < stop; ++it) {
             if (dead) continue;
-            const int2 dd = desc[s];
-            const int lo = dd.y & 0xFFFF, hi = dd.y >> 16;
-            if (dd.x != u && lane == 0) atomicOr(p.meta.status, kStatusBadState);
-            const uint8_t* tk = stages + s * kD4StageBytes;
+            const uint32_t parity = it & 1;
+            dead = __any_sync(0xffffffffu, !mbar_wait(&my_full[0], parity, abort_flag, p.meta.status));
+            if (dead) continue;
+            visible = next.visible;
+            const int lo = visible & 0xFF, hi = visible >> 8;
+            const uint8_t* tk = my_stages;
             const uint8_t* tv = tk + kD4TileBytes;
-            if (lo < hi) {
-                float sc[2][NH][4];                  // [group][heads][accumulator]
-                float mx[NH][2];
+            float sc[kD4Groups][NH][4];              // [group][heads][accumulator]
+            #pragma unroll
+            for (int q = 0; q < kD4Groups; ++q) {
                 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh) mx[nh][0] = mx[nh][1] = -INFINITY;
-                #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int nh = 0; nh < NH; ++nh)
                     #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh)
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[q][nh][e] = 0.f;
-                    if (16 * q + 16 <= lo || 16 * q >= hi) {
+                    for (int e = 0; e < 4; ++e) sc[q][nh][e] = 0.f;
+                const uint8_t* gk = tk + q * kFp4GroupBytes;
+                const uint4 ca = *reinterpret_cast<const uint4*>(gk + gl * 64 + j * 16);
+                const uint4 cb = *reinterpret_cast<const uint4*>(gk + (gl + 8) * 64 + j * 16);
+                const uint32_t sw = *reinterpret_cast<const uint32_t*>(gk + kFp4ScaleOff + (gl * 4 + j) * 4);
+                const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+                #pragma unroll
+                for (int w = 0; w < 4; ++w) {        // 8 dimensions: two steps
+                    // this block's scale of both rows, twice in a word, as f16
+                    const uint32_t fa = prmt(sw, 0u, (w >> 1) ? 0x4141u : 0x4040u) << 7;
+                    const uint32_t fb = prmt(sw, 0u, (w >> 1) ? 0x4343u : 0x4242u) << 7;
+                    uint32_t a[4], bb[4];
+                    fp4_word_f16(wa[w], a[0], a[1], a[2], a[3]);
+                    fp4_word_f16(wb[w], bb[0], bb[1], bb[2], bb[3]);
+                    #pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t af[4] = {hmul2(a[2 * e], fa), hmul2(bb[2 * e], fb),
+                                                hmul2(a[2 * e + 1], fa), hmul2(bb[2 * e + 1], fb)};
                         #pragma unroll
                         for (int nh = 0; nh < NH; ++nh)
-                            #pragma unroll
-                            for (int e = 0; e < 4; ++e) sc[q][nh][e] = -INFINITY;
-                        continue;
+                            mma_f16_16816(sc[q][nh], af, qb[nh][2 * w + e][0], qb[nh][2 * w + e][1]);
                     }
-                    const uint8_t* gk = tk + q * kFp4GroupBytes;
-                    const uint4 ca = *reinterpret_cast<const uint4*>(gk + gl * 64 + j * 16);
-                    const uint4 cb = *reinterpret_cast<const uint4*>(gk + (gl + 8) * 64 + j * 16);
-                    const uint32_t sw = *reinterpret_cast<const uint32_t*>(gk + kFp4ScaleOff + (gl * 4 + j) * 4);
-                    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+                }
+            }
+            // K's half is read: refill it with the next item's
+            const bool more = it + 1 < mine;
+            __syncwarp();
+            if (more) { take(it + 1); load(0); }
+            #pragma unroll
+            for (int q = 0; q < kD4Groups; ++q)
+                #pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
                     #pragma unroll
-                    for (int w = 0; w < 4; ++w) {    // 8 dimensions: two steps
-                        // this block's scale of both rows, twice in a word, as f16
-                        const uint32_t fa = prmt(sw, 0u, (w >> 1) ? 0x4141u : 0x4040u) << 7;
-                        const uint32_t fb = prmt(sw, 0u, (w >> 1) ? 0x4343u : 0x4242u) << 7;
-                        uint32_t a[4], bb[4];
-                        fp4_word_f16(wa[w], a[0], a[1], a[2], a[3]);
-                        fp4_word_f16(wb[w], bb[0], bb[1], bb[2], bb[3]);
-                        #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t af[4] = {hmul2(a[2 * e], fa), hmul2(bb[2 * e], fb),
-                                                    hmul2(a[2 * e + 1], fa), hmul2(bb[2 * e + 1], fb)};
-                            #pragma unroll
-                            for (int nh = 0; nh < NH; ++nh)
-                                mma_f16_16816(sc[q][nh], af, qb[nh][2 * w + e][0], qb[nh][2 * w + e][1]);
-                        }
-                    }
-                    const bool cut = 16 * q < lo || 16 * q + 16 > hi;
-                    const bool in_a = !cut || (16 * q + slot_a >= lo && 16 * q + slot_a < hi);
-                    const bool in_b = !cut || (16 * q + slot_b >= lo && 16 * q + slot_b < hi);
+                    for (int e = 0; e < 4; ++e)
+                        sc[q][nh][e] = CAP ? capped_log2(sc[q][nh][e], p.cap) : sc[q][nh][e] * p.scale_log2;
+            if (lo > 0 || hi < kFp4ItemSlots) {
+                #pragma unroll
+                for (int q = 0; q < kD4Groups; ++q) {
+                    const bool in_a = 16 * q + slot_a >= lo && 16 * q + slot_a < hi;
+                    const bool in_b = 16 * q + slot_b >= lo && 16 * q + slot_b < hi;
                     #pragma unroll
                     for (int nh = 0; nh < NH; ++nh)
                         #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = CAP ? capped_log2(sc[q][nh][e], p.cap) : sc[q][nh][e] * p.scale_log2;
-                            if (!(e < 2 ? in_a : in_b)) v = -INFINITY;
-                            sc[q][nh][e] = v;
-                            mx[nh][e & 1] = fmaxf(mx[nh][e & 1], v);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (!(e < 2 ? in_a : in_b)) sc[q][nh][e] = -INFINITY;
                 }
-                bool grew = false;
+            }
+            // Running maximum, raised only when a score passes it by 2^8 (or the
+            // unit has none yet): below that P stays inside f16 and the sums
+            // inside fp32, and a warp agrees by one vote instead of exchanging
+            // its rows' maxima for every item.
+            float mx[NH][2];
+            bool grew = false;
+            #pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+                #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[nh][e] = fmaxf(sc[0][nh][e], sc[0][nh][2 + e]);
+                    #pragma unroll
+                    for (int q = 1; q < kD4Groups; ++q)
+                        mx[nh][e] = fmaxf(mx[nh][e], fmaxf(sc[q][nh][e], sc[q][nh][2 + e]));
+                    grew = grew || mx[nh][e] > m_run[nh][e] + kLazyLog2;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
                 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh)
                     #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        mx[nh][e] = fmaxf(mx[nh][e], __shfl_xor_sync(0xffffffffu, mx[nh][e], 4));
-                        mx[nh][e] = fmaxf(mx[nh][e], __shfl_xor_sync(0xffffffffu, mx[nh][e], 8));
-                        mx[nh][e] = fmaxf(mx[nh][e], __shfl_xor_sync(0xffffffffu, mx[nh][e], 16));
-                        grew = grew || mx[nh][e] > m_run[nh][e];
-                    }
-                if (__any_sync(0xffffffffu, grew)) {
-                    #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh)
+                        float x = mx[nh][e];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        const float m_new = fmaxf(m_run[nh][e], x);
+                        const float alpha = fast_exp2(m_run[nh][e] - (m_new == -INFINITY ? 0.f : m_new));
+                        m_run[nh][e] = m_new;
+                        l_run[nh][e] *= alpha;
                         #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float m_new = fmaxf(m_run[nh][e], mx[nh][e]);
-                            const float alpha = fast_exp2(m_run[nh][e] - (m_new == -INFINITY ? 0.f : m_new));
-                            m_run[nh][e] = m_new;
-                            l_run[nh][e] *= alpha;
-                            #pragma unroll
-                            for (int mt = 0; mt < 8; ++mt) {
-                                o[nh][mt][e] *= alpha;
-                                o[nh][mt][2 + e] *= alpha;
-                            }
+                        for (int mt = 0; mt < 8; ++mt) {
+                            o[nh][mt][e] *= alpha;
+                            o[nh][mt][2 + e] *= alpha;
                         }
-                }
+                    }
+            }
+            uint32_t pb[kD4Groups][NH][2];
+            #pragma unroll
+            for (int q = 0; q < kD4Groups; ++q)
                 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (16 * q + 16 <= lo || 16 * q >= hi) continue;
-                    uint32_t pb[NH][2];
+                for (int nh = 0; nh < NH; ++nh) {
+                    float pv[4];
                     #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh) {
-                        float pv[4];
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float mb = m_run[nh][e & 1] == -INFINITY ? 0.f : m_run[nh][e & 1];
-                            pv[e] = fast_exp2(sc[q][nh][e] - mb);
-                            l_run[nh][e & 1] += pv[e];
-                        }
-                        pb[nh][0] = transpose8x8(pack_f16(pv[0], pv[1]));
-                        pb[nh][1] = transpose8x8(pack_f16(pv[2], pv[3]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float mb = m_run[nh][e & 1] == -INFINITY ? 0.f : m_run[nh][e & 1];
+                        pv[e] = fast_exp2(sc[q][nh][e] - mb);
+                        l_run[nh][e & 1] += pv[e];
                     }
-                    // V: the codes of block gl of slots j, j+4, j+8, j+12
-                    const uint8_t* gv = tv + q * kFp4GroupBytes;
-                    const int unit = (gl ^ ((j & 2) << 1)) * 8;
-                    uint2 cv[4];
+                    pb[q][nh][0] = transpose8x8(pack_f16(pv[0], pv[1]));
+                    pb[q][nh][1] = transpose8x8(pack_f16(pv[2], pv[3]));
+                }
+            dead = __any_sync(0xffffffffu, !mbar_wait(&my_full[1], parity, abort_flag, p.meta.status));
+            if (dead) continue;
+            #pragma unroll
+            for (int q = 0; q < kD4Groups; ++q) {
+                // V: the codes of block gl of slots j, j+4, j+8, j+12
+                const uint8_t* gv = tv + q * kFp4GroupBytes;
+                const int unit = (gl ^ ((j & 2) << 1)) * 8;
+                uint2 cv[4];
+                #pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    cv[t] = *reinterpret_cast<const uint2*>(gv + (j + 4 * t) * 64 + unit);
+                const uint32_t sw = *reinterpret_cast<const uint32_t*>(gv + kFp4ScaleOff + gl * 16 + j * 4);
+                const uint32_t f0 = prmt(sw, 0u, 0x4140u) << 7, f1 = prmt(sw, 0u, 0x4342u) << 7;
+                #pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t v0 = w ? cv[0].y : cv[0].x, v1 = w ? cv[1].y : cv[1].x;
+                    const uint32_t v2 = w ? cv[2].y : cv[2].x, v3 = w ? cv[3].y : cv[3].x;
+                    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                    // bytes (first key low, second key high) of dimensions 0,2,4,6 and 1,3,5,7
+                    const uint32_t e0 = (v0 & kLow) | ((v1 << 4) & ~kLow), d0 = ((v0 >> 4) & kLow) | (v1 & ~kLow);
+                    const uint32_t e1 = (v2 & kLow) | ((v3 << 4) & ~kLow), d1 = ((v2 >> 4) & kLow) | (v3 & ~kLow);
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    fp4_word_f16(e0, a0[0], a0[1], a0[2], a0[3]);
+                    fp4_word_f16(d0, a1[0], a1[1], a1[2], a1[3]);
+                    fp4_word_f16(e1, a2[0], a2[1], a2[2], a2[3]);
+                    fp4_word_f16(d1, a3[0], a3[1], a3[2], a3[3]);
                     #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        cv[t] = *reinterpret_cast<const uint2*>(gv + (j + 4 * t) * 64 + unit);
-                    const uint32_t sw = *reinterpret_cast<const uint32_t*>(gv + kFp4ScaleOff + gl * 16 + j * 4);
-                    const uint32_t f0 = prmt(sw, 0u, 0x4140u) << 7, f1 = prmt(sw, 0u, 0x4342u) << 7;
-                    #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t v0 = w ? cv[0].y : cv[0].x, v1 = w ? cv[1].y : cv[1].x;
-                        const uint32_t v2 = w ? cv[2].y : cv[2].x, v3 = w ? cv[3].y : cv[3].x;
-                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-                        // bytes (first key low, second key high) of dimensions 0,2,4,6 and 1,3,5,7
-                        const uint32_t e0 = (v0 & kLow) | ((v1 << 4) & ~kLow), d0 = ((v0 >> 4) & kLow) | (v1 & ~kLow);
-                        const uint32_t e1 = (v2 & kLow) | ((v3 << 4) & ~kLow), d1 = ((v2 >> 4) & kLow) | (v3 & ~kLow);
-                        uint32_t a0[4], a1[4], a2[4], a3[4];
-                        fp4_word_f16(e0, a0[0], a0[1], a0[2], a0[3]);
-                        fp4_word_f16(d0, a1[0], a1[1], a1[2], a1[3]);
-                        fp4_word_f16(e1, a2[0], a2[1], a2[2], a2[3]);
-                        fp4_word_f16(d1, a3[0], a3[1], a3[2], a3[3]);
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t af[4] = {hmul2(a0[t], f0), hmul2(a1[t], f0), hmul2(a2[t], f1), hmul2(a3[t], f1)};
                         #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t af[4] = {hmul2(a0[t], f0), hmul2(a1[t], f0), hmul2(a2[t], f1), hmul2(a3[t], f1)};
-                            #pragma unroll
-                            for (int nh = 0; nh < NH; ++nh)
-                                mma_f16_16816(o[nh][4 * w + t], af, pb[nh][0], pb[nh][1]);
-                        }
+                        for (int nh = 0; nh < NH; ++nh)
+                            mma_f16_16816(o[nh][4 * w + t], af, pb[q][nh][0], pb[q][nh][1]);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            s += kD4Warps;
-            if (s >= NST) { s -= NST; ++rounds; }
+            if (more) load(1);
         }
 
-        // ------------- merge the warps' partial states -------------
+        // after an abort: nothing may land in this warp's stages any more (bounded)
+        if (dead && lane == 0)
+            for (int kv = 0; kv < 2; ++kv)
+                mbar_wait(&my_full[kv], (issued[kv] - 1) & 1, nullptr, nullptr);
+        __syncwarp();
+
+        // The unit's sums of this run: the result itself if the run holds the
+        // whole unit, else a partial, in this warp's slot (the run goes on) or
+        // in its stages (it ends here, and nothing is in flight).
+        const bool complete = u_begin >= wx0 && u_end <= wx1;
+        const int entry = 2 * warp + (it < mine ? 0 : 1);
+        float* po = it < mine ? slots + warp * group * kD4HeadFloats : reinterpret_cast<float*>(my_stages);
+        if (!complete && lane == 0) entry_unit[entry] = u;
         #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
             #pragma unroll
@@ -388,140 +445,145 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int head = nh * 8 + 2 * j + e;
-                if (head < group) {
-                    float* mo = merge_o + ((size_t)warp * group + head) * D + gl * 16;
+                if (head >= group) continue;
+                if (complete) {
+                    const float inv = 1.f / l;
+                    const int64_t orow = (int64_t)b * g.hq + h * group + head;
+                    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + orow * D + gl * 16);
                     #pragma unroll
                     for (int mt = 0; mt < 8; ++mt)
-                        *reinterpret_cast<float2*>(mo + 2 * mt) =
+                        out[mt] = pack_bf16(o[nh][mt][e] * __ldg(vs + gl * 16 + 2 * mt) * inv,
+                                            o[nh][mt][2 + e] * __ldg(vs + gl * 16 + 2 * mt + 1) * inv);
+                    if (gl == 0 && p.lse) p.lse[orow] = (m_run[nh][e] + __log2f(l)) * 0.69314718055994531f;
+                } else {
+                    #pragma unroll
+                    for (int mt = 0; mt < 8; ++mt)
+                        *reinterpret_cast<float2*>(po + head * kD4HeadFloats + mt * 16 + gl * 2) =
                             make_float2(o[nh][mt][e] * __ldg(vs + gl * 16 + 2 * mt),
                                         o[nh][mt][2 + e] * __ldg(vs + gl * 16 + 2 * mt + 1));
-                    if (gl == 0) {
-                        merge_ml[(warp * group + head) * 2] = m_run[nh][e];
-                        merge_ml[(warp * group + head) * 2 + 1] = l;
-                    }
+                    if (gl == 0) entry_ml[entry * group + head] = make_float2(m_run[nh][e], l);
                 }
             }
-        asm volatile("bar.sync 1, %0;" ::"n"(CT));
+    }
+    __syncthreads();
 
-        const int64_t ia = p.item_off[u], ib = p.item_off[u + 1];
-        const int c_first = (int)cta_of_item(ia, T, G), c_last = (int)cta_of_item(ib - 1, T, G);
-        const bool whole = c_first == c_last;
-        const int64_t part = (int64_t)u + c;
+    // ------------- merge the partials of the CTA, unit by unit -------------
+    // Thread e holds output (head e / 128, place e % 128 of the slots' order).
+    int split_unit[2] = {-1, -1};                    // units that other CTAs share
+    for (int i = 0; i < 2 * kD4Warps;) {
+        const int u = entry_unit[i];
+        if (u < 0) { ++i; continue; }
+        int k = i + 1;
+        while (k < 2 * kD4Warps && (entry_unit[k] < 0 || entry_unit[k] == u)) ++k;
+        const int b = u / g.hkv, h = u - b * g.hkv;
+        const bool whole = p.item_off[u] >= x0 && p.item_off[u + 1] <= x1;
+        if (!whole) split_unit[split_unit[0] < 0 ? 0 : 1] = u;
         for (int e = ctid; e < group * D; e += CT) {
-            const int r = e / D, col = e % D;
+            const int r = e / D, at = e % D;
             float mst = -INFINITY;
-            #pragma unroll
-            for (int w = 0; w < kD4Warps; ++w) mst = fmaxf(mst, merge_ml[(w * group + r) * 2]);
+            for (int w = i; w < k; ++w)
+                if (entry_unit[w] == u) mst = fmaxf(mst, entry_ml[w * group + r].x);
             float lst = 0.f, ost = 0.f;
-            #pragma unroll
-            for (int w = 0; w < kD4Warps; ++w) {
-                const float sc_w = fast_exp2(merge_ml[(w * group + r) * 2] - mst);
-                lst += sc_w * merge_ml[(w * group + r) * 2 + 1];
-                ost += sc_w * merge_o[((size_t)w * group + r) * D + col];
+            for (int w = i; w < k; ++w) {
+                if (entry_unit[w] != u) continue;
+                const float2 ml = entry_ml[w * group + r];
+                const float* po = (w & 1) ? reinterpret_cast<const float*>(stages + (w >> 1) * kD4Depth * kD4StageBytes)
+                                          : slots + (w >> 1) * group * kD4HeadFloats;
+                const float f = fast_exp2(ml.x - (mst == -INFINITY ? 0.f : mst));
+                lst += f * ml.y;
+                ost += f * po[r * kD4HeadFloats + at];
             }
-            const int64_t orow = (int64_t)b * g.hq + h * group + r;
             if (whole) {
-                p.out[orow * D + col] = __float2bfloat16(ost / lst);
-                if (col == 0 && p.lse) p.lse[orow] = (mst + __log2f(lst)) * 0.69314718055994531f;
+                const int64_t orow = (int64_t)b * g.hq + h * group + r;
+                p.out[orow * D + d4_dim(at)] = __float2bfloat16(ost / lst);
+                if (at == 0 && p.lse) p.lse[orow] = (mst + __log2f(lst)) * 0.69314718055994531f;
             } else {
-                p.part_o[(part * group + r) * D + col] = ost;
-                if (col == 0) {
+                const int64_t part = (int64_t)u + c;
+                p.part_o[(part * group + r) * D + at] = ost;
+                if (at == 0) {
                     p.part_ml[(part * group + r) * 2] = mst;
                     p.part_ml[(part * group + r) * 2 + 1] = lst;
                 }
             }
         }
-        if (!whole) {
-            __threadfence();
-            asm volatile("bar.sync 1, %0;" ::"n"(CT));
-            if (ctid == 0) {
-                int target = 0;
-                for (int cc = c_first; cc <= c_last; ++cc)
-                    target += (T * cc / G) < (T * (cc + 1) / G) ? 1 : 0;
-                const int old = atomicAdd(&p.counters[u], 1);
-                *flag_last = (old == target - 1) ? 1 : 0;
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(CT));
-            if (*flag_last) {
-                // the last CTA of the unit: weights 2^(m - m*) of the parts, then
-                // the weighted sum of their outputs
-                __threadfence();
-                const int nseg = c_last - c_first + 1;
-                float* wts = merge_o;                          // [nseg][group] weights
-                float* mls = merge_o + p.merge_floats / 2;     // [nseg][group] l
-                float* mstar = merge_ml;                       // [group] m*, l*
-                for (int e = ctid; e < nseg * group; e += CT) {
-                    const int sg = e / group, r = e % group;
-                    const int cc = c_first + sg;
-                    const bool live = (T * cc / G) < (T * (cc + 1) / G);
-                    const int64_t pi = (int64_t)u + cc;
-                    wts[e] = live ? __ldcg(&p.part_ml[(pi * group + r) * 2]) : -INFINITY;
-                    mls[e] = live ? __ldcg(&p.part_ml[(pi * group + r) * 2 + 1]) : 0.f;
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(CT));
-                if (ctid < group) {
-                    const int r = ctid;
-                    float mst = -INFINITY;
-                    for (int sg = 0; sg < nseg; ++sg) mst = fmaxf(mst, wts[sg * group + r]);
-                    float lst = 0.f;
-                    for (int sg = 0; sg < nseg; ++sg) {
-                        const float w = fast_exp2(wts[sg * group + r] - mst);
-                        wts[sg * group + r] = w;
-                        lst += w * mls[sg * group + r];
-                    }
-                    mstar[2 * r] = mst;
-                    mstar[2 * r + 1] = lst;
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(CT));
-                for (int e = ctid; e < group * D; e += CT) {
-                    const int r = e / D, col = e % D;
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    int sg = 0;
-                    for (; sg + 4 <= nseg; sg += 4) {
-                        float v4[4];
-                        #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float w = wts[(sg + q) * group + r];
-                            const int64_t pi = (int64_t)u + c_first + sg + q;
-                            v4[q] = w != 0.f ? __ldcg(&p.part_o[(pi * group + r) * D + col]) * w : 0.f;
-                        }
-                        #pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[q] += v4[q];
-                    }
-                    for (; sg < nseg; ++sg) {
-                        const float w = wts[sg * group + r];
-                        const int64_t pi = (int64_t)u + c_first + sg;
-                        if (w != 0.f) acc[0] += w * __ldcg(&p.part_o[(pi * group + r) * D + col]);
-                    }
-                    const float ost = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                    const float lst = mstar[2 * r + 1];
-                    const int64_t orow = (int64_t)b * g.hq + h * group + r;
-                    p.out[orow * D + col] = __float2bfloat16(ost / lst);
-                    if (col == 0 && p.lse) p.lse[orow] = (mstar[2 * r] + __log2f(lst)) * 0.69314718055994531f;
-                }
-                if (ctid == 0) p.counters[u] = 0;
-            }
+        i = k;
+    }
+    if (split_unit[0] < 0) return;                    // the same for every thread
+    __threadfence();
+    __syncthreads();
+    if (ctid < 2 && split_unit[ctid] >= 0) {
+        // every CTA of the grid holds an item, so a unit's CTAs are c_first .. c_last
+        const int u = split_unit[ctid];
+        const int n = (int)cta_of_item(p.item_off[u + 1] - 1, T, G) - (int)cta_of_item(p.item_off[u], T, G) + 1;
+        flag_last[ctid] = atomicAdd(&p.counters[u], 1) == n - 1;
+    }
+    __syncthreads();
+    for (int q = 0; q < 2; ++q) {
+        if (split_unit[q] < 0 || !flag_last[q]) continue;
+        // the last CTA of the unit: weights 2^(m - m*) of the parts, then the
+        // weighted sum of their outputs
+        __threadfence();
+        const int u = split_unit[q];
+        const int b = u / g.hkv, h = u - b * g.hkv;
+        const int c_first = (int)cta_of_item(p.item_off[u], T, G);
+        const int nseg = (int)cta_of_item(p.item_off[u + 1] - 1, T, G) - c_first + 1;
+        float* wts = slots;                            // [nseg][group] weights
+        float* mls = slots + p.merge_floats / 2;       // [nseg][group] l
+        for (int e = ctid; e < nseg * group; e += CT) {
+            const int64_t pi = (int64_t)u + c_first + e / group;
+            wts[e] = __ldcg(&p.part_ml[(pi * group + e % group) * 2]);
+            mls[e] = __ldcg(&p.part_ml[(pi * group + e % group) * 2 + 1]);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(CT));
+        __syncthreads();
+        if (ctid < group) {
+            const int r = ctid;
+            float mst = -INFINITY;
+            for (int sg = 0; sg < nseg; ++sg) mst = fmaxf(mst, wts[sg * group + r]);
+            float lst = 0.f;
+            for (int sg = 0; sg < nseg; ++sg) {
+                const float w = fast_exp2(wts[sg * group + r] - (mst == -INFINITY ? 0.f : mst));
+                wts[sg * group + r] = w;
+                lst += w * mls[sg * group + r];
+            }
+            entry_ml[r] = make_float2(mst, lst);
+        }
+        __syncthreads();
+        for (int e = ctid; e < group * D; e += CT) {
+            const int r = e / D, at = e % D;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const float* po = p.part_o + (((int64_t)u + c_first) * group + r) * D + at;
+            const int64_t step = (int64_t)group * D;
+            int sg = 0;
+            for (; sg + 4 <= nseg; sg += 4) {
+                float v4[4];
+                #pragma unroll
+                for (int t = 0; t < 4; ++t) v4[t] = __ldcg(po + (sg + t) * step);
+                #pragma unroll
+                for (int t = 0; t < 4; ++t) acc[t] += wts[(sg + t) * group + r] * v4[t];
+            }
+            for (; sg < nseg; ++sg) acc[0] += wts[sg * group + r] * __ldcg(po + sg * step);
+            const float ost = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            const float2 ml = entry_ml[r];
+            const int64_t orow = (int64_t)b * g.hq + h * group + r;
+            p.out[orow * D + d4_dim(at)] = __float2bfloat16(ost / ml.y);
+            if (at == 0 && p.lse) p.lse[orow] = (ml.x + __log2f(ml.y)) * 0.69314718055994531f;
+        }
+        if (ctid == 0) p.counters[u] = 0;
+        __syncthreads();
     }
 }
 
 template <int NH, bool CAP>
 cudaError_t launch_decode4_t(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s) {
-    // merge buffer: the warps' [group][D] partials, or two [grid][group] arrays
+    // merge buffer: the warps' first partials, or two [grid][group] arrays
     // for the merge across CTAs, whichever is larger (a multiple of 4)
-    constexpr int kCap = NH == 1 ? 113 * 1024 : 227 * 1024;
+    constexpr int kCap = (NH == 1 ? 113 : 227) * 1024 - 1024;   // static shared memory besides
     const int group = c->geo.group;
-    const int mo = std::max(kD4Warps * group * kD4Dim, 2 * grid * group);
+    const int mo = std::max(kD4Warps * group * kD4HeadFloats, 2 * grid * group);
     p.merge_floats = (mo + 3) & ~3;
-    const int merge_bytes = (p.merge_floats + kD4Warps * group * 2) * 4;
-    constexpr int kMaxStages4 = 32;
-    constexpr int kMisc = kMaxStages4 * 24 + 16 + 32 * 32 + 16 + 128;   // barriers, descriptions, flags, batch, alignment
-    // a multiple of the warps, so a stage always belongs to the same one
-    p.nst = std::min(kMaxStages4, (kCap - merge_bytes - kMisc) / kD4StageBytes) / kD4Warps * kD4Warps;
-    p.owners = kD4Warps;
-    if (p.nst < kD4Warps) return cudaErrorInvalidConfiguration;
-    const int smem = p.nst * kD4StageBytes + merge_bytes + kMisc;
+    const int merge_bytes = (p.merge_floats + 2 * kD4Warps * group * 2) * 4;
+    const int smem = kD4Stages * kD4StageBytes + merge_bytes;
+    if (smem > kCap) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap);
     if (e == cudaSuccess && NH == 1)
         e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributePreferredSharedMemoryCarveout,
