@@ -65,7 +65,9 @@ struct CallSeqs {
 struct Cap {
     int32_t on;
     float k1, a, b;
-    float ref;                   // prefill: fixed reference of the exponentials
+    // prefill: the exponentials' fixed reference; a tanh(y) as an odd polynomial
+    // of the raw product for |y| <= 1/2, |x| <= limit
+    float ref, limit, poly[4];
 };
 Cap make_cap(float score_cap, int head_dim);
 constexpr float kMinScoreCap = 1.f / 64.f, kMaxScoreCap = 64.f;

@@ -196,6 +196,21 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Bits of a start for 1 / d, less d's: twice the bits of 1.0, less what
+// centres the error (12.5 % at most over d's mantissa).
+constexpr uint32_t kRcpStart = 0x7EF311C7u;
+// max(|a|, |b|, |c|).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // max(a, b, c) in one instruction (three-input max.f32, sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
@@ -786,11 +801,12 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     uint32_t sr[128];
                     tmem_ld128(tS, sr);
                     const bool fast = !masked && kt.nkeys == 128;
-                    if (!CAP && !fast) {
-                        // invisible or absent columns -> -inf, once (branch-free)
+                    if (!fast) {
+                        // invisible or absent columns -> -inf, once (branch-free); capped
+                        // scores: 0, so that what an absent column holds decides nothing
                         #pragma unroll
                         for (int c = 0; c < 128; ++c)
-                            sr[c] = ((vm[c >> 5] >> (c & 31)) & 1u) ? sr[c] : 0xff800000u;
+                            sr[c] = ((vm[c >> 5] >> (c & 31)) & 1u) ? sr[c] : CAP ? 0u : 0xff800000u;
                     }
                     if constexpr (CAP) {
                         // A capped score lies in [-cap, cap], so the exponentials
@@ -800,28 +816,93 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // full precision, and O is never rescaled.  Invisible columns
                         // are zeroed after the exponential (their capped score is
                         // finite too).
-                        uint64_t rsum2[4] = {0ull, 0ull, 0ull, 0ull};
-                        const float top = p.cap.a - p.cap.ref;
-                        #pragma unroll
-                        for (int g4 = 0; g4 < 4; ++g4) {
-                            float pv[32];
-                            #pragma unroll
-                            for (int e2 = 0; e2 < 32; ++e2) {
-                                const float z = fast_exp2(__uint_as_float(sr[g4 * 32 + e2]) * p.cap.k1);
-                                pv[e2] = fast_exp2(top - __fdividef(p.cap.b, 1.f + z));
-                            }
+                        //
+                        // tanh: MUFU.RCP (and TANH, too coarse besides) issue at a
+                        // quarter of EX2's rate here, 16 against 4 cycles a warp, so the
+                        // reciprocal of 1 - 2 / (1 + e^2y) would cost more than all the
+                        // rest.  While every |y| of the warp's tile is at most 1/2 (scores
+                        // up to half the cap), tanh is an odd polynomial of degree 7
+                        // (1.3e-7 off at most), five FMA-pipe operations on raw scores.
+                        // Otherwise the tile's exponentials are taken again with the
+                        // formula, its reciprocal by Newton's iteration.
+                        uint64_t rsum2[4];
+                        uint32_t pk[16];
+                        // P of 16 columns: bf16 pairs and their sums
+                        auto put_half = [&](int c, float (&pv)[16], uint32_t* pk) {
                             if (!fast) {
                                 #pragma unroll
-                                for (int e2 = 0; e2 < 32; ++e2)
-                                    pv[e2] = ((vm[g4] >> e2) & 1u) ? pv[e2] : 0.f;
+                                for (int e2 = 0; e2 < 16; ++e2)
+                                    pv[e2] = ((vm[c >> 5] >> ((c & 31) + e2)) & 1u) ? pv[e2] : 0.f;
                             }
-                            uint32_t pk[16];
                             #pragma unroll
-                            for (int e2 = 0; e2 < 16; ++e2) {
+                            for (int e2 = 0; e2 < 8; ++e2) {
                                 rsum2[e2 & 3] = add_f32x2(rsum2[e2 & 3], pack_f32x2(pv[2 * e2], pv[2 * e2 + 1]));
                                 pk[e2] = pack_bf16(pv[2 * e2], pv[2 * e2 + 1]);
                             }
-                            tmem_st16(tS + g4 * 16, pk);
+                        };
+                        float far[4] = {0.f, 0.f, 0.f, 0.f};      // largest |score| seen
+                        {
+                            const uint64_t nref = pack_f32x2(-p.cap.ref, -p.cap.ref);
+                            const uint64_t c0 = pack_f32x2(p.cap.poly[0], p.cap.poly[0]);
+                            const uint64_t c1 = pack_f32x2(p.cap.poly[1], p.cap.poly[1]);
+                            const uint64_t c2 = pack_f32x2(p.cap.poly[2], p.cap.poly[2]);
+                            const uint64_t c3 = pack_f32x2(p.cap.poly[3], p.cap.poly[3]);
+                            #pragma unroll
+                            for (int e2 = 0; e2 < 4; ++e2) rsum2[e2] = 0ull;
+                            #pragma unroll
+                            for (int g8 = 0; g8 < 8; ++g8) {
+                                float pv[16];
+                                #pragma unroll
+                                for (int e2 = 0; e2 < 8; ++e2) {
+                                    const int c = g8 * 16 + 2 * e2;
+                                    far[e2 & 3] = fmax3_abs(far[e2 & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                                    const uint64_t x = pack_u32x2(sr[c], sr[c + 1]);
+                                    const uint64_t tt = mul_f32x2(x, x);
+                                    const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(c3, tt, c2), tt, c1), tt, c0);
+                                    float x0, x1;
+                                    unpack_f32x2(fma_f32x2(x, y, nref), x0, x1);
+                                    pv[2 * e2] = fast_exp2(x0);
+                                    pv[2 * e2 + 1] = fast_exp2(x1);
+                                }
+                                put_half(g8 * 16, pv, pk + (g8 & 1) * 8);
+                                if (g8 & 1) tmem_st16(tS + (g8 >> 1) * 16, pk);
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, fmax3(fmaxf(far[0], far[1]), far[2], far[3]) > p.cap.limit)) {
+                            const float top = p.cap.a - p.cap.ref;
+                            const uint64_t topx2 = pack_f32x2(top, top);
+                            const uint64_t k1x2 = pack_f32x2(p.cap.k1, p.cap.k1);
+                            const uint64_t one = pack_f32x2(1.f, 1.f), two = pack_f32x2(2.f, 2.f);
+                            const uint64_t neg = pack_f32x2(-1.f, -1.f), nb = pack_f32x2(-p.cap.b, -p.cap.b);
+                            #pragma unroll
+                            for (int e2 = 0; e2 < 4; ++e2) rsum2[e2] = 0ull;
+                            #pragma unroll
+                            for (int g8 = 0; g8 < 8; ++g8) {
+                                float pv[16];
+                                #pragma unroll
+                                for (int e2 = 0; e2 < 8; ++e2) {
+                                    const int c = g8 * 16 + 2 * e2;
+                                    float x0, x1;
+                                    unpack_f32x2(mul_f32x2(pack_u32x2(sr[c], sr[c + 1]), k1x2), x0, x1);
+                                    // past 2^30 tanh is 1 in fp32 already
+                                    const float z0 = fast_exp2(fminf(x0, 30.f)), z1 = fast_exp2(fminf(x1, 30.f));
+                                    const uint64_t d = add_f32x2(pack_f32x2(z0, z1), one);
+                                    // start: the exponent and mantissa fields subtracted from
+                                    // twice those of 1 (within 12.5 %), then three steps
+                                    // r (2 - d r), each squaring the error
+                                    float d0, d1;
+                                    unpack_f32x2(d, d0, d1);
+                                    const uint64_t dn = mul_f32x2(d, neg);
+                                    uint64_t r2 = pack_u32x2(kRcpStart - __float_as_uint(d0), kRcpStart - __float_as_uint(d1));
+                                    #pragma unroll
+                                    for (int n3 = 0; n3 < 3; ++n3) r2 = mul_f32x2(r2, fma_f32x2(dn, r2, two));
+                                    unpack_f32x2(fma_f32x2(nb, r2, topx2), x0, x1);
+                                    pv[2 * e2] = fast_exp2(x0);
+                                    pv[2 * e2 + 1] = fast_exp2(x1);
+                                }
+                                put_half(g8 * 16, pv, pk + (g8 & 1) * 8);
+                                if (g8 & 1) tmem_st16(tS + (g8 >> 1) * 16, pk);
+                            }
                         }
                         tmem_st_wait();
                         tc_fence_before();
