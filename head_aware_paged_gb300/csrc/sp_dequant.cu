@@ -1,0 +1,79 @@
+// sp_dequant.cu -- 4-bit history pages -> bf16 pages in the workspace, ahead of
+// a prefill over them.
+//
+// Every query tile of a chunk reads the same history, so its codes are turned
+// into bf16(code * scale * channel scale) once per call instead of once per
+// work item: a converter inside k_prefill (two warps next to eight softmax
+// warps) took about 8,000 cycles for the K and V of a tile whose products take
+// 2,048, and a fourth warpgroup of converters cost the softmax its registers
+// (2,048 rows after 16,384: 188 us that way, 137 us this way, 128 us on bf16
+// pages).  Bound by memory: 144 bytes read and 512 written a key, most of which
+// stay in L2 for the kernel that follows.
+#include "sp_device.cuh"
+#include "sp_internal.h"
+
+namespace sp {
+
+namespace {
+
+// One block per (unit, page) of the call, grid-strided.  A thread converts one
+// block of 16 dimensions of a row; eight neighbours write a row's 256 bytes.
+__global__ void __launch_bounds__(256) k_dequant4(const __grid_constant__ DequantParams p) {
+    const Geo& g = p.geo;
+    const int P = g.page, D = g.d;
+    const int total = p.page_off[p.n_units];
+    for (int blk = blockIdx.x; blk < total; blk += gridDim.x) {
+        int a = 0, z = p.n_units - 1;                // unit with page_off[u] <= blk < page_off[u + 1]
+        while (a < z) {
+            const int mid = (a + z + 1) >> 1;
+            if (p.page_off[mid] <= blk) a = mid; else z = mid - 1;
+        }
+        const int u = p.unit0 + a, pg = blk - p.page_off[a];
+        const int b = u / g.hkv, h = u - b * g.hkv;
+        const int64_t row = g.unit_row(p.seq[b], p.layer, h);
+        int32_t phys = p.meta.ptab[row * g.max_pages_unit + pg];
+        if (phys < 0 || phys >= g.num_pages) {       // the same for the whole block
+            if (threadIdx.x == 0) atomicOr(p.meta.status, kStatusBadPage);
+            phys = 0;                                // convert something harmless
+        }
+        if (threadIdx.x == 0) p.tab[(int64_t)u * g.max_pages_unit + pg] = blk;
+        const float* ks = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
+        const float* vs = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
+        const int c = threadIdx.x & 7;               // this thread's block of a row
+        #pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float sc[16];
+            #pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 v4 = __ldg(reinterpret_cast<const float4*>((kv ? vs : ks) + c * 16 + e));
+                sc[e] = v4.x; sc[e + 1] = v4.y; sc[e + 2] = v4.z; sc[e + 3] = v4.w;
+            }
+            for (int r = threadIdx.x >> 3; r < P; r += 32) {
+                const int s = r & 15;
+                const uint8_t* grp = (kv ? p.vpool : p.kpool) + fp4_group_off(phys, r, P);
+                float x[16];
+                fp4_value16(__ldg(reinterpret_cast<const uint2*>(grp + (kv ? fp4_v_code(s, c) : fp4_k_code(s, c)))),
+                            __ldg(grp + (kv ? fp4_v_scale(s, c) : fp4_k_scale(s, c))), x);
+                uint32_t o[8];
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = pack_bf16(x[2 * e] * sc[2 * e], x[2 * e + 1] * sc[2 * e + 1]);
+                st_global_v8((kv ? p.v : p.k) + ((int64_t)blk * P + r) * D + c * 16,
+                             o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+            }
+        }
+    }
+}
+
+static_assert(sizeof(DequantParams) <= 32764, "dequantisation parameters exceed the kernel parameter space");
+
+}  // namespace
+
+cudaError_t launch_dequant4(const sp_cache* c, const DequantParams& p, cudaStream_t s) {
+    const int total = p.page_off[p.n_units];
+    if (total <= 0) return cudaSuccess;
+    const int grid = total < 16 * c->num_sms ? total : 16 * c->num_sms;
+    k_dequant4<<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace sp

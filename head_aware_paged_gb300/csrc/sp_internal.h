@@ -153,6 +153,9 @@ struct Workspace {
     int32_t* counters;    int64_t max_counter_units;
     float* split_o;       float* split_ml;        // prefill pieces of split items
     int32_t* scratch;     int64_t scratch_ints;   // export / visible-count staging
+    // 4-bit pages: bf16 copies of a prefill's history pages, and their table
+    __nv_bfloat16* deq_k; __nv_bfloat16* deq_v;  int64_t deq_pages;
+    int32_t* deq_tab;
 };
 
 }  // namespace sp
@@ -187,8 +190,8 @@ struct sp_cache {
     cudaEvent_t stage_ev[kStaging] = {};
     size_t stage_bytes = 0;                       // size of each buffer
     int stage_next = 0;
-    // [capped ? 6 : 0 + (speculative ? 4 : two issuers ? 3 : 4-bit ? 5 : FP8 ? 2 : D == 128)][log2(P) - 4, or 0]: attributes set
-    bool prefill_checked[12][4] = {};
+    // [capped ? 5 : 0 + (speculative ? 4 : two issuers ? 3 : FP8 ? 2 : D == 128)][log2(P) - 4, or 0]: attributes set
+    bool prefill_checked[10][4] = {};
     // Caller's event pair armed by sp_set_launch_events for the next
     // attention call (both null when not armed).
     cudaEvent_t launch_ev[2] = {};
@@ -246,6 +249,20 @@ cudaError_t launch_decode(const sp_cache* c, DecodeParams& p, cudaStream_t s);
 cudaError_t launch_decode_capped(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
 cudaError_t launch_decode4(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
 cudaError_t launch_decode4_capped(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s);
+// One prefill's units whose 4-bit pages become bf16 pages in the workspace
+// (sp_dequant.cu): unit (b, h) of the call takes the workspace pages from
+// page_off[b * hkv + h - unit0] on.
+struct DequantParams {
+    Meta meta;
+    Geo geo;
+    int32_t layer, unit0, n_units;
+    const uint8_t *kpool, *vpool;
+    __nv_bfloat16 *k, *v;
+    int32_t* tab;                // [max_batch][hkv][max_pages_unit]
+    int32_t seq[kMaxCallSeqs];
+    int32_t page_off[kMaxDecodeUnits + 1];
+};
+cudaError_t launch_dequant4(const sp_cache* c, const DequantParams& p, cudaStream_t s);
 cudaError_t launch_rope(const sp_cache* c, const RopeParams& p, cudaStream_t s);
 cudaError_t launch_transfer(const sp_cache* c, const TransferParams& p, cudaStream_t s);
 

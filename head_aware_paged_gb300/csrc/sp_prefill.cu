@@ -117,12 +117,13 @@ int64_t prefill_max_tiles(const sp_config* c) {
     return ((int64_t)c->max_tokens / 128 + c->max_batch + 1) * c->num_q_heads + 512;
 }
 
-sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
-                       const int32_t* cu_q, const __nv_bfloat16* q, const __nv_bfloat16* k,
-                       const __nv_bfloat16* v, __nv_bfloat16* out, float* lse,
-                       const Cap& cap, cudaStream_t stream) {
+// The call's units [unit0, unit1) (call sequence * hkv + KV head); `first` and
+// `last` of the call's launches carry its launch events.
+static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                               const int32_t* cu_q, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                               const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, const Cap& cap,
+                               int unit0, int unit1, bool first, bool last, cudaStream_t stream) {
     const int T = cu_q[n_seqs];
-    if (T == 0) return SP_OK;
     std::unique_ptr<PrefillParams> pp(new PrefillParams());
     PrefillParams& p = *pp;
     p.meta = c->meta;
@@ -135,8 +136,11 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     p.out = out;
     p.lse = lse;
     p.cap = cap;
-    p.kcodes = reinterpret_cast<const uint8_t*>(c->kpool);
-    p.vcodes = reinterpret_cast<const uint8_t*>(c->vpool);
+    p.hist_ptab = nullptr;
+    if (c->geo.fp4) {                          // the history is read from its bf16 copies
+        p.hist_ptab = c->ws.deq_tab;
+        p.geo.num_pages = (int32_t)c->ws.deq_pages;
+    }
     p.split_o = reinterpret_cast<float4*>(c->ws.split_o);
     p.split_ml = reinterpret_cast<float2*>(c->ws.split_ml);
     struct Cand { int64_t cost; int32_t unit; int4 item; };   // unit: call sequence * Hkv + KV head
@@ -156,6 +160,8 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
         p.cnt[b] = cb;
         p.row0[b] = cu_q[b];
         for (int h = 0; h < c->cfg.num_kv_heads; ++h) {
+            const int cu = b * c->cfg.num_kv_heads + h;
+            if (cu < unit0 || cu >= unit1) continue;
             const size_t ui = ((size_t)seq * c->cfg.num_layers + layer) * c->cfg.num_kv_heads + h;
             const UnitPol& u = c->h_pol[ui];
             const int32_t* idx = c->h_idx[seq].data() + u.idx_off;
@@ -228,7 +234,8 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     std::vector<int32_t> rank(n_units, 0);
     int64_t kv_bytes = 0;
     for (int b = 0; b < n_seqs; ++b)
-        kv_bytes += (int64_t)(p.n_b[b] + p.cnt[b]) * c->cfg.num_kv_heads * 2 * c->geo.row_bytes();
+        kv_bytes += (int64_t)(p.n_b[b] + p.cnt[b]) * c->cfg.num_kv_heads * 2 * c->cfg.head_dim *
+                    (c->geo.fp8 ? 1 : 2);
     if (kv_bytes > kL2UnitOrderBytes) {
         std::vector<int64_t> unit_cost(n_units, 0);
         for (const Cand& cd : cands) unit_cost[cd.unit] += cd.cost;
@@ -279,6 +286,10 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
             std::push_heap(heap.begin(), heap.end(), later);
         }
     }
+    if (n_items == 0) {                        // no rows in these units
+        if (last) launch_mark_end(c, stream);
+        return SP_OK;
+    }
     // The items grouped by CTA (each CTA's in the sorted order), then the CTA
     // offsets: inside the kernel parameters when they fit, else one upload
     // through the next pinned staging buffer (asynchronous; waits only if
@@ -301,7 +312,7 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     // bf16 K/V, head_dim 128, two query tiles per item (the single issuer
     // sits behind its own commits and waits while the other tile's P is
     // ready: 0.67 vs 0.73 of peak on 128K calls, 0.46 vs 0.50 on 8K).
-    const bool two = !c->geo.fp8 && !c->geo.fp4 && p.nq == 2 && c->cfg.head_dim == 128;
+    const bool two = !c->geo.fp8 && p.nq == 2 && c->cfg.head_dim == 128;
     // speculative exponentials (SPEC) for calls whose items average more
     // than kSpecTilesPerItem tiles
     bool spec = false;
@@ -327,18 +338,16 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
         !encode_tmap_2d(&tv, v, (uint64_t)c->cfg.num_kv_heads * D, T,
                         (uint64_t)c->cfg.num_kv_heads * D * 2, 64, 128, true, &err))
         return fail(SP_ERR_CUDA, err);
-    launch_mark_start(c, stream);
+    if (first && !c->geo.fp4) launch_mark_start(c, stream);
 #define SP_PF(DD, PP) \
     if (D == DD && P == PP) e = launch_prefill_t<DD, PP>(c, p, grid, tq, tk, tv, stream); else
 #define SP_PF2(PP) \
-    if (P == PP) e = spec ? launch_prefill_t<128, PP, kHistBf16, true, true>(c, p, grid, tq, tk, tv, stream) \
-                          : launch_prefill_t<128, PP, kHistBf16, true>(c, p, grid, tq, tk, tv, stream); else
+    if (P == PP) e = spec ? launch_prefill_t<128, PP, false, true, true>(c, p, grid, tq, tk, tv, stream) \
+                          : launch_prefill_t<128, PP, false, true>(c, p, grid, tq, tk, tv, stream); else
 #define SP_PF8(PP) \
-    if (D == 128 && P == PP) e = launch_prefill_t<128, PP, kHistFp8>(c, p, grid, tq, tk, tv, stream); else
+    if (D == 128 && P == PP) e = launch_prefill_t<128, PP, true>(c, p, grid, tq, tk, tv, stream); else
     if (cap.on) {
         e = launch_prefill_capped(c, p, grid, two, tq, tk, tv, stream);
-    } else if (c->geo.fp4) {   // 4-bit pages (head_dim 128, checked at create)
-        e = launch_prefill_t<128, 0, kHistFp4>(c, p, grid, tq, tk, tv, stream);
     } else if (c->geo.fp8) {   // FP8 pages (head_dim 128, checked at create)
         SP_PF8(16) SP_PF8(32) SP_PF8(64) SP_PF8(128)
         e = cudaErrorInvalidValue;
@@ -369,7 +378,53 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, "prefill merge launch");
     }
-    launch_mark_end(c, stream);
+    if (last) launch_mark_end(c, stream);
+    return SP_OK;
+}
+
+sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                       const int32_t* cu_q, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                       const __nv_bfloat16* v, __nv_bfloat16* out, float* lse,
+                       const Cap& cap, cudaStream_t stream) {
+    if (cu_q[n_seqs] == 0) return SP_OK;
+    const int H = c->cfg.num_kv_heads, units = n_seqs * H;
+    if (!c->geo.fp4)
+        return prefill_units(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse, cap, 0, units, true, true, stream);
+    // 4-bit pages: the units' history becomes bf16 pages in the workspace, as
+    // many units at a time as fit, and the bf16 kernel reads those
+    // (sp_dequant.cu says why).
+    std::unique_ptr<DequantParams> dp(new DequantParams());
+    dp->meta = c->meta;
+    dp->geo = c->geo;
+    dp->layer = layer;
+    dp->kpool = reinterpret_cast<const uint8_t*>(c->kpool);
+    dp->vpool = reinterpret_cast<const uint8_t*>(c->vpool);
+    dp->k = c->ws.deq_k;
+    dp->v = c->ws.deq_v;
+    dp->tab = c->ws.deq_tab;
+    std::copy(seq_ids, seq_ids + n_seqs, dp->seq);
+    launch_mark_start(c, stream);
+    for (int u0 = 0; u0 < units;) {
+        int64_t pages = 0;
+        int u1 = u0;
+        dp->unit0 = u0;
+        dp->page_off[0] = 0;
+        for (; u1 < units; ++u1) {
+            const int b = u1 / H;
+            const int64_t n = cu_q[b + 1] > cu_q[b]
+                                  ? c->h_npages[((size_t)seq_ids[b] * c->cfg.num_layers + layer) * H + u1 % H] : 0;
+            if (pages + n > c->ws.deq_pages) break;   // (one unit always fits)
+            pages += n;
+            dp->page_off[u1 - u0 + 1] = (int32_t)pages;
+        }
+        dp->n_units = u1 - u0;
+        const cudaError_t e = launch_dequant4(c, *dp, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "history conversion launch");
+        const sp_status s = prefill_units(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse, cap, u0, u1, u0 == 0,
+                                          u1 == units, stream);
+        if (s != SP_OK) return s;
+        u0 = u1;
+    }
     return SP_OK;
 }
 

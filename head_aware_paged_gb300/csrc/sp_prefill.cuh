@@ -98,8 +98,9 @@ struct PrefillParams {
     float4* split_o;
     float2* split_ml;
     Cap cap;                     // capped scores (instances with CAP)
-    const uint8_t* kcodes;       // 4-bit pages (sp_fp4.cuh)
-    const uint8_t* vcodes;
+    // 4-bit pages: the call's history as bf16 pages in the workspace, and their
+    // table [sequence of the call][KV head][max_pages_unit] (null otherwise)
+    const int32_t* hist_ptab;
     int32_t seq[kMaxCallSeqs];
     int32_t n_b[kMaxCallSeqs];   // tokens held before the chunk
     int32_t cnt[kMaxCallSeqs];   // chunk rows
@@ -115,9 +116,7 @@ struct PrefillParams {
 
 namespace {
 
-enum { kHistBf16 = 0, kHistFp8 = 1, kHistFp4 = 2 };   // page type of the history
-
-template <int D, int KV = kHistBf16>
+template <int D, bool F8 = false>
 struct PfShape {
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfBytes = 128 * 128;            // 128 rows x 128 bytes
@@ -125,9 +124,8 @@ struct PfShape {
     static constexpr int kKVBytes = kHalves * kHalfBytes;    // one K or V tile
     // FP8 history pages land in one of two code slots (128 keys x 128 bytes)
     // before the converter warps write them into a bf16 stage
-    // (4-bit pages: eight groups of 1152 bytes)
-    static constexpr int kF8Slot = KV == kHistFp4 ? 8 * kFp4GroupBytes : 128 * 128;
-    static constexpr int kFixed = 2 * kQBytes + (KV != kHistBf16 ? 2 * kF8Slot : 0);
+    static constexpr int kF8Slot = 128 * 128;
+    static constexpr int kFixed = 2 * kQBytes + (F8 ? 2 * kF8Slot : 0);
     static constexpr int kMisc = 2048;                       // barriers, flags, alignment slack
     static constexpr int kStagesFit = (kSmemLimit - kFixed - kMisc) / kKVBytes;
     static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
@@ -166,7 +164,8 @@ __device__ __forceinline__ Item load_item(const PrefillParams& p, const int4* it
     const int64_t urow = g.unit_row(seq, p.layer, m.kvh);
     m.pol = p.meta.pol[urow];
     m.idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + m.pol.idx_off;
-    m.ptab = p.meta.ptab + urow * g.max_pages_unit;
+    m.ptab = p.hist_ptab ? p.hist_ptab + ((int64_t)m.b * g.hkv + m.kvh) * g.max_pages_unit
+                         : p.meta.ptab + urow * g.max_pages_unit;
     return m;
 }
 
@@ -223,16 +222,14 @@ __device__ __forceinline__ uint32_t lowmask32(int32_t n) {
     return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : ((1u << n) - 1u);
 }
 
-// PT: the page size, or 0 to read it from the geometry (capped scores and
-// 4-bit pages: one instance for every page size).
-template <int D, int PT, int KV, bool TWO = false, bool SPEC = false, bool CAP = false>
+// PT: the page size, or 0 to read it from the geometry (capped scores: one
+// instance for every page size).
+template <int D, int PT, bool F8, bool TWO = false, bool SPEC = false, bool CAP = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
           const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp) {
-    using S = PfShape<D, KV>;
-    constexpr bool F8 = KV != kHistBf16;     // history of codes, turned into bf16 rows by warps 10-11
-    constexpr bool F4 = KV == kHistFp4;
+    using S = PfShape<D, F8>;
     const int P = PT ? PT : p.geo.page;
     constexpr int NS = S::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -350,15 +347,9 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     for (int pg = 0; pg < np; ++pg) {
                         const int32_t phys = it.ptab[pk.start / P + pg];
                         if (phys < 0 || phys >= g.num_pages) continue;
-                        if constexpr (F4) {
-                            const int64_t off = (int64_t)phys * P * kFp4RowBytes;
-                            bulk_prefetch(p.kcodes + off, P * kFp4RowBytes);
-                            bulk_prefetch(p.vcodes + off, P * kFp4RowBytes);
-                        } else {
-                            for (int hf = 0; hf < (F8 ? 1 : S::kHalves); ++hf) {   // FP8 rows: one 128-byte box
-                                tma_prefetch_2d(&tmKp, hf * 64, phys * P);
-                                tma_prefetch_2d(&tmVp, hf * 64, phys * P);
-                            }
+                        for (int hf = 0; hf < (F8 ? 1 : S::kHalves); ++hf) {   // FP8 rows: one 128-byte box
+                            tma_prefetch_2d(&tmKp, hf * 64, phys * P);
+                            tma_prefetch_2d(&tmVp, hf * 64, phys * P);
                         }
                     }
                 }
@@ -396,17 +387,12 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         const uint32_t f = F & 1, fr = F >> 1;
                         if (fr > 0 && !mbar_wait(&f_empty[f], (fr - 1) & 1, abort_flag, status)) { ok = false; break; }
                         jobs[f] = make_int4((int)st, kv, it.kvh, np * P);
-                        mbar_arrive_expect_tx(&f_full[f], np * P * (F4 ? kFp4RowBytes : 128));
+                        mbar_arrive_expect_tx(&f_full[f], np * P * 128);
                         for (int pg = 0; pg < np; ++pg) {
                             int32_t phys = it.ptab[kt.start / P + pg];
                             if (phys < 0 || phys >= g.num_pages) { atomicOr(status, kStatusBadPage); phys = 0; }
-                            if constexpr (F4)
-                                bulk_load(sF8 + f * S::kF8Slot + pg * P * kFp4RowBytes,
-                                          (kv ? p.vcodes : p.kcodes) + (int64_t)phys * P * kFp4RowBytes,
-                                          P * kFp4RowBytes, &f_full[f]);
-                            else
-                                tma_load_2d(sF8 + f * S::kF8Slot + pg * P * 128, kv ? &tmVp : &tmKp,
-                                            &f_full[f], 0, phys * P);
+                            tma_load_2d(sF8 + f * S::kF8Slot + pg * P * 128, kv ? &tmVp : &tmKp,
+                                        &f_full[f], 0, phys * P);
                         }
                         ++F;
                     } else {
@@ -678,22 +664,7 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
             const uint8_t* src = sF8 + f * S::kF8Slot;
             uint8_t* dst = sKV + jb.x * S::kKVBytes + (c16 >> 2) * S::kHalfBytes;
             const uint32_t ch = (c16 & 3) * 2;
-            if constexpr (F4) {
-                // block c16 of row r: code * scale (exact) times the channel's scale
-                for (int r = r0; r < jb.w; r += 8) {
-                    const uint8_t* grp = src + (r >> 4) * kFp4GroupBytes;
-                    const uint2 codes = *reinterpret_cast<const uint2*>(
-                        grp + (jb.y ? fp4_v_code(r & 15, c16) : fp4_k_code(r & 15, c16)));
-                    float x[16];
-                    fp4_value16(codes, grp[jb.y ? fp4_v_scale(r & 15, c16) : fp4_k_scale(r & 15, c16)], x);
-                    uint32_t o[8];
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[e] = pack_bf16(x[2 * e] * sc[2 * e], x[2 * e + 1] * sc[2 * e + 1]);
-                    *reinterpret_cast<uint4*>(dst + sw128(r, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + sw128(r, ch + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-            } else for (int r = r0; r < jb.w; r += 8) {
+            for (int r = r0; r < jb.w; r += 8) {
                 const uint4 q4 = *reinterpret_cast<const uint4*>(src + sw128(r, c16));
                 const uint32_t w[4] = {q4.x, q4.y, q4.z, q4.w};
                 uint32_t o[8];
@@ -1158,24 +1129,24 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
 static_assert(sizeof(PrefillParams) + 5 * sizeof(CUtensorMap) <= 32764,
               "prefill parameters exceed the kernel parameter space");
 
-template <int D, int P, int KV = kHistBf16, bool TWO = false, bool SPEC = false, bool CAP = false>
+template <int D, int P, bool F8 = false, bool TWO = false, bool SPEC = false, bool CAP = false>
 cudaError_t launch_prefill_t(sp_cache* c, const PrefillParams& p, int grid,
                              const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              cudaStream_t s) {
-    using Sh = PfShape<D, KV>;
-    bool& checked = c->prefill_checked[(CAP ? 6 : 0) + (SPEC ? 4 : TWO ? 3 : KV == kHistFp4 ? 5 : KV == kHistFp8 ? 2 : D == 128)][P == 0 || P == 16 ? 0 : P == 32 ? 1 : P == 64 ? 2 : 3];
+    using Sh = PfShape<D, F8>;
+    bool& checked = c->prefill_checked[(CAP ? 5 : 0) + (SPEC ? 4 : TWO ? 3 : F8 ? 2 : D == 128)][P == 0 || P == 16 ? 0 : P == 32 ? 1 : P == 64 ? 2 : 3];
     if (!checked) {   // once per cache and kernel instance
         cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, P, KV, TWO, SPEC, CAP>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, P, F8, TWO, SPEC, CAP>);
         if (e != cudaSuccess) return e;
         // The setmaxnreg split assumes exactly kLaunchRegs registers per thread
         // at launch; anything else could leave an increase waiting forever.
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(k_prefill<D, P, KV, TWO, SPEC, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        e = cudaFuncSetAttribute(k_prefill<D, P, F8, TWO, SPEC, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
         if (e != cudaSuccess) return e;
         checked = true;
     }
-    k_prefill<D, P, KV, TWO, SPEC, CAP><<<grid, kPfThreads, Sh::kSmem, s>>>(p, tq, tk, tv, c->tm_kpool, c->tm_vpool);
+    k_prefill<D, P, F8, TWO, SPEC, CAP><<<grid, kPfThreads, Sh::kSmem, s>>>(p, tq, tk, tv, c->tm_kpool, c->tm_vpool);
     return cudaGetLastError();
 }
 

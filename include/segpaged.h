@@ -115,7 +115,8 @@ typedef struct sp_config {
  * x * (1 / channel scale) is what the block quantises, and the stored value is
  * code * scale * channel scale.  Every call that takes a cache takes such a
  * one: decode multiplies code * scale (exact in f16) with q * channel scale
- * in f16, prefill reads bf16(code * scale * channel scale), sp_rope_realign
+ * in f16, prefill reads bf16(code * scale * channel scale) from copies that it
+ * makes in the workspace, sp_rope_realign
  * dequantises, rotates and quantises again with new block scales, and a packed
  * row is its 64 code bytes (two dimensions a byte, the even one low), then its
  * 8 scales. */
@@ -128,7 +129,9 @@ typedef struct sp_cache sp_cache;  /* opaque host handle */
  *         of kv_dtype (bf16, or one byte for FP8); FP4: [num_pages]
  *         [page_size / 16][1152] bytes, 16 rows' codes and their scales.
  *   meta: page tables, policies, retrieval lists, free-page stack, status.
- *   ws:   per-call scratch (prefill work list, decode split partials). */
+ *   ws:   per-call scratch (prefill work list, decode split partials; FP4:
+ *         also bf16 copies of a prefill's history, 2 GiB or the whole pool's
+ *         rows if that is less, at least one unit's). */
 sp_status sp_required_bytes(const sp_config* cfg, size_t* pool_bytes,
                             size_t* meta_bytes, size_t* ws_bytes);
 
