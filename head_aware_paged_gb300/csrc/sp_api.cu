@@ -697,8 +697,10 @@ sp_status sp_attention_prefill_capped(sp_cache* c, int32_t layer, const int32_t*
                                       float* lse, void* stream) {
     if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_cap(score_cap)) return fail(SP_ERR_INVALID_ARG, "score_cap must lie in [1/64, 64]");
-    return attention_prefill(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse,
-                             make_cap(score_cap, c->cfg.head_dim), stream);
+    return no_throw([&] {
+        return attention_prefill(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse,
+                                 make_cap(score_cap, c->cfg.head_dim), stream);
+    });
 }
 
 sp_status sp_attention_decode_capped(sp_cache* c, int32_t layer, const int32_t* seq_ids,
@@ -706,8 +708,10 @@ sp_status sp_attention_decode_capped(sp_cache* c, int32_t layer, const int32_t* 
                                      float* lse, void* stream) {
     if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_cap(score_cap)) return fail(SP_ERR_INVALID_ARG, "score_cap must lie in [1/64, 64]");
-    return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
-                            make_cap(score_cap, c->cfg.head_dim), stream);
+    return no_throw([&] {
+        return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
+                                make_cap(score_cap, c->cfg.head_dim), stream);
+    });
 }
 
 sp_status sp_set_launch_events(sp_cache* c, void* start_event, void* end_event) {

@@ -46,7 +46,10 @@ constexpr int kD4Stages = kD4Warps * kD4Depth;
 constexpr int kD4TileBytes = kFp4ItemSlots * kFp4RowBytes;
 constexpr int kD4StageBytes = 2 * kD4TileBytes;      // K, then V
 constexpr int kD4Dim = 128;
-constexpr float kLazyLog2 = 8.f;
+// The reference of the exponentials is set kRefBelow under a maximum and
+// raised when a score passes it by kRefAbove, so P lies between 2^7 (at first)
+// and 2^15 at its largest: f16 then holds weights down to 2^-31 of it.
+constexpr float kRefBelow = 7.f, kRefAbove = 15.f;
 // A partial's head in shared memory: dimension 16 gl + 2 mt + i at 16 mt + 2 gl +
 // i, heads 132 floats apart (a half warp's 8-byte stores then meet no bank twice).
 constexpr int kD4HeadFloats = 132;
@@ -333,10 +336,9 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                             if (!(e < 2 ? in_a : in_b)) sc[q][nh][e] = -INFINITY;
                 }
             }
-            // Running maximum, raised only when a score passes it by 2^8 (or the
-            // unit has none yet): below that P stays inside f16 and the sums
-            // inside fp32, and a warp agrees by one vote instead of exchanging
-            // its rows' maxima for every item.
+            // Running reference, raised only when a score passes it by kRefAbove
+            // (or the unit has none yet): a warp agrees by one vote instead of
+            // exchanging its rows' maxima for every item.
             float mx[NH][2];
             bool grew = false;
             #pragma unroll
@@ -347,7 +349,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                     #pragma unroll
                     for (int q = 1; q < kD4Groups; ++q)
                         mx[nh][e] = fmaxf(mx[nh][e], fmaxf(sc[q][nh][e], sc[q][nh][2 + e]));
-                    grew = grew || mx[nh][e] > m_run[nh][e] + kLazyLog2;
+                    grew = grew || mx[nh][e] > m_run[nh][e] + kRefAbove;
                 }
             if (__any_sync(0xffffffffu, grew)) {
                 #pragma unroll
@@ -358,7 +360,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        const float m_new = fmaxf(m_run[nh][e], x);
+                        const float m_new = fmaxf(m_run[nh][e], x - kRefBelow);
                         const float alpha = fast_exp2(m_run[nh][e] - (m_new == -INFINITY ? 0.f : m_new));
                         m_run[nh][e] = m_new;
                         l_run[nh][e] *= alpha;

@@ -22,7 +22,9 @@
 //             with their halves swapped;
 //   V scales  one 32-bit word per (block, slot mod 4): slots j, j+4, j+8, j+12.
 #pragma once
+#if defined(__CUDACC__)
 #include <cuda_fp16.h>
+#endif
 #include <stdint.h>
 
 #include "sp_rules.h"

@@ -227,6 +227,15 @@ inline void launch_mark_end(sp_cache* c, cudaStream_t s) {
 // Error plumbing (sp_api.cu).
 sp_status fail(sp_status s, const std::string& msg);
 sp_status cuda_fail(cudaError_t e, const char* what);
+// Runs a C entry point's body: no C++ exception (host memory) leaves it.
+template <typename F>
+sp_status no_throw(F&& body) {
+    try {
+        return body();
+    } catch (...) {
+        return fail(SP_ERR_UNSUPPORTED, "no host memory");
+    }
+}
 bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
                     bool swizzle128, std::string* err, bool bytes = false);

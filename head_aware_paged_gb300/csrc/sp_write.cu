@@ -295,7 +295,7 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
         for (int h = 0; h < H; ++h) {
             const UnitPol& u = c->h_pol[((size_t)seq * L + layer) * H + h];
             const int32_t* idx = c->h_idx[seq].data() + u.idx_off;
-            demand += (int32_t)(unit_pages(u, idx, n_new, P) - unit_pages(u, idx, n, P));
+            if (n_new != n) demand += (int32_t)(unit_pages(u, idx, n_new, P) - unit_pages(u, idx, n, P));
             p.off[b * H + h + 1] = demand;
         }
     }
@@ -348,11 +348,19 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
                                        int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                        int64_t v_stride, void* q_out, double rope_theta,
                                        const double* inv_freq, void* stream) {
-    if (!c || !cu_new || !k || !v) return fail(SP_ERR_INVALID_ARG, "null argument");
-    if ((q == nullptr) != (q_out == nullptr)) return fail(SP_ERR_INVALID_ARG, "give both q and q_out or neither");
+    if (!c || !cu_new) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     sp_status s = check_seq_list(c, seq_ids, n_seqs);
     if (s != SP_OK) return s;
+    if (cu_new[0] != 0) return fail(SP_ERR_INVALID_ARG, "cu_new[0] must be 0");
+    for (int b = 0; b < n_seqs; ++b)
+        if (cu_new[b + 1] < cu_new[b]) return fail(SP_ERR_INVALID_ARG, "cu_new must be non-decreasing");
+    if (cu_new[n_seqs] > c->cfg.max_tokens) return fail(SP_ERR_INVALID_ARG, "more new tokens than max_tokens");
+    if (cu_new[n_seqs] > 0) {                    // (without rows there may be no tensors)
+        if (!k || !v) return fail(SP_ERR_INVALID_ARG, "null argument");
+        if ((q == nullptr) != (q_out == nullptr))
+            return fail(SP_ERR_INVALID_ARG, "give both q and q_out or neither");
+    }
     const int d = c->cfg.head_dim;
     const int64_t kv = (int64_t)c->cfg.num_kv_heads * d;
     if (k_stride < kv || v_stride < kv || (q && q_stride < (int64_t)c->cfg.num_q_heads * d) ||
@@ -361,10 +369,6 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
          reinterpret_cast<uintptr_t>(q_out)) & 15)
         return fail(SP_ERR_INVALID_ARG, "q, k, v and q_out must be 16-byte aligned");
-    if (cu_new[0] != 0) return fail(SP_ERR_INVALID_ARG, "cu_new[0] must be 0");
-    for (int b = 0; b < n_seqs; ++b)
-        if (cu_new[b + 1] < cu_new[b]) return fail(SP_ERR_INVALID_ARG, "cu_new must be non-decreasing");
-    if (cu_new[n_seqs] > c->cfg.max_tokens) return fail(SP_ERR_INVALID_ARG, "more new tokens than max_tokens");
     if (!inv_freq && (!(rope_theta > 0.0) || !std::isfinite(rope_theta)))
         return fail(SP_ERR_INVALID_ARG, "rope_theta must be positive and finite");
     // frequencies as fractions of a turn, modulo one turn (whole turns a
@@ -386,9 +390,11 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
     auto* vp = static_cast<const __nv_bfloat16*>(v);
     auto* qo = static_cast<__nv_bfloat16*>(q_out);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (n_seqs <= kSmallSeqs && n_seqs * c->cfg.num_kv_heads <= kSmallUnits)
-        return write_rope<SmallWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
+    return no_throw([&] {
+        if (n_seqs <= kSmallSeqs && n_seqs * c->cfg.num_kv_heads <= kSmallUnits)
+            return write_rope<SmallWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
+                                          v_stride, qo, turn, st);
+        return write_rope<LargeWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
                                       v_stride, qo, turn, st);
-    return write_rope<LargeWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
-                                  v_stride, qo, turn, st);
+    });
 }

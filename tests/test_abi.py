@@ -78,3 +78,22 @@ def test_null_handle_calls_fail_cleanly(lib):
     assert lib.sp_attention_decode(None, 0, i32_array([0]), 1, None, None, None, None) == 1
     n = ctypes.c_int32()
     assert lib.sp_free_pages(None, ctypes.byref(n)) == 1
+
+
+def test_new_calls_refuse_null_handles(lib):
+    from head_aware_paged_gb300._lib import i32_array
+    one = i32_array([0, 1])
+    assert lib.sp_append_kv_rope(None, 0, one, 1, one, None, None, 0, None, 0, None, 0, None, 1e4, None, None) == 1
+    assert lib.sp_attention_prefill_capped(None, 0, one, 1, one, None, None, None, 30.0, None, None, None) == 1
+    assert lib.sp_attention_decode_capped(None, 0, one, 1, None, 30.0, None, None, None) == 1
+
+
+def test_fp4_config(lib):
+    from head_aware_paged_gb300 import KV_FP4, SegPagedError, sp_required_bytes
+    pool, _, ws = sp_required_bytes(_cfg(kv_dtype=KV_FP4))
+    assert pool == 2 * 512 * 64 * 72
+    assert ws >= 2 * 512 * 64 * 128 * 2           # bf16 copies of a prefill's history
+    for bad in (dict(head_dim=64), dict(page_size=8)):
+        with pytest.raises(SegPagedError) as ei:
+            sp_required_bytes(_cfg(kv_dtype=KV_FP4, **bad))
+        assert ei.value.status == 3

@@ -1,0 +1,156 @@
+"""GPU: attention over scores capped by cap * tanh(s / cap), prefill and
+decode, every page type, against 64 bits.
+
+Tolerances count roundings (tests/_attn64.py): prefill rounds P to bf16
+(2^-8 of each weight), decode to bf16 (bf16 pages) or f16 (FP8 and 4-bit
+pages, 2^-11, whose query times channel scale is f16 too, 2^-11 of each
+product); prefill reads FP8 rows rounded to bf16 (2^-8 of K's and V's).  The
+cap only shrinks what a score may be off by."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from _attn64 import attend, check
+from _gpu_common import f64, gpu_ready, pol_tuple, to_c_policies
+from oracle import fp4, fp8
+
+pytestmark = pytest.mark.gpu
+
+G, L, R = W.GLOBAL, W.LOCAL, W.RETRIEVAL
+
+
+def _mk(hq, hkv, d, P, seqs, max_len, pages, kv="bf16"):
+    import head_aware_paged_gb300 as H
+    return H.SegPagedCache(H.Config(num_layers=1, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=P,
+                                    max_seqs=seqs, max_seq_len=max_len, num_pages=pages, max_idx_per_seq=8192,
+                                    max_tokens=max_len, max_batch=seqs,
+                                    kv_dtype={"bf16": H.KV_BF16, "fp8": H.KV_FP8, "fp4": H.KV_FP4}[kv]))
+
+
+def _held(x, kv, s):
+    """What the pages hold of rows x [n, hkv, d], 64 bits on the device."""
+    if kv == "bf16" or x.shape[0] == 0:
+        return x.double()
+    xs = f64(x)
+    f = (lambda y, h: fp8.dequantize(fp8.quantize(y, s[h]), s[h])) if kv == "fp8" else (lambda y, h: fp4.stored(y))
+    return torch.tensor(np.stack([f(xs[:, h], h) for h in range(xs.shape[1])], 1), device="cuda")
+
+
+def _pols(hkv, n):
+    idx = np.arange(min(n, 70), n, 3, dtype=np.int32)          # early rows see nothing
+    return [W.HeadPolicy(G), W.HeadPolicy(L, 4, 90), W.HeadPolicy(R, idx=idx), W.HeadPolicy(L, 0, 1)][:hkv]
+
+
+CASES = [("bf16", 64, 16, 6, 2), ("bf16", 64, 128, 4, 4), ("bf16", 128, 64, 32, 4), ("bf16", 128, 32, 3, 3),
+         ("fp8", 128, 64, 16, 4), ("fp8", 128, 16, 3, 1), ("fp4", 128, 32, 8, 4), ("fp4", 128, 128, 36, 3)]
+
+
+@pytest.mark.parametrize("cap,qs", [(50.0, 1.0), (30.0, 12.0), (2.0, 1.0), (1.0 / 64, 3.0), (64.0, 40.0)])
+@pytest.mark.parametrize("kv,d,P,hq,hkv", CASES)
+def test_prefill_and_decode(kv, d, P, hq, hkv, cap, qs):
+    """qs spreads the scores: well inside the cap, around it, far past it."""
+    gpu_ready()
+    n, c = 300, 141
+    cache = _mk(hq, hkv, d, P, 2, n + c, 2 * hkv * ((n + c) // P + 4), kv)
+    pols = _pols(hkv, n + c)
+    pt = [pol_tuple(p) for p in pols]
+    ks = np.full((hkv, d), 2.0 ** -6, np.float32)
+    for s in range(2):
+        if kv == "fp8" and s == 0:
+            cache.set_kv_scales(0, ks, ks)
+        cache.set_policy(s, to_c_policies([pols]))
+    hist = [W.normal((n, hkv, d), 5 + i, device="cuda") for i in range(2)]
+    cache.build(0, 0, *hist)                                   # sequence 1 starts empty
+    q = (W.normal((2 * c, hq, d), 7, device="cuda").float() * qs).to(torch.bfloat16)
+    k, v = W.normal((2 * c, hkv, d), 8, device="cuda"), W.normal((2 * c, hkv, d), 9, device="cuda")
+    out, lse = cache.prefill(0, [0, 1], [0, c, 2 * c], q, k, v, score_cap=cap)
+    hk, hv = _held(hist[0], kv, ks), _held(hist[1], kv, ks)
+    for b, m in ((0, n), (1, 0)):
+        sl = slice(b * c, b * c + c)
+        ref = attend(q[sl].double(), torch.cat([hk[:m], k[sl].double()]), torch.cat([hv[:m], v[sl].double()]),
+                     range(m, m + c), pt, cap)
+        check(out[sl], lse[sl], ref, 2.0 ** -8, 0.0, "prefill %d" % b, cap)
+    cache.append_kv(0, [0, 1], [0, c, 2 * c], k, v)
+    qd = q[[c - 1, 2 * c - 1]].contiguous()
+    out, lse = cache.decode(0, [0, 1], qd, score_cap=cap)
+    for b, m in ((0, n), (1, 0)):
+        sl = slice(b * c, b * c + c)
+        kk = torch.cat([hk[:m], _held(k[sl], kv, ks)])
+        vv = torch.cat([hv[:m], _held(v[sl], kv, ks)])
+        ref = attend(qd[b:b + 1].double(), kk, vv, [m + c - 1], pt, cap)
+        # q * scale is exact in f16 (a power of two), so scores carry no rounding
+        check(out[b:b + 1], lse[b:b + 1], ref, 2.0 ** -8 if kv == "bf16" else 2.0 ** -11, 0.0, "decode %d" % b, cap)
+    assert cache.status() == 0
+
+
+def test_long_split_items():
+    """A chunk of two row blocks over a long history: items in pieces, merged."""
+    gpu_ready()
+    hq, hkv, d, P, n, c, cap = 4, 2, 128, 64, 20000, 140, 30.0
+    cache = _mk(hq, hkv, d, P, 1, n + c, 2 * hkv * ((n + c) // P + 4))
+    pols = [W.HeadPolicy(G), W.HeadPolicy(L, 4, 9000)]
+    cache.set_policy(0, to_c_policies([pols]))
+    hist = [W.normal((n, hkv, d), 5 + i, device="cuda") for i in range(2)]
+    cache.build(0, 0, *hist)
+    q = (W.normal((c, hq, d), 7, device="cuda").float() * 8).to(torch.bfloat16)
+    k, v = W.normal((c, hkv, d), 8, device="cuda"), W.normal((c, hkv, d), 9, device="cuda")
+    out, lse = cache.prefill(0, [0], [0, c], q, k, v, score_cap=cap)
+    rows = [0, 1, 77, 127, 128, c - 1]
+    ref = attend(q[rows].double(), torch.cat([hist[0], k]).double(), torch.cat([hist[1], v]).double(),
+                 [n + r for r in rows], [pol_tuple(p) for p in pols], cap)
+    check(out[rows], lse[rows], ref, 2.0 ** -8, 0.0, "split", cap)
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("cap", [1.0 / 64, 1.0, 50.0, 64.0])
+def test_extreme_scores(cap):
+    """Scores of +-1e30 and rows all at -cap: weights at the ends of the
+    exponentials' range, equal where every score sits on the cap."""
+    gpu_ready()
+    d, n = 64, 200
+    cache = _mk(1, 1, d, 16, 1, n, 20)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = torch.full((n, 1, d), 1e15, dtype=torch.bfloat16, device="cuda")
+    k[1::2] *= -1
+    q = torch.full((n, 1, d), 1e15, dtype=torch.bfloat16, device="cuda")
+    q[100:] *= -1
+    k[:, :, 1:], q[:, :, 1:] = 0, 0
+    v = W.normal((n, 1, d), 3, device="cuda")
+    out, lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)
+    ref = attend(q.double(), k.double(), v.double(), range(n), [(G, 0, 0, None)], cap)
+    ref = ref[:3] + (torch.zeros_like(ref[3]), ref[4])         # every score is +-cap, exactly
+    check(out, lse, ref, 2.0 ** -8, 0.0, "prefill", cap)
+    low = torch.full_like(k, -1e15)                             # every score at -cap
+    low[:, :, 1:] = 0
+    q[:] = q[:1].abs()
+    out, lse = cache.prefill(0, [0], [0, n], q, low, v, score_cap=cap)
+    ref = attend(q.double(), low.double(), v.double(), range(n), [(G, 0, 0, None)], cap)
+    check(out, lse, ref[:3] + (torch.zeros_like(ref[3]), ref[4]), 2.0 ** -8, 0.0, "all low", cap)
+    cache.append_kv(0, [0], [0, n], low, v)
+    out, lse = cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
+    mean = v.double().mean(0, keepdim=True)
+    assert ((out.double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -8 * v.double().abs().mean(0)).all()
+    assert abs(lse.item() - (math.log(n) - cap)) <= 2.0 ** -18 * (1 + cap) + 3e-7 * cap
+    assert cache.status() == 0
+
+
+def test_uncapped_calls_keep_their_results_and_refusals():
+    gpu_ready()
+    from head_aware_paged_gb300 import SegPagedError
+    cache = _mk(4, 2, 64, 16, 1, 128, 40)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)] * 2]))
+    q, k, v = (W.normal((50, h, 64), 1 + h, device="cuda") for h in (4, 2, 2))
+    a = cache.prefill(0, [0], [0, 50], q, k, v)
+    cache.prefill(0, [0], [0, 50], q, k, v, score_cap=5.0)
+    b = cache.prefill(0, [0], [0, 50], q, k, v)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    cache.append_kv(0, [0], [0, 50], k, v)
+    for cap in (0.0, -1.0, 1.0 / 65, 64.5, math.inf, math.nan):
+        with pytest.raises(SegPagedError):
+            cache.prefill(0, [0], [0, 50], q, k, v, score_cap=cap)
+        with pytest.raises(SegPagedError):
+            cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
+    assert cache.status() == 0
