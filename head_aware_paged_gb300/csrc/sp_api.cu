@@ -483,6 +483,7 @@ sp_status sp_cache_create(const sp_config* cfg, void* pool, void* meta, void* ws
     c->h_policy_set.assign(cfg->max_seqs, 0);
     c->h_seqlen.assign((size_t)cfg->max_seqs * cfg->num_layers, 0);
     c->h_npages.assign(units, 0);
+    c->h_scaled.assign(cfg->num_layers, 0);
     c->h_free = cfg->num_pages;
     *out = c;
     return SP_OK;
@@ -650,6 +651,7 @@ static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq
     p->item_off[0] = 0;
     int64_t total = 0;
     p->cap = cap;
+    p->scaled = c->h_scaled[layer];
     const int P = c->cfg.page_size, slots = decode_item_slots(c->geo);
     for (int b = 0; b < n_seqs; ++b) {
         const int seq = seq_ids[b];
@@ -765,6 +767,7 @@ sp_status sp_set_kv_scales(sp_cache* c, int32_t layer, const float* k_scale, con
     if (e == cudaSuccess) e = cudaMemcpyAsync(c->meta.vinv + off, vi.data(), n * 4, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "scale upload");
+    c->h_scaled[layer] = 1;
     return SP_OK;
 }
 

@@ -41,8 +41,6 @@ namespace {
 
 constexpr int kD4Warps = 8;
 constexpr int kD4Threads = kD4Warps * 32;
-constexpr int kD4Depth = 1;                          // stages of a warp
-constexpr int kD4Stages = kD4Warps * kD4Depth;
 constexpr int kD4TileBytes = kFp4ItemSlots * kFp4RowBytes;
 constexpr int kD4StageBytes = 2 * kD4TileBytes;      // K, then V
 constexpr int kD4Dim = 128;
@@ -54,10 +52,15 @@ constexpr float kRefBelow = 7.f, kRefAbove = 15.f;
 // i, heads 132 floats apart (a half warp's 8-byte stores then meet no bank twice).
 constexpr int kD4HeadFloats = 132;
 __device__ __forceinline__ int d4_dim(int at) { return ((at >> 1) & 7) * 16 + (at >> 4) * 2 + (at & 1); }
-static_assert(16 * kD4HeadFloats * 4 <= kD4Depth * kD4StageBytes, "16 heads fit a warp's stages");
+static_assert(16 * kD4HeadFloats * 4 <= kD4StageBytes, "16 heads fit a warp's stages");
 constexpr int kD4Groups = kFp4ItemSlots / kFp4Group;
 static_assert(kD4Groups == 4, "an item is four groups of 16 slots");
 
+// CTA whose share of the items holds item x.
+__device__ __forceinline__ int cta_of(const DecodeParams& p, int32_t x) {
+    const int32_t more = p.rem * (p.per + 1);        // items of the CTAs that take one more
+    return x < more ? x / (p.per + 1) : p.rem + (x - more) / p.per;
+}
 // Transpose of an 8x8 f16 matrix held as one pair a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
@@ -142,24 +145,26 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
           const uint8_t* __restrict__ vpool) {
     constexpr int D = kD4Dim;
     extern __shared__ __align__(128) uint8_t smem_raw[];
+    const Geo& g = p.geo;
+    const int group = g.group;
     uint8_t* stages = smem_raw;
     // A warp's first and last partials are entries 2 w and 2 w + 1: (m, l) and
     // unit here, outputs in its slot and in its stages.
-    float* slots = reinterpret_cast<float*>(stages + kD4Stages * kD4StageBytes);     // [warps][group][kD4HeadFloats]
+    float* slots = reinterpret_cast<float*>(stages + kD4Warps * kD4StageBytes);     // [warps][group][kD4HeadFloats]
     float2* entry_ml = reinterpret_cast<float2*>(slots + p.merge_floats);           // [2 warps][group]
-    __shared__ uint64_t full[2 * kD4Stages];         // K and V of each stage landed
-    __shared__ int abort_word, flag_last[2], entry_unit[2 * kD4Warps];
+    float2* unit_ml = entry_ml + 2 * kD4Warps * group;                              // [2 warps][group]
+    float* entry_weight = reinterpret_cast<float*>(unit_ml + 2 * kD4Warps * group); // [2 warps][group]
+    __shared__ uint64_t full[2 * kD4Warps];          // K and V of each warp's stage landed
+    __shared__ int abort_word, flag_last[2], entry_unit[2 * kD4Warps], list[2 * kD4Warps], n_list;
     volatile int* abort_flag = &abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, c = blockIdx.x;
-    const int64_t T = p.total_items;
-    const int64_t x0 = T * c / G, x1 = T * (c + 1) / G;
-    const Geo& g = p.geo;
-    const int group = g.group;
+    // CTA c takes p.per items, one more if c < p.rem (per >= 1)
+    const int32_t x0 = c * p.per + min(c, p.rem), x1 = x0 + p.per + (c < p.rem ? 1 : 0);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2 * kD4Stages; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < 2 * kD4Warps; ++s) mbar_init(&full[s], 1);
         for (int e = 0; e < 2 * kD4Warps; ++e) entry_unit[e] = -1;
         abort_word = 0;
         fence_mbar_init();
@@ -178,15 +183,14 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
             if (col == 0 && p.lse) p.lse[(int64_t)b * g.hq + h * group + r] = -INFINITY;
         }
     }
-    if (x0 >= x1) return;
+    if (p.total_items == 0) return;
 
     // This warp's items [wx0, wx1) of the CTA's.  The lanes hold 32 of them,
     // [batch, batch + 32).
-    const int32_t wx0 = (int32_t)(x0 + (x1 - x0) * warp / kD4Warps);
-    const int32_t wx1 = (int32_t)(x0 + (x1 - x0) * (warp + 1) / kD4Warps);
+    const int32_t wx0 = x0 + (x1 - x0) * warp / kD4Warps, wx1 = x0 + (x1 - x0) * (warp + 1) / kD4Warps;
     const int mine = wx1 - wx0;
-    uint8_t* my_stages = stages + warp * kD4Depth * kD4StageBytes;
-    uint64_t* my_full = full + warp * kD4Depth * 2;
+    uint8_t* my_stages = stages + warp * kD4StageBytes;
+    uint64_t* my_full = full + warp * 2;
     int u_first = 0;                                 // first unit with an item >= wx0
     for (int u_hi = p.n_units - 1; u_first < u_hi;) {
         const int mid = (u_first + u_hi) >> 1;
@@ -236,9 +240,25 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
         for (int k = 0; k < kD4Groups; ++k)
             bulk_load(dst + k * kFp4GroupBytes, pool + (int64_t)next.g[k] * kFp4GroupBytes, kFp4GroupBytes, bar);
     };
-    if (mine > 0) { take(0); load(0); load(1); }
-
     const int gl = lane >> 2, j = lane & 3;          // fragment row, column pair
+    // raw query words of a unit's heads; the first unit's travel while the
+    // first item is looked up
+    uint32_t qraw[NH][8][2];
+    auto load_q = [&](int u) {
+        const int b = u / g.hkv, h = u - b * g.hkv;
+        #pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const int head = nh * 8 + gl;
+            const __nv_bfloat16* qr = p.q + ((int64_t)b * g.hq + h * group + head) * D + j * 32;
+            #pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                #pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    qraw[nh][kk][e] = head < group ? *reinterpret_cast<const uint32_t*>(qr + kk * 4 + 2 * e) : 0u;
+        }
+    };
+    if (mine > 0) { load_q(u_first); take(0); load(0); load(1); }
+
     // slots of this lane's rows of S^T in a group (positions gl and gl + 8)
     const int slot_a = (gl >> 1) + 4 * (gl & 1), slot_b = slot_a + 8;
     uint32_t qb[NH][8][2];
@@ -252,20 +272,21 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
         const int b = u / g.hkv, h = u - b * g.hkv;
         const float* ks = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
         const float* vs = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
+        if (it > 0) load_q(u);
         #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
-            const int head = nh * 8 + gl;
-            const __nv_bfloat16* qr = p.q + ((int64_t)b * g.hq + h * group + head) * D + j * 32;
             #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
                 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int cc = kk * 4 + 2 * e;
-                    uint32_t w = 0;
-                    if (head < group) w = *reinterpret_cast<const uint32_t*>(qr + cc);
-                    const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
-                    qb[nh][kk][e] = pack_f16(__low2float(v2) * __ldg(ks + j * 32 + cc),
-                                             __high2float(v2) * __ldg(ks + j * 32 + cc + 1));
+                    const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(&qraw[nh][kk][e]);
+                    float q0 = __low2float(v2), q1 = __high2float(v2);
+                    if (p.scaled) {
+                        const int cc = j * 32 + kk * 4 + 2 * e;
+                        q0 *= __ldg(ks + cc);
+                        q1 *= __ldg(ks + cc + 1);
+                    }
+                    qb[nh][kk][e] = pack_f16(q0, q1);
                 }
             m_run[nh][0] = m_run[nh][1] = -INFINITY;
             l_run[nh][0] = l_run[nh][1] = 0.f;
@@ -434,6 +455,17 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
         // The unit's sums of this run: the result itself if the run holds the
         // whole unit, else a partial, in this warp's slot (the run goes on) or
         // in its stages (it ends here, and nothing is in flight).
+        if (p.scaled) {
+            #pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                const float v0 = __ldg(vs + gl * 16 + 2 * mt), v1 = __ldg(vs + gl * 16 + 2 * mt + 1);
+                #pragma unroll
+                for (int nh = 0; nh < NH; ++nh) {
+                    o[nh][mt][0] *= v0; o[nh][mt][1] *= v0;
+                    o[nh][mt][2] *= v1; o[nh][mt][3] *= v1;
+                }
+            }
+        }
         const bool complete = u_begin >= wx0 && u_end <= wx1;
         const int entry = 2 * warp + (it < mine ? 0 : 1);
         float* po = it < mine ? slots + warp * group * kD4HeadFloats : reinterpret_cast<float*>(my_stages);
@@ -454,15 +486,13 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                     uint32_t* out = reinterpret_cast<uint32_t*>(p.out + orow * D + gl * 16);
                     #pragma unroll
                     for (int mt = 0; mt < 8; ++mt)
-                        out[mt] = pack_bf16(o[nh][mt][e] * __ldg(vs + gl * 16 + 2 * mt) * inv,
-                                            o[nh][mt][2 + e] * __ldg(vs + gl * 16 + 2 * mt + 1) * inv);
+                        out[mt] = pack_bf16(o[nh][mt][e] * inv, o[nh][mt][2 + e] * inv);
                     if (gl == 0 && p.lse) p.lse[orow] = (m_run[nh][e] + __log2f(l)) * 0.69314718055994531f;
                 } else {
                     #pragma unroll
                     for (int mt = 0; mt < 8; ++mt)
                         *reinterpret_cast<float2*>(po + head * kD4HeadFloats + mt * 16 + gl * 2) =
-                            make_float2(o[nh][mt][e] * __ldg(vs + gl * 16 + 2 * mt),
-                                        o[nh][mt][2 + e] * __ldg(vs + gl * 16 + 2 * mt + 1));
+                            make_float2(o[nh][mt][e], o[nh][mt][2 + e]);
                     if (gl == 0) entry_ml[entry * group + head] = make_float2(m_run[nh][e], l);
                 }
             }
@@ -470,41 +500,59 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
     __syncthreads();
 
     // ------------- merge the partials of the CTA, unit by unit -------------
+    // The entries in use, in order (units ascend), and every entry's weight
+    // 2^(m - m*) in its unit's sum; a unit's (m*, l*) go to all its entries.
+    if (warp == 0) {
+        const int u = lane < 2 * kD4Warps ? entry_unit[lane] : -1;
+        const uint32_t used = __ballot_sync(0xffffffffu, u >= 0);
+        if (u >= 0) list[__popc(used & ((1u << lane) - 1u))] = lane;
+        if (lane == 0) n_list = __popc(used);
+    }
+    for (int e = ctid; e < 2 * kD4Warps * group; e += CT) {
+        const int w = e / group, r = e - w * group, u = entry_unit[w];
+        if (u < 0) continue;
+        float mst = -INFINITY, lst = 0.f;
+        #pragma unroll
+        for (int x = 0; x < 2 * kD4Warps; ++x)
+            mst = fmaxf(mst, entry_unit[x] == u ? entry_ml[x * group + r].x : -INFINITY);
+        const float ref = mst == -INFINITY ? 0.f : mst;
+        #pragma unroll
+        for (int x = 0; x < 2 * kD4Warps; ++x)
+            lst += entry_unit[x] == u ? fast_exp2(entry_ml[x * group + r].x - ref) * entry_ml[x * group + r].y : 0.f;
+        entry_weight[e] = fast_exp2(entry_ml[e].x - ref);
+        unit_ml[e] = make_float2(mst, lst);
+    }
+    __syncthreads();
     // Thread e holds output (head e / 128, place e % 128 of the slots' order).
     int split_unit[2] = {-1, -1};                    // units that other CTAs share
-    for (int i = 0; i < 2 * kD4Warps;) {
-        const int u = entry_unit[i];
-        if (u < 0) { ++i; continue; }
+    for (int i = 0; i < n_list;) {
+        const int u = entry_unit[list[i]];
         int k = i + 1;
-        while (k < 2 * kD4Warps && (entry_unit[k] < 0 || entry_unit[k] == u)) ++k;
+        while (k < n_list && entry_unit[list[k]] == u) ++k;
         const int b = u / g.hkv, h = u - b * g.hkv;
         const bool whole = p.item_off[u] >= x0 && p.item_off[u + 1] <= x1;
         if (!whole) split_unit[split_unit[0] < 0 ? 0 : 1] = u;
         for (int e = ctid; e < group * D; e += CT) {
             const int r = e / D, at = e % D;
-            float mst = -INFINITY;
-            for (int w = i; w < k; ++w)
-                if (entry_unit[w] == u) mst = fmaxf(mst, entry_ml[w * group + r].x);
-            float lst = 0.f, ost = 0.f;
-            for (int w = i; w < k; ++w) {
-                if (entry_unit[w] != u) continue;
-                const float2 ml = entry_ml[w * group + r];
-                const float* po = (w & 1) ? reinterpret_cast<const float*>(stages + (w >> 1) * kD4Depth * kD4StageBytes)
+            float ost = 0.f;
+            #pragma unroll 4
+            for (int y = i; y < k; ++y) {
+                const int w = list[y];
+                const float* po = (w & 1) ? reinterpret_cast<const float*>(stages + (w >> 1) * kD4StageBytes)
                                           : slots + (w >> 1) * group * kD4HeadFloats;
-                const float f = fast_exp2(ml.x - (mst == -INFINITY ? 0.f : mst));
-                lst += f * ml.y;
-                ost += f * po[r * kD4HeadFloats + at];
+                ost += entry_weight[w * group + r] * po[r * kD4HeadFloats + at];
             }
+            const float2 ml = unit_ml[list[i] * group + r];
             if (whole) {
                 const int64_t orow = (int64_t)b * g.hq + h * group + r;
-                p.out[orow * D + d4_dim(at)] = __float2bfloat16(ost / lst);
-                if (at == 0 && p.lse) p.lse[orow] = (mst + __log2f(lst)) * 0.69314718055994531f;
+                p.out[orow * D + d4_dim(at)] = __float2bfloat16(ost / ml.y);
+                if (at == 0 && p.lse) p.lse[orow] = (ml.x + __log2f(ml.y)) * 0.69314718055994531f;
             } else {
                 const int64_t part = (int64_t)u + c;
                 p.part_o[(part * group + r) * D + at] = ost;
                 if (at == 0) {
-                    p.part_ml[(part * group + r) * 2] = mst;
-                    p.part_ml[(part * group + r) * 2 + 1] = lst;
+                    p.part_ml[(part * group + r) * 2] = ml.x;
+                    p.part_ml[(part * group + r) * 2 + 1] = ml.y;
                 }
             }
         }
@@ -514,9 +562,9 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
     __threadfence();
     __syncthreads();
     if (ctid < 2 && split_unit[ctid] >= 0) {
-        // every CTA of the grid holds an item, so a unit's CTAs are c_first .. c_last
+        // every CTA of the grid holds an item, so a unit's CTAs are neighbours
         const int u = split_unit[ctid];
-        const int n = (int)cta_of_item(p.item_off[u + 1] - 1, T, G) - (int)cta_of_item(p.item_off[u], T, G) + 1;
+        const int n = cta_of(p, p.item_off[u + 1] - 1) - cta_of(p, p.item_off[u]) + 1;
         flag_last[ctid] = atomicAdd(&p.counters[u], 1) == n - 1;
     }
     __syncthreads();
@@ -527,8 +575,8 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
         __threadfence();
         const int u = split_unit[q];
         const int b = u / g.hkv, h = u - b * g.hkv;
-        const int c_first = (int)cta_of_item(p.item_off[u], T, G);
-        const int nseg = (int)cta_of_item(p.item_off[u + 1] - 1, T, G) - c_first + 1;
+        const int c_first = cta_of(p, p.item_off[u]);
+        const int nseg = cta_of(p, p.item_off[u + 1] - 1) - c_first + 1;
         float* wts = slots;                            // [nseg][group] weights
         float* mls = slots + p.merge_floats / 2;       // [nseg][group] l
         for (int e = ctid; e < nseg * group; e += CT) {
@@ -547,7 +595,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                 wts[sg * group + r] = w;
                 lst += w * mls[sg * group + r];
             }
-            entry_ml[r] = make_float2(mst, lst);
+            unit_ml[r] = make_float2(mst, lst);
         }
         __syncthreads();
         for (int e = ctid; e < group * D; e += CT) {
@@ -565,7 +613,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
             }
             for (; sg < nseg; ++sg) acc[0] += wts[sg * group + r] * __ldcg(po + sg * step);
             const float ost = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            const float2 ml = entry_ml[r];
+            const float2 ml = unit_ml[r];
             const int64_t orow = (int64_t)b * g.hq + h * group + r;
             p.out[orow * D + d4_dim(at)] = __float2bfloat16(ost / ml.y);
             if (at == 0 && p.lse) p.lse[orow] = (ml.x + __log2f(ml.y)) * 0.69314718055994531f;
@@ -583,8 +631,10 @@ cudaError_t launch_decode4_t(const sp_cache* c, DecodeParams& p, int grid, cudaS
     const int group = c->geo.group;
     const int mo = std::max(kD4Warps * group * kD4HeadFloats, 2 * grid * group);
     p.merge_floats = (mo + 3) & ~3;
-    const int merge_bytes = (p.merge_floats + 2 * kD4Warps * group * 2) * 4;
-    const int smem = kD4Stages * kD4StageBytes + merge_bytes;
+    const int merge_bytes = (p.merge_floats + 2 * kD4Warps * group * 5) * 4;
+    p.per = (int32_t)(p.total_items / grid);
+    p.rem = (int32_t)(p.total_items % grid);
+    const int smem = kD4Warps * kD4StageBytes + merge_bytes;
     if (smem > kCap) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap);
     if (e == cudaSuccess && NH == 1)

@@ -96,6 +96,7 @@ extern "C" sp_status sp_attention_decode_static_scratch(sp_cache* c, int32_t lay
     p.item_off[0] = 0;
     int64_t total = 0;
     p.cap = Cap{};
+    p.scaled = c->h_scaled[layer];
     const int P = c->cfg.page_size, slots = decode_item_slots(c->geo);
     for (int b = 0; b < n_seqs; ++b) {
         const int seq = seq_ids[b];

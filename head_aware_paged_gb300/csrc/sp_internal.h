@@ -95,6 +95,8 @@ struct DecodeParams {
     int32_t* counters;           // [n_units], zero between calls
     float scale_log2;            // log2(e) / sqrt(d)
     Cap cap;                     // capped scores (cap.on = 0: as they are)
+    int32_t scaled;              // 4-bit pages: channel scales other than 1 may be set
+    int32_t per, rem;            // 4-bit pages: items of a CTA, CTAs that take one more (launcher)
     int32_t nst;                 // pipeline stages (set by the launcher)
     int32_t owners;              // consumer warps that own stages (divides nst)
     int32_t merge_floats;        // merge buffer floats (set by the launcher)
@@ -180,6 +182,7 @@ struct sp_cache {
     std::vector<uint8_t> h_policy_set;           // per sequence
     std::vector<int32_t> h_seqlen;               // [max_seqs][layers]
     std::vector<int32_t> h_npages;               // [max_seqs][layers][hkv]
+    std::vector<uint8_t> h_scaled;               // [layers]: sp_set_kv_scales was called
     int64_t h_free = 0;
     // Pinned host staging for the per-call prefill work list, so its upload is
     // an asynchronous copy and the host never waits for the device.  A ring:
