@@ -83,20 +83,30 @@ __device__ __forceinline__ void fp4_word_f16(uint32_t w, uint32_t& p0, uint32_t&
         : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3) : "r"(w));
 }
 
-// A block of 16 values: its 8 code bytes and its scale code.  The quotient is
-// a true division: x * fl(1 / s) misses ties between two e2m1 values (a scale
-// mantissa of 13/8 at 1.75, for one).
-__device__ __forceinline__ uint2 fp4_quant16(const float (&x)[16], uint32_t& scale_code) {
+// A block of 16 values: its 8 code bytes and its scale code.  x / s is x times
+// the rounded reciprocal, corrected once by its residual x - y s (iterative
+// refinement): the uncorrected product misses ties between two e2m1 values (a
+// scale mantissa of 13/8 at 1.75, for one), the corrected one is exact there.
+__device__ __forceinline__ uint2 fp4_quant16(float (&x)[16], uint32_t& scale_code) {
     float amax = 0.f;
     #pragma unroll
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
     scale_code = fp4_scale_code(amax);
     if (scale_code == 0) return make_uint2(0u, 0u);   // largest value below half the least scale
-    const float s = fp4_scale_value(scale_code);
+    if (amax > 1e30f) {                               // an infinity has no residual: far past 6 s will do
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = fabsf(x[i]) > 1e30f ? copysignf(1e30f, x[i]) : x[i];
+    }
+    const float s = fp4_scale_value(scale_code), inv = __frcp_rn(s);
+    float y[16];
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float q = x[i] * inv;
+        y[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), inv, q);
+    }
     uint32_t w[2] = {0u, 0u};
     #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= fp4_pair_code(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= fp4_pair_code(y[2 * i], y[2 * i + 1]) << (8 * (i & 3));
     return make_uint2(w[0], w[1]);
 }
 // ... and back: code * scale of the 16 elements.

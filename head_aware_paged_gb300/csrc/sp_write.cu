@@ -13,7 +13,10 @@
 // per token and pair serves every head.
 //
 // Bound by memory: 4 bytes a q element, 2 + the page type's size a stored
-// k / v element; a token that a head does not keep is not read.  A thread
+// k / v element; a token that a head does not keep is not read.  Measured,
+// 8,192 rows of 32 query and 8 KV heads: 33.5 us for every head GLOBAL (201 MB,
+// 6.0 TB/s, 88 % of the copy rate), 29.1 us for one of eight (150 MB); FP8 and
+// 4-bit pages 38.2 and 39.7 us.  64 rows of 64 sequences: 3.9 us.  A thread
 // rotates one chunk of 8 dimensions and its partner chunk (16-byte loads and
 // stores; a whole block of 16 for 4-bit pages, whose scale needs its maximum).
 //
@@ -34,6 +37,7 @@ namespace sp {
 namespace {
 
 constexpr int kWriteThreads = 256;
+constexpr int kMaxTok = 4;                  // tokens of a block, at most
 
 // MAXS sequences and MAXU (sequence, KV head) units: a call's parameters are
 // copied at launch, so a small call uses the small record.
@@ -43,6 +47,7 @@ struct WriteParams {
     Geo geo;
     int32_t layer, n_seqs, rows, top;      // top: free-stack height before the call
     int32_t row_blocks, tok, new_pages;    // blocks that write rows, tokens of each; any new page or length?
+    int32_t scaled;                        // channel scales other than 1 may be set
     int64_t q_stride, k_stride, v_stride;  // elements between tokens
     const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16* q_out;
@@ -51,8 +56,6 @@ struct WriteParams {
     int32_t seq[MAXS], n_old[MAXS], n_new[MAXS], pos[MAXS], row0[MAXS + 1];
     int32_t off[MAXU + 1];                 // prefix of the units' new pages
 };
-
-struct Rows16 { uint4 a, b; };             // a chunk and its partner chunk
 
 // Eight elements of each half, rotated; fp32.
 __device__ __forceinline__ void rotate8(const uint4& xa, const uint4& yb, const float2* cs, float* x,
@@ -82,14 +85,22 @@ __device__ __forceinline__ void plain8(const uint4& a, float* x) {
 __device__ __forceinline__ uint4 bf16x8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
-// e4m3(x * inv) of eight elements (fp32 product, nearest even, saturating).
-__device__ __forceinline__ uint2 e4m3x8(const float* x, const float* inv) {
+// N elements times their channels' reciprocal scales.
+template <int N>
+__device__ __forceinline__ void times(float* x, const float* inv) {
+    #pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(inv + i));
+        x[i] *= f.x; x[i + 1] *= f.y; x[i + 2] *= f.z; x[i + 3] *= f.w;
+    }
+}
+// e4m3 of eight elements (nearest even, saturating).
+__device__ __forceinline__ uint2 e4m3x8(const float* x) {
     uint32_t o[2] = {0u, 0u};
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
         uint16_t code;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-            : "=h"(code) : "f"(x[2 * e + 1] * __ldg(inv + 2 * e + 1)), "f"(x[2 * e] * __ldg(inv + 2 * e)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(x[2 * e + 1]), "f"(x[2 * e]));
         o[e >> 1] |= (uint32_t)code << (16 * (e & 1));
     }
     return make_uint2(o[0], o[1]);
@@ -97,23 +108,39 @@ __device__ __forceinline__ uint2 e4m3x8(const float* x, const float* inv) {
 
 enum { kBf16, kFp8, kFp4 };
 
+// Pages a unit of n tokens owns (unit_pages of sp_rules.h in 32 bits, P = 2^lp).
+__device__ __forceinline__ int32_t pages32(const UnitPol& u, const int32_t* idx, int32_t n, int lp) {
+    const int32_t up = (1 << lp) - 1;
+    if (u.kind == kGlobal) return (n + up) >> lp;
+    if (u.kind == kLocal)
+        return ((min(n, u.sink) + up) >> lp) + min(u.ring, (max(0, n - u.sink) + up) >> lp);
+    return ((int32_t)count_below(idx, u.n_idx, n) + up) >> lp;
+}
+
 // Where a token's row of one KV head goes: false if the head does not keep it.
 struct RowAt { int32_t page; int32_t slot; };
 template <typename PR>
 __device__ __forceinline__ bool row_at(const PR& p, int b, int h, int32_t t, RowAt& at) {
     const Geo& g = p.geo;
+    const int lp = 31 - __clz(g.page);
     const int64_t row = g.unit_row(p.seq[b], p.layer, h);
     const UnitPol pol = p.meta.pol[row];
     const int32_t* idx = p.meta.idx + (int64_t)p.seq[b] * g.max_idx_per_seq + pol.idx_off;
-    if (pol.kind == kLocal && t >= pol.sink && (int64_t)t < (int64_t)p.n_new[b] - (int64_t)pol.ring * g.page)
-        return false;                                  // a newer token of the call takes its slot
-    const int64_t us = unit_slot(pol, idx, t, g.page);
-    if (us < 0) return false;
-    const int32_t pg = (int32_t)(us / g.page);
-    const int32_t have = (int32_t)unit_pages(pol, idx, p.n_old[b], g.page);
+    int32_t us = t;                                     // unit slot (unit_slot of sp_rules.h)
+    if (pol.kind == kLocal && t >= pol.sink) {
+        const int32_t ring = pol.ring << lp;
+        if (t < p.n_new[b] - ring) return false;        // a newer token of the call takes its slot
+        us = (pol.sink_pages << lp) + (int32_t)((uint32_t)(t - pol.sink) % (uint32_t)ring);
+    } else if (pol.kind == kRetrieval) {
+        us = (int32_t)count_below(idx, pol.n_idx, t);
+        if (us >= pol.n_idx || idx[us] != t) return false;
+    }
+    const int32_t pg = us >> lp;
+    // old pages are in the table; new ones come from the stack
+    const int32_t have = p.new_pages ? pages32(pol, idx, p.n_old[b], lp) : pg + 1;
     at.page = pg < have ? p.meta.ptab[row * g.max_pages_unit + pg]
                         : p.meta.fstack[p.top - 1 - (p.off[b * g.hkv + h] + pg - have)];
-    at.slot = (int32_t)(us - (int64_t)pg * g.page);
+    at.slot = us & (g.page - 1);
     if (at.page < 0 || at.page >= g.num_pages) {
         atomicOr(p.meta.status, kStatusBadPage);
         return false;
@@ -136,7 +163,7 @@ k_write_rope(const __grid_constant__ PR p) {
             const int64_t row = g.unit_row(p.seq[b], p.layer, h);
             const UnitPol pol = p.meta.pol[row];
             const int32_t* idx = p.meta.idx + (int64_t)p.seq[b] * g.max_idx_per_seq + pol.idx_off;
-            const int32_t have = (int32_t)unit_pages(pol, idx, p.n_old[b], g.page);
+            const int32_t have = pages32(pol, idx, p.n_old[b], 31 - __clz(g.page));
             const int32_t off = p.off[u], cnt = p.off[u + 1] - off;
             if (have + cnt > g.max_pages_unit || off + cnt > p.top) {      // the host checked; never expected
                 if (lane == 0) atomicOr(p.meta.status, kStatusBadState);
@@ -151,10 +178,30 @@ k_write_rope(const __grid_constant__ PR p) {
         return;
     }
     constexpr int CH = KV == kFp4 ? 16 : 8;              // k / v dimensions of a chunk
-    __shared__ float2 cs[4 * 64];
-    __shared__ int32_t tok_b[4], tok_t[4];
+    __shared__ float2 cs[kMaxTok * 64];
+    __shared__ int32_t tok_b[kMaxTok], tok_t[kMaxTok];
     const int D = g.d, half = D / 2;
     const int r0 = (int)blockIdx.x * p.tok, nt = min(p.tok, p.rows - r0);
+    // queries: two chunk pairs a pass (four 16-byte loads in flight a thread),
+    // the first pass's loads ahead of the angles
+    const int stride = kWriteThreads * gridDim.y, first = blockIdx.y * kWriteThreads + tid;
+    const int lq = 28 - __clz(half), q_row = g.hq << lq, q_all = p.q ? nt * q_row : 0;   // half / 8 = 2^lq chunks a head
+    uint4 qa[2], qb[2];
+    int qt[2], qat[2];                                   // token, element inside its row
+    auto fetch = [&](int e0) {
+        #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = e0 + k * stride;
+            if (e >= q_all) break;
+            qt[k] = e / q_row;
+            const int w = e - qt[k] * q_row;
+            qat[k] = (w >> lq) * D + (w & ((1 << lq) - 1)) * 8;
+            const __nv_bfloat16* src = p.q + (int64_t)(r0 + qt[k]) * p.q_stride + qat[k];
+            qa[k] = *reinterpret_cast<const uint4*>(src);
+            qb[k] = *reinterpret_cast<const uint4*>(src + half);
+        }
+    };
+    fetch(first);
     if (tid < nt) {
         int a = 0, z = p.n_seqs - 1;                     // sequence with row0[b] <= row < row0[b + 1]
         while (a < z) {
@@ -172,17 +219,14 @@ k_write_rope(const __grid_constant__ PR p) {
         sincospif(x, &cs[e].y, &cs[e].x);
     }
     __syncthreads();
-    const int stride = kWriteThreads * gridDim.y, first = blockIdx.y * kWriteThreads + tid;
-    if (p.q) {
-        const int qc = half / 8, per = g.hq * qc;
-        for (int e = first; e < nt * per; e += stride) {
-            const int t = e / per, h = (e - t * per) / qc, c = (e - t * per) % qc;
-            const __nv_bfloat16* src = p.q + (int64_t)(r0 + t) * p.q_stride + h * D + c * 8;
-            const uint4 a = *reinterpret_cast<const uint4*>(src);
-            const uint4 b = *reinterpret_cast<const uint4*>(src + half);
+    for (int e0 = first; e0 < q_all; e0 += 2 * stride) {
+        if (e0 != first) fetch(e0);
+        #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (e0 + k * stride >= q_all) break;
             float x[8], y[8];
-            rotate8(a, b, cs + t * half + c * 8, x, y);
-            __nv_bfloat16* dst = p.q_out + ((int64_t)(r0 + t) * g.hq + h) * D + c * 8;
+            rotate8(qa[k], qb[k], cs + qt[k] * half + (qat[k] & (D - 1)), x, y);
+            __nv_bfloat16* dst = p.q_out + (int64_t)(r0 + qt[k]) * g.hq * D + qat[k];
             *reinterpret_cast<uint4*>(dst) = bf16x8(x);
             *reinterpret_cast<uint4*>(dst + half) = bf16x8(y);
         }
@@ -211,10 +255,9 @@ k_write_rope(const __grid_constant__ PR p) {
             uint32_t sc;
             rotate8(ka[0], kb[0], ang, x, y);
             rotate8(ka[1], kb[1], ang + 8, x + 8, y + 8);
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] *= __ldg(p.meta.kinv + so + i);
-                y[i] *= __ldg(p.meta.kinv + so + half + i);
+            if (p.scaled) {
+                times<16>(x, p.meta.kinv + so);
+                times<16>(y, p.meta.kinv + so + half);
             }
             *reinterpret_cast<uint2*>(kg + fp4_k_code(s, c)) = fp4_quant16(x, sc);
             kg[fp4_k_scale(s, c)] = (uint8_t)sc;
@@ -224,10 +267,9 @@ k_write_rope(const __grid_constant__ PR p) {
             plain8(va[1], x + 8);
             plain8(vb[0], y);
             plain8(vb[1], y + 8);
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] *= __ldg(p.meta.vinv + so + i);
-                y[i] *= __ldg(p.meta.vinv + so + half + i);
+            if (p.scaled) {
+                times<16>(x, p.meta.vinv + so);
+                times<16>(y, p.meta.vinv + so + half);
             }
             *reinterpret_cast<uint2*>(vg + fp4_v_code(s, c)) = fp4_quant16(x, sc);
             vg[fp4_v_scale(s, c)] = (uint8_t)sc;
@@ -244,12 +286,20 @@ k_write_rope(const __grid_constant__ PR p) {
             if constexpr (KV == kFp8) {
                 uint8_t* kp = static_cast<uint8_t*>(p.kpool) + dst;
                 uint8_t* vp = static_cast<uint8_t*>(p.vpool) + dst;
-                *reinterpret_cast<uint2*>(kp) = e4m3x8(x, p.meta.kinv + so);
-                *reinterpret_cast<uint2*>(kp + half) = e4m3x8(y, p.meta.kinv + so + half);
+                if (p.scaled) {
+                    times<8>(x, p.meta.kinv + so);
+                    times<8>(y, p.meta.kinv + so + half);
+                }
+                *reinterpret_cast<uint2*>(kp) = e4m3x8(x);
+                *reinterpret_cast<uint2*>(kp + half) = e4m3x8(y);
                 plain8(va, x);
                 plain8(vb, y);
-                *reinterpret_cast<uint2*>(vp) = e4m3x8(x, p.meta.vinv + so);
-                *reinterpret_cast<uint2*>(vp + half) = e4m3x8(y, p.meta.vinv + so + half);
+                if (p.scaled) {
+                    times<8>(x, p.meta.vinv + so);
+                    times<8>(y, p.meta.vinv + so + half);
+                }
+                *reinterpret_cast<uint2*>(vp) = e4m3x8(x);
+                *reinterpret_cast<uint2*>(vp + half) = e4m3x8(y);
             } else {
                 __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(p.kpool) + dst;
                 __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(p.vpool) + dst;
@@ -311,13 +361,15 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     p.n_seqs = n_seqs;
     p.rows = rows;
     p.top = (int32_t)c->h_free;
+    p.scaled = c->h_scaled[layer];
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
     p.q = q; p.k = k; p.v = v; p.q_out = q_out;
     p.kpool = c->kpool; p.vpool = c->vpool;
     std::memcpy(p.turn, turn, sizeof(p.turn));
-    // Four tokens a block share its set-up once that still fills the GPU; a
-    // short call spreads one token's heads over two blocks instead.
-    p.tok = rows >= 8 * c->num_sms ? 4 : 1;
+    // Four tokens a block share its set-up once that still fills the GPU (8,192
+    // rows: 31.1 us with two, 29.1 with four, 34.5 with eight); a short call
+    // spreads one token's heads over two blocks instead.
+    p.tok = rows >= 4 * c->num_sms ? kMaxTok : 1;
     p.row_blocks = (rows + p.tok - 1) / p.tok;
     const int items = (q ? c->cfg.num_q_heads : H) * c->cfg.head_dim / 16;
     const int split = p.tok == 1 && rows < 2 * c->num_sms && items > kWriteThreads ? 2 : 1;
