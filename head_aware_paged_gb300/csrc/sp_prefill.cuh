@@ -763,22 +763,6 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                             vm[w] = b;
                         }
                     }
-                    // S row of this thread, all 128 columns at once (the softmax
-                    // warpgroups hold 208 registers a thread).  Columns at or past
-                    // nkeys were not written by this tile's MMA and hold stale
-                    // values; their visibility bits are 0, so the select below
-                    // turns them into -inf like any invisible key.  One code path
-                    // for every tile width keeps the loop small.
-                    uint32_t sr[128];
-                    tmem_ld128(tS, sr);
-                    const bool fast = !masked && kt.nkeys == 128;
-                    if (!fast) {
-                        // invisible or absent columns -> -inf, once (branch-free); capped
-                        // scores: 0, so that what an absent column holds decides nothing
-                        #pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            sr[c] = ((vm[c >> 5] >> (c & 31)) & 1u) ? sr[c] : CAP ? 0u : 0xff800000u;
-                    }
                     if constexpr (CAP) {
                         // A capped score lies in [-cap, cap], so the exponentials
                         // need no running maximum: they are taken against the fixed
@@ -791,70 +775,105 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // tanh: MUFU.RCP (and TANH, too coarse besides) issue at a
                         // quarter of EX2's rate here, 16 against 4 cycles a warp, so the
                         // reciprocal of 1 - 2 / (1 + e^2y) would cost more than all the
-                        // rest.  While every |y| of the warp's tile is at most 1/2 (scores
-                        // up to half the cap), tanh is an odd polynomial of degree 7
-                        // (1.3e-7 off at most), five FMA-pipe operations on raw scores.
-                        // Otherwise the tile's exponentials are taken again with the
-                        // formula, its reciprocal by Newton's iteration.
-                        uint64_t rsum2[4];
-                        uint32_t pk[16];
-                        // P of 16 columns: bf16 pairs and their sums
-                        auto put_half = [&](int c, float (&pv)[16], uint32_t* pk) {
+                        // rest (8K layer: 323 us).  While every |y| of the warp's tile is
+                        // at most 1/2 (scores up to half the cap), tanh is an odd
+                        // polynomial of degree 7 (1.3e-7 off at most), five FMA-pipe
+                        // operations on raw scores; otherwise the tile takes the formula,
+                        // its reciprocal by Newton's iteration.
+                        //
+                        // The row is read from TMEM 32 columns at a time, the next ones on
+                        // their way while these are worked on: once for the largest
+                        // |score|, once for P, which takes the place of columns already
+                        // read.  (All 128 in registers with every step unrolled: XXX us.)
+                        uint32_t ra[32], rb[32];
+                        // visibility bits of columns 32 w .. 32 w + 31
+                        auto bits = [&](int w) { return w < 2 ? (w ? vm[1] : vm[0]) : w == 2 ? vm[2] : vm[3]; };
+                        const bool fast = !masked && kt.nkeys == 128;
+                        float far[4] = {0.f, 0.f, 0.f, 0.f};      // largest |visible score|
+                        auto farthest = [&](uint32_t (&x)[32], int w) {
                             if (!fast) {
+                                const uint32_t b = bits(w);
                                 #pragma unroll
-                                for (int e2 = 0; e2 < 16; ++e2)
-                                    pv[e2] = ((vm[c >> 5] >> ((c & 31) + e2)) & 1u) ? pv[e2] : 0.f;
+                                for (int e = 0; e < 32; ++e) x[e] = ((b >> e) & 1u) ? x[e] : 0u;
                             }
                             #pragma unroll
-                            for (int e2 = 0; e2 < 8; ++e2) {
-                                rsum2[e2 & 3] = add_f32x2(rsum2[e2 & 3], pack_f32x2(pv[2 * e2], pv[2 * e2 + 1]));
-                                pk[e2] = pack_bf16(pv[2 * e2], pv[2 * e2 + 1]);
+                            for (int e = 0; e < 16; ++e)
+                                far[e & 3] = fmax3_abs(far[e & 3], __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        };
+                        tmem_ld32(tS, ra);
+                        tmem_ld32_wait(ra);
+                        tmem_ld32(tS + 32, rb);
+                        farthest(ra, 0);
+                        tmem_ld32_wait(rb);
+                        tmem_ld32(tS + 64, ra);
+                        farthest(rb, 1);
+                        tmem_ld32_wait(ra);
+                        tmem_ld32(tS + 96, rb);
+                        farthest(ra, 2);
+                        tmem_ld32_wait(rb);
+                        tmem_ld32(tS, ra);
+                        farthest(rb, 3);
+                        uint64_t rsum2[4] = {0ull, 0ull, 0ull, 0ull};
+                        // P of 32 columns (bf16 pairs) to TMEM columns 16 w .., their sums alongside
+                        auto put = [&](float (&pv)[32], int w) {
+                            if (!fast) {
+                                const uint32_t b = bits(w);
+                                #pragma unroll
+                                for (int e = 0; e < 32; ++e) pv[e] = ((b >> e) & 1u) ? pv[e] : 0.f;
+                            }
+                            uint32_t pk[16];
+                            #pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                rsum2[e & 3] = add_f32x2(rsum2[e & 3], pack_f32x2(pv[2 * e], pv[2 * e + 1]));
+                                pk[e] = pack_bf16(pv[2 * e], pv[2 * e + 1]);
+                            }
+                            tmem_st16(tS + w * 16, pk);
+                        };
+                        const bool wide = __any_sync(0xffffffffu, fmax3(fmaxf(far[0], far[1]), far[2], far[3]) > p.cap.limit);
+                        // The four quarters of the row, each loaded while the last is worked on.
+                        auto row = [&](auto&& quarter) {
+                            #pragma unroll 1
+                            for (int h = 0; h < 4; h += 2) {
+                                float pv[32];
+                                tmem_ld32_wait(ra);
+                                tmem_ld32(tS + (h + 1) * 32, rb);
+                                quarter(ra, pv);
+                                put(pv, h);
+                                tmem_ld32_wait(rb);
+                                if (h == 0) tmem_ld32(tS + 64, ra);
+                                quarter(rb, pv);
+                                put(pv, h + 1);
                             }
                         };
-                        float far[4] = {0.f, 0.f, 0.f, 0.f};      // largest |score| seen
-                        {
+                        if (!wide) {
                             const uint64_t nref = pack_f32x2(-p.cap.ref, -p.cap.ref);
                             const uint64_t c0 = pack_f32x2(p.cap.poly[0], p.cap.poly[0]);
                             const uint64_t c1 = pack_f32x2(p.cap.poly[1], p.cap.poly[1]);
                             const uint64_t c2 = pack_f32x2(p.cap.poly[2], p.cap.poly[2]);
                             const uint64_t c3 = pack_f32x2(p.cap.poly[3], p.cap.poly[3]);
-                            #pragma unroll
-                            for (int e2 = 0; e2 < 4; ++e2) rsum2[e2] = 0ull;
-                            #pragma unroll
-                            for (int g8 = 0; g8 < 8; ++g8) {
-                                float pv[16];
+                            row([&](const uint32_t (&sx)[32], float (&pv)[32]) {
                                 #pragma unroll
-                                for (int e2 = 0; e2 < 8; ++e2) {
-                                    const int c = g8 * 16 + 2 * e2;
-                                    far[e2 & 3] = fmax3_abs(far[e2 & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-                                    const uint64_t x = pack_u32x2(sr[c], sr[c + 1]);
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint64_t x = pack_u32x2(sx[2 * e], sx[2 * e + 1]);
                                     const uint64_t tt = mul_f32x2(x, x);
                                     const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(c3, tt, c2), tt, c1), tt, c0);
                                     float x0, x1;
                                     unpack_f32x2(fma_f32x2(x, y, nref), x0, x1);
-                                    pv[2 * e2] = fast_exp2(x0);
-                                    pv[2 * e2 + 1] = fast_exp2(x1);
+                                    pv[2 * e] = fast_exp2(x0);
+                                    pv[2 * e + 1] = fast_exp2(x1);
                                 }
-                                put_half(g8 * 16, pv, pk + (g8 & 1) * 8);
-                                if (g8 & 1) tmem_st16(tS + (g8 >> 1) * 16, pk);
-                            }
-                        }
-                        if (__any_sync(0xffffffffu, fmax3(fmaxf(far[0], far[1]), far[2], far[3]) > p.cap.limit)) {
+                            });
+                        } else {
                             const float top = p.cap.a - p.cap.ref;
                             const uint64_t topx2 = pack_f32x2(top, top);
                             const uint64_t k1x2 = pack_f32x2(p.cap.k1, p.cap.k1);
                             const uint64_t one = pack_f32x2(1.f, 1.f), two = pack_f32x2(2.f, 2.f);
                             const uint64_t neg = pack_f32x2(-1.f, -1.f), nb = pack_f32x2(-p.cap.b, -p.cap.b);
-                            #pragma unroll
-                            for (int e2 = 0; e2 < 4; ++e2) rsum2[e2] = 0ull;
-                            #pragma unroll
-                            for (int g8 = 0; g8 < 8; ++g8) {
-                                float pv[16];
+                            row([&](const uint32_t (&sx)[32], float (&pv)[32]) {
                                 #pragma unroll
-                                for (int e2 = 0; e2 < 8; ++e2) {
-                                    const int c = g8 * 16 + 2 * e2;
+                                for (int e = 0; e < 16; ++e) {
                                     float x0, x1;
-                                    unpack_f32x2(mul_f32x2(pack_u32x2(sr[c], sr[c + 1]), k1x2), x0, x1);
+                                    unpack_f32x2(mul_f32x2(pack_u32x2(sx[2 * e], sx[2 * e + 1]), k1x2), x0, x1);
                                     // past 2^30 tanh is 1 in fp32 already
                                     const float z0 = fast_exp2(fminf(x0, 30.f)), z1 = fast_exp2(fminf(x1, 30.f));
                                     const uint64_t d = add_f32x2(pack_f32x2(z0, z1), one);
@@ -868,12 +887,10 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                                     #pragma unroll
                                     for (int n3 = 0; n3 < 3; ++n3) r2 = mul_f32x2(r2, fma_f32x2(dn, r2, two));
                                     unpack_f32x2(fma_f32x2(nb, r2, topx2), x0, x1);
-                                    pv[2 * e2] = fast_exp2(x0);
-                                    pv[2 * e2 + 1] = fast_exp2(x1);
+                                    pv[2 * e] = fast_exp2(x0);
+                                    pv[2 * e + 1] = fast_exp2(x1);
                                 }
-                                put_half(g8 * 16, pv, pk + (g8 & 1) * 8);
-                                if (g8 & 1) tmem_st16(tS + (g8 >> 1) * 16, pk);
-                            }
+                            });
                         }
                         tmem_st_wait();
                         tc_fence_before();
@@ -884,7 +901,24 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         for (int e2 = 0; e2 < 4; ++e2) unpack_f32x2(rsum2[e2], rsum[2 * e2], rsum[2 * e2 + 1]);
                         l += ((rsum[0] + rsum[1]) + (rsum[2] + rsum[3])) + ((rsum[4] + rsum[5]) + (rsum[6] + rsum[7]));
                         m = l > 0.f ? p.cap.ref : -INFINITY;
-                    } else if constexpr (!SPEC) {
+                        continue;
+                    }
+                    // S row of this thread, all 128 columns at once (the softmax
+                    // warpgroups hold 208 registers a thread).  Columns at or past
+                    // nkeys were not written by this tile's MMA and hold stale
+                    // values; their visibility bits are 0, so the select below
+                    // turns them into -inf like any invisible key.  One code path
+                    // for every tile width keeps the loop small.
+                    uint32_t sr[128];
+                    tmem_ld128(tS, sr);
+                    const bool fast = !masked && kt.nkeys == 128;
+                    if (!fast) {
+                        // invisible or absent columns -> -inf, once (branch-free)
+                        #pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            sr[c] = ((vm[c >> 5] >> (c & 31)) & 1u) ? sr[c] : 0xff800000u;
+                    }
+                    if constexpr (!SPEC) {
                         // row maximum (raw score units; the scale is positive): eight
                         // running maxima, two new columns each per three-input max
                         float tmax;
