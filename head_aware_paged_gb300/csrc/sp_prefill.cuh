@@ -781,68 +781,50 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // operations on raw scores; otherwise the tile takes the formula,
                         // its reciprocal by Newton's iteration.
                         //
-                        // The row is read from TMEM 32 columns at a time, the next ones on
-                        // their way while these are worked on: once for the largest
-                        // |score|, once for P, which takes the place of columns already
-                        // read.  (All 128 in registers with every step unrolled: XXX us.)
-                        uint32_t ra[32], rb[32];
+                        // The row is read from TMEM 32 columns at a time in two small
+                        // loops, one for the largest |score|, one for P, which takes the
+                        // place of columns already read: the instruction cache decides
+                        // here (the same with the loops unrolled and the next columns
+                        // loaded ahead: 269 and 289 us; all 128 columns in registers: 272).
+                        uint32_t ra[32];
+                        const bool fast = !masked && kt.nkeys == 128;
                         // visibility bits of columns 32 w .. 32 w + 31
                         auto bits = [&](int w) { return w < 2 ? (w ? vm[1] : vm[0]) : w == 2 ? vm[2] : vm[3]; };
-                        const bool fast = !masked && kt.nkeys == 128;
                         float far[4] = {0.f, 0.f, 0.f, 0.f};      // largest |visible score|
-                        auto farthest = [&](uint32_t (&x)[32], int w) {
+                        #pragma unroll 1
+                        for (int w = 0; w < 4; ++w) {
+                            tmem_ld32(tS + w * 32, ra);
+                            tmem_ld32_wait(ra);
                             if (!fast) {
-                                const uint32_t b = bits(w);
+                                const uint32_t seen = bits(w);
                                 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = ((b >> e) & 1u) ? x[e] : 0u;
+                                for (int e = 0; e < 32; ++e) ra[e] = ((seen >> e) & 1u) ? ra[e] : 0u;
                             }
                             #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                far[e & 3] = fmax3_abs(far[e & 3], __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                        };
-                        tmem_ld32(tS, ra);
-                        tmem_ld32_wait(ra);
-                        tmem_ld32(tS + 32, rb);
-                        farthest(ra, 0);
-                        tmem_ld32_wait(rb);
-                        tmem_ld32(tS + 64, ra);
-                        farthest(rb, 1);
-                        tmem_ld32_wait(ra);
-                        tmem_ld32(tS + 96, rb);
-                        farthest(ra, 2);
-                        tmem_ld32_wait(rb);
-                        tmem_ld32(tS, ra);
-                        farthest(rb, 3);
-                        uint64_t rsum2[4] = {0ull, 0ull, 0ull, 0ull};
-                        // P of 32 columns (bf16 pairs) to TMEM columns 16 w .., their sums alongside
-                        auto put = [&](float (&pv)[32], int w) {
-                            if (!fast) {
-                                const uint32_t b = bits(w);
-                                #pragma unroll
-                                for (int e = 0; e < 32; ++e) pv[e] = ((b >> e) & 1u) ? pv[e] : 0.f;
-                            }
-                            uint32_t pk[16];
-                            #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                rsum2[e & 3] = add_f32x2(rsum2[e & 3], pack_f32x2(pv[2 * e], pv[2 * e + 1]));
-                                pk[e] = pack_bf16(pv[2 * e], pv[2 * e + 1]);
-                            }
-                            tmem_st16(tS + w * 16, pk);
-                        };
+                                far[e & 3] = fmax3_abs(far[e & 3], __uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
+                        }
                         const bool wide = __any_sync(0xffffffffu, fmax3(fmaxf(far[0], far[1]), far[2], far[3]) > p.cap.limit);
-                        // The four quarters of the row, each loaded while the last is worked on.
+                        uint64_t rsum2[4] = {0ull, 0ull, 0ull, 0ull};
                         auto row = [&](auto&& quarter) {
                             #pragma unroll 1
-                            for (int h = 0; h < 4; h += 2) {
+                            for (int w = 0; w < 4; ++w) {
                                 float pv[32];
+                                tmem_ld32(tS + w * 32, ra);
                                 tmem_ld32_wait(ra);
-                                tmem_ld32(tS + (h + 1) * 32, rb);
                                 quarter(ra, pv);
-                                put(pv, h);
-                                tmem_ld32_wait(rb);
-                                if (h == 0) tmem_ld32(tS + 64, ra);
-                                quarter(rb, pv);
-                                put(pv, h + 1);
+                                if (!fast) {
+                                    const uint32_t seen = bits(w);
+                                    #pragma unroll
+                                    for (int e = 0; e < 32; ++e) pv[e] = ((seen >> e) & 1u) ? pv[e] : 0.f;
+                                }
+                                uint32_t pk[16];
+                                #pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    rsum2[e & 3] = add_f32x2(rsum2[e & 3], pack_f32x2(pv[2 * e], pv[2 * e + 1]));
+                                    pk[e] = pack_bf16(pv[2 * e], pv[2 * e + 1]);
+                                }
+                                tmem_st16(tS + w * 16, pk);
                             }
                         };
                         if (!wide) {
