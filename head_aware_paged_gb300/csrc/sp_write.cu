@@ -14,9 +14,9 @@
 //
 // Bound by memory: 4 bytes a q element, 2 + the page type's size a stored
 // k / v element; a token that a head does not keep is not read.  Measured,
-// 8,192 rows of 32 query and 8 KV heads: 33.5 us for every head GLOBAL (201 MB,
-// 6.0 TB/s, 88 % of the copy rate), 29.1 us for one of eight (150 MB); FP8 and
-// 4-bit pages 38.2 and 39.7 us.  64 rows of 64 sequences: 3.9 us.  A thread
+// 8,192 rows of 32 query and 8 KV heads: 31.8 us for every head GLOBAL (201 MB,
+// 6.3 TB/s, 93 % of the copy rate), 24.8 us for one of eight (150 MB); FP8 and
+// 4-bit pages 31.3 and 33.7 us.  64 rows of 64 sequences: 3.8 us.  A thread
 // rotates one chunk of 8 dimensions and its partner chunk (16-byte loads and
 // stores; a whole block of 16 for 4-bit pages, whose scale needs its maximum).
 //
@@ -57,20 +57,21 @@ struct WriteParams {
     int32_t off[MAXU + 1];                 // prefix of the units' new pages
 };
 
-// Eight elements of each half, rotated; fp32.
-__device__ __forceinline__ void rotate8(const uint4& xa, const uint4& yb, const float2* cs, float* x,
-                                        float* y) {
+// Eight elements of each half, rotated; fp32.  cs: this chunk's first (cos,
+// sin, cos, sin) of two frequencies, the next two nc further.
+__device__ __forceinline__ void rotate8(const uint4& xa, const uint4& yb, const float4* cs, int nc,
+                                        float* x, float* y) {
     const uint32_t xw[4] = {xa.x, xa.y, xa.z, xa.w}, yw[4] = {yb.x, yb.y, yb.z, yb.w};
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const __nv_bfloat162 u = *reinterpret_cast<const __nv_bfloat162*>(&xw[e]);
         const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&yw[e]);
         const float x0 = __low2float(u), x1 = __high2float(u), y0 = __low2float(v), y1 = __high2float(v);
-        const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
-        x[2 * e] = x0 * c0.x - y0 * c0.y;
-        y[2 * e] = y0 * c0.x + x0 * c0.y;
-        x[2 * e + 1] = x1 * c1.x - y1 * c1.y;
-        y[2 * e + 1] = y1 * c1.x + x1 * c1.y;
+        const float4 c = cs[e * nc];
+        x[2 * e] = x0 * c.x - y0 * c.y;
+        y[2 * e] = y0 * c.x + x0 * c.y;
+        x[2 * e + 1] = x1 * c.z - y1 * c.w;
+        y[2 * e + 1] = y1 * c.z + x1 * c.w;
     }
 }
 __device__ __forceinline__ void plain8(const uint4& a, float* x) {
@@ -149,7 +150,7 @@ __device__ __forceinline__ bool row_at(const PR& p, int b, int h, int32_t t, Row
 }
 
 template <int KV, typename PR>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, KV == kFp4 ? 4 : 1)
 k_write_rope(const __grid_constant__ PR p) {
     const Geo& g = p.geo;
     const int tid = threadIdx.x;
@@ -178,14 +179,16 @@ k_write_rope(const __grid_constant__ PR p) {
         return;
     }
     constexpr int CH = KV == kFp4 ? 16 : 8;              // k / v dimensions of a chunk
-    __shared__ float2 cs[kMaxTok * 64];
+    // angles, [token][pair of a chunk][chunk]: lanes read neighbouring chunks
+    __shared__ float4 cs[kMaxTok * 32];
     __shared__ int32_t tok_b[kMaxTok], tok_t[kMaxTok];
     const int D = g.d, half = D / 2;
     const int r0 = (int)blockIdx.x * p.tok, nt = min(p.tok, p.rows - r0);
     // queries: two chunk pairs a pass (four 16-byte loads in flight a thread),
     // the first pass's loads ahead of the angles
     const int stride = kWriteThreads * gridDim.y, first = blockIdx.y * kWriteThreads + tid;
-    const int lq = 28 - __clz(half), q_row = g.hq << lq, q_all = p.q ? nt * q_row : 0;   // half / 8 = 2^lq chunks a head
+    const int nc = half / 8;                             // chunks of a head's half
+    const int lq = 28 - __clz(half), q_row = g.hq << lq, q_all = p.q ? nt * q_row : 0;   // nc = 2^lq
     uint4 qa[2], qb[2];
     int qt[2], qat[2];                                   // token, element inside its row
     auto fetch = [&](int e0) {
@@ -213,10 +216,12 @@ k_write_rope(const __grid_constant__ PR p) {
     }
     __syncthreads();
     for (int e = tid; e < nt * half; e += kWriteThreads) {
-        const uint64_t turns = (uint64_t)(uint32_t)tok_t[e / half] * p.turn[e % half];
+        const int t = e / half, f = e % half;
+        const uint64_t turns = (uint64_t)(uint32_t)tok_t[t] * p.turn[f];
         // nearest 2^-32 turn, as a signed number of half turns
         const float x = (float)(int32_t)(uint32_t)((turns + 0x80000000ull) >> 32) * 4.6566128730773926e-10f;
-        sincospif(x, &cs[e].y, &cs[e].x);
+        float2* c = reinterpret_cast<float2*>(cs + (t * 4 + ((f & 7) >> 1)) * nc + (f >> 3)) + (f & 1);
+        sincospif(x, &c->y, &c->x);
     }
     __syncthreads();
     for (int e0 = first; e0 < q_all; e0 += 2 * stride) {
@@ -225,7 +230,7 @@ k_write_rope(const __grid_constant__ PR p) {
         for (int k = 0; k < 2; ++k) {
             if (e0 + k * stride >= q_all) break;
             float x[8], y[8];
-            rotate8(qa[k], qb[k], cs + qt[k] * half + (qat[k] & (D - 1)), x, y);
+            rotate8(qa[k], qb[k], cs + qt[k] * half / 2 + ((qat[k] & (D - 1)) >> 3), nc, x, y);
             __nv_bfloat16* dst = p.q_out + (int64_t)(r0 + qt[k]) * g.hq * D + qat[k];
             *reinterpret_cast<uint4*>(dst) = bf16x8(x);
             *reinterpret_cast<uint4*>(dst + half) = bf16x8(y);
@@ -238,23 +243,20 @@ k_write_rope(const __grid_constant__ PR p) {
         if (!row_at(p, tok_b[t], h, tok_t[t], at)) continue;
         const __nv_bfloat16* ks = p.k + (int64_t)(r0 + t) * p.k_stride + h * D + c * CH;
         const __nv_bfloat16* vs = p.v + (int64_t)(r0 + t) * p.v_stride + h * D + c * CH;
-        const float2* ang = cs + t * half + c * CH;
+        const float4* ang = cs + t * half / 2 + c * (CH / 8);
         const int64_t so = ((int64_t)p.layer * g.hkv + h) * D + c * CH;
         if constexpr (KV == kFp4) {
             const uint4* k4 = reinterpret_cast<const uint4*>(ks);
             const uint4* k4b = reinterpret_cast<const uint4*>(ks + half);
-            const uint4* v4 = reinterpret_cast<const uint4*>(vs);
-            const uint4* v4b = reinterpret_cast<const uint4*>(vs + half);
             const uint4 ka[2] = {k4[0], k4[1]}, kb[2] = {k4b[0], k4b[1]};
-            const uint4 va[2] = {v4[0], v4[1]}, vb[2] = {v4b[0], v4b[1]};
             const int64_t go = fp4_group_off(at.page, at.slot, g.page);
             uint8_t* kg = static_cast<uint8_t*>(p.kpool) + go;
             uint8_t* vg = static_cast<uint8_t*>(p.vpool) + go;
             const int s = at.slot & 15;
             float x[16], y[16];
             uint32_t sc;
-            rotate8(ka[0], kb[0], ang, x, y);
-            rotate8(ka[1], kb[1], ang + 8, x + 8, y + 8);
+            rotate8(ka[0], kb[0], ang, nc, x, y);
+            rotate8(ka[1], kb[1], ang + 1, nc, x + 8, y + 8);
             if (p.scaled) {
                 times<16>(x, p.meta.kinv + so);
                 times<16>(y, p.meta.kinv + so + half);
@@ -263,10 +265,12 @@ k_write_rope(const __grid_constant__ PR p) {
             kg[fp4_k_scale(s, c)] = (uint8_t)sc;
             *reinterpret_cast<uint2*>(kg + fp4_k_code(s, c + 4)) = fp4_quant16(y, sc);
             kg[fp4_k_scale(s, c + 4)] = (uint8_t)sc;
-            plain8(va[0], x);
-            plain8(va[1], x + 8);
-            plain8(vb[0], y);
-            plain8(vb[1], y + 8);
+            const uint4* v4 = reinterpret_cast<const uint4*>(vs);
+            const uint4* v4b = reinterpret_cast<const uint4*>(vs + half);
+            plain8(v4[0], x);
+            plain8(v4[1], x + 8);
+            plain8(v4b[0], y);
+            plain8(v4b[1], y + 8);
             if (p.scaled) {
                 times<16>(x, p.meta.vinv + so);
                 times<16>(y, p.meta.vinv + so + half);
@@ -282,7 +286,7 @@ k_write_rope(const __grid_constant__ PR p) {
             const uint4 vb = *reinterpret_cast<const uint4*>(vs + half);
             const int64_t dst = ((int64_t)at.page * g.page + at.slot) * D + c * 8;
             float x[8], y[8];
-            rotate8(ka, kb, ang, x, y);
+            rotate8(ka, kb, ang, nc, x, y);
             if constexpr (KV == kFp8) {
                 uint8_t* kp = static_cast<uint8_t*>(p.kpool) + dst;
                 uint8_t* vp = static_cast<uint8_t*>(p.vpool) + dst;
@@ -367,7 +371,7 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     p.kpool = c->kpool; p.vpool = c->vpool;
     std::memcpy(p.turn, turn, sizeof(p.turn));
     // Four tokens a block share its set-up once that still fills the GPU (8,192
-    // rows: 31.1 us with two, 29.1 with four, 34.5 with eight); a short call
+    // rows: 29.1 us with four, 31.1 with two, 34.5 with eight); a short call
     // spreads one token's heads over two blocks instead.
     p.tok = rows >= 4 * c->num_sms ? kMaxTok : 1;
     p.row_blocks = (rows + p.tok - 1) / p.tok;
