@@ -16,7 +16,7 @@
 // k / v element; a token that a head does not keep is not read.  Measured,
 // 8,192 rows of 32 query and 8 KV heads: 31.8 us for every head GLOBAL (201 MB,
 // 6.3 TB/s, 93 % of the copy rate), 24.8 us for one of eight (150 MB); FP8 and
-// 4-bit pages 31.3 and 33.7 us.  64 rows of 64 sequences: 3.8 us.  A thread
+// 4-bit pages 30.5 and 33.7 us.  64 rows of 64 sequences: 3.8 us.  A thread
 // rotates one chunk of 8 dimensions and its partner chunk (16-byte loads and
 // stores; a whole block of 16 for 4-bit pages, whose scale needs its maximum).
 //
@@ -149,8 +149,10 @@ __device__ __forceinline__ bool row_at(const PR& p, int b, int h, int32_t t, Row
     return true;
 }
 
+// (Five blocks an SM, four for 4-bit pages: with more registers and fewer blocks
+// 28.5 instead of 24.8 us, and 40.2 instead of 31.7 us.)
 template <int KV, typename PR>
-__global__ void __launch_bounds__(kWriteThreads, KV == kFp4 ? 4 : 1)
+__global__ void __launch_bounds__(kWriteThreads, KV == kFp4 ? 4 : 5)
 k_write_rope(const __grid_constant__ PR p) {
     const Geo& g = p.geo;
     const int tid = threadIdx.x;
