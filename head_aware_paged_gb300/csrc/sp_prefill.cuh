@@ -203,6 +203,12 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 // Bits of a start for 1 / d, less d's: twice the bits of 1.0, less what
 // centres the error (12.5 % at most over d's mantissa).
 constexpr uint32_t kRcpStart = 0x7EF311C7u;
+// min(a, b), NaN if either is.
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // max(|a|, |b|, |c|).
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
     float r;
@@ -856,8 +862,8 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                                 for (int e = 0; e < 16; ++e) {
                                     float x0, x1;
                                     unpack_f32x2(mul_f32x2(pack_u32x2(sx[2 * e], sx[2 * e + 1]), k1x2), x0, x1);
-                                    // past 2^30 tanh is 1 in fp32 already
-                                    const float z0 = fast_exp2(fminf(x0, 30.f)), z1 = fast_exp2(fminf(x1, 30.f));
+                                    // past 2^30 tanh is 1 in fp32 already (and a NaN stays one)
+                                    const float z0 = fast_exp2(fmin_nan(x0, 30.f)), z1 = fast_exp2(fmin_nan(x1, 30.f));
                                     const uint64_t d = add_f32x2(pack_f32x2(z0, z1), one);
                                     // start: the exponent and mantissa fields subtracted from
                                     // twice those of 1 (within 12.5 %), then three steps

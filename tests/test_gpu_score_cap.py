@@ -137,6 +137,54 @@ def test_extreme_scores(cap):
     assert cache.status() == 0
 
 
+@pytest.mark.parametrize("cap", [1.0 / 64, 1.0, 50.0, 64.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_extreme_scores_decode(d, cap):
+    """Scores of +-1e30, both signs of the query: every score sits on +-cap."""
+    gpu_ready()
+    n = 200
+    cache = _mk(2, 1, d, 16, 1, n, 20)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 0] = 1e15
+    k[1::3] *= -1
+    v = W.normal((n, 1, d), 3, device="cuda")
+    cache.append_kv(0, [0], [0, n], k, v)
+    q = torch.zeros(1, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0], q[:, 1, 0] = 1e15, -1e15
+    out, lse = cache.decode(0, [0], q, score_cap=cap)
+    ref = attend(q.double(), k.double(), v.double(), [n - 1], [(G, 0, 0, None)], cap)
+    check(out, lse, ref[:3] + (torch.zeros_like(ref[3]), ref[4]), 2.0 ** -8, 0.0, "decode", cap)
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("cap,qs", [(50.0, 1.0), (2.0, 12.0)])
+def test_nan_query_stays_in_its_row(kv, cap, qs):
+    """A NaN query answers NaN, inside the cap and far past it, and the
+    other rows of its tile stay right."""
+    gpu_ready()
+    hq, d, n = 2, 128, 200
+    cache = _mk(hq, 1, d, 64, 1, n, 10, kv)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    q = (W.normal((n, hq, d), 7, device="cuda").float() * qs).to(torch.bfloat16)
+    k, v = W.normal((n, 1, d), 8, device="cuda"), W.normal((n, 1, d), 9, device="cuda")
+    want, want_lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)
+    bad = q.clone()
+    bad[[5, 150], 1, 3] = math.nan
+    got, lse = cache.prefill(0, [0], [0, n], bad, k, v, score_cap=cap)
+    hit = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    hit[[5, 150], 1] = True
+    assert torch.isnan(got[hit]).all()
+    ref = attend(q.double(), k.double(), v.double(), range(n), [(G, 0, 0, None)], cap)
+    got[hit], lse[hit] = want[hit], want_lse[hit]               # (checked above)
+    check(got, lse, ref, 2.0 ** -8, 0.0, "the other rows", cap)
+    cache.append_kv(0, [0], [0, n], k, v)
+    got, _ = cache.decode(0, [0], bad[150:151].contiguous(), score_cap=cap)
+    assert torch.isnan(got[0, 1]).all() and torch.isfinite(got[0, 0]).all()
+    assert cache.status() == 0
+
+
 def test_uncapped_calls_keep_their_results_and_refusals():
     gpu_ready()
     from head_aware_paged_gb300 import SegPagedError
