@@ -326,6 +326,13 @@ sp_status cuda_fail(cudaError_t e, const char* what) {
     return SP_ERR_CUDA;
 }
 
+sp_status check_device(const sp_cache* c) {
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    return dev == c->device ? SP_OK : fail(SP_ERR_INVALID_ARG, "current device is not the cache's device");
+}
+
 bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128,
                     std::string* err, bool bytes) {
@@ -627,6 +634,8 @@ static sp_status attention_prefill(sp_cache* c, int32_t layer, const int32_t* se
             return fail(SP_ERR_INVALID_ARG, "chunk would pass max_seq_len");
     }
     if (cu_q[n_seqs] > c->cfg.max_tokens) return fail(SP_ERR_INVALID_ARG, "more rows than max_tokens");
+    s = check_device(c);
+    if (s != SP_OK) return s;
     return prefill_impl(c, layer, seq_ids, n_seqs, cu_q, static_cast<const __nv_bfloat16*>(q),
                         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                         static_cast<__nv_bfloat16*>(out), lse, cap, static_cast<cudaStream_t>(stream));
@@ -641,6 +650,8 @@ static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq
     if (s != SP_OK) return s;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 3)
         return fail(SP_ERR_INVALID_ARG, "q and out must be 4-byte aligned");
+    s = check_device(c);
+    if (s != SP_OK) return s;
     DecodeParams* p = new DecodeParams();   // large; keep it off the host stack
     std::unique_ptr<DecodeParams> guard(p);
     p->meta = c->meta;

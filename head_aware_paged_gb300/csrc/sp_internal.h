@@ -230,6 +230,8 @@ inline void launch_mark_end(sp_cache* c, cudaStream_t s) {
 // Error plumbing (sp_api.cu).
 sp_status fail(sp_status s, const std::string& msg);
 sp_status cuda_fail(cudaError_t e, const char* what);
+// SP_ERR_INVALID_ARG unless the cache's device is the current one.
+sp_status check_device(const sp_cache* c);
 // Runs a C entry point's body: no C++ exception (host memory) leaves it.
 template <typename F>
 sp_status no_throw(F&& body) {

@@ -439,10 +439,8 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
         const double f = w / two_pi, frac = f - std::floor(f);      // [0, 1]
         turn[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
     }
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (dev != c->device) return fail(SP_ERR_INVALID_ARG, "current device is not the cache's device");
+    s = check_device(c);
+    if (s != SP_OK) return s;
     auto* qp = static_cast<const __nv_bfloat16*>(q);
     auto* kp = static_cast<const __nv_bfloat16*>(k);
     auto* vp = static_cast<const __nv_bfloat16*>(v);

@@ -196,6 +196,8 @@ sp_status sp_append_kv(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
  *     k and v likewise with num_kv_heads (strides in elements, multiples of 8,
  *     at least a row); all 16-byte aligned.  q and q_out may both be null: keys
  *     and values only.  q_out is contiguous; it may be q itself if q is.
+ * A prompt chunk attends before it is stored (sp_attention_prefill wants its
+ * keys rotated already); afterwards this call stores the unrotated rows, q null.
  * One launch, pages included; works for every page type and head class.  The
  * current device must be the cache's.  Captured into a graph, a replay writes
  * the same positions and pages again. */
@@ -235,7 +237,10 @@ sp_status sp_attention_decode(sp_cache* cache, int32_t layer,
  * of score_cap * tanh(s / score_cap), s = q . k / sqrt(head_dim), over each
  * head's visible keys.  score_cap in [1/64, 64] (SP_ERR_INVALID_ARG
  * otherwise); everything else is as for sp_attention_prefill and
- * sp_attention_decode (lse is that of the capped scores). */
+ * sp_attention_decode (lse is that of the capped scores).  In all four calls a
+ * key that a row does not see, and a row of another sequence, may enter its
+ * sums with the weight 0: k and v must be finite (a NaN in q stays in its row).
+ * The current device must be the cache's. */
 sp_status sp_attention_prefill_capped(sp_cache* cache, int32_t layer,
                                       const int32_t* seq_ids, int32_t n_seqs,
                                       const int32_t* cu_q, const void* q,
