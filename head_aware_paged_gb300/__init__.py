@@ -30,7 +30,7 @@ import numpy as np
 import torch
 
 from ._lib import (EXPORTS, GLOBAL, KV_BF16, KV_FP4, KV_FP8, LOCAL, RETRIEVAL, SegPagedError, SpConfig, SpHeadPolicy,
-                   check, i32_array, i64_array, load)
+                   check, i32_array, i32_buffer, i64_array, i64_buffer, load)
 
 __all__ = ["Config", "Policy", "SegPagedCache", "SegPagedError", "GLOBAL", "LOCAL",
            "RETRIEVAL", "KV_BF16", "KV_FP8", "KV_FP4", "load", "EXPORTS"] + list(EXPORTS)
@@ -129,15 +129,17 @@ def sp_append_kv(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequence[in
 def sp_attention_prefill(handle, layer: int, seq_ids: Sequence[int], cu_q: Sequence[int],
                          q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                          lse: Optional[torch.Tensor] = None, stream=None) -> None:
-    check(load().sp_attention_prefill(handle, layer, i32_array(seq_ids), len(seq_ids),
-                                      i32_array(cu_q), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+    ids, cu = i32_buffer(seq_ids), i32_buffer(cu_q)
+    check(load().sp_attention_prefill(handle, layer, ids.buffer_info()[0], len(seq_ids),
+                                      cu.buffer_info()[0], _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                       _ptr(lse), _stream(stream)))
 
 
 def sp_attention_decode(handle, layer: int, seq_ids: Sequence[int], q: torch.Tensor,
                         out: torch.Tensor, lse: Optional[torch.Tensor] = None,
                         stream=None) -> None:
-    check(load().sp_attention_decode(handle, layer, i32_array(seq_ids), len(seq_ids), _ptr(q),
+    ids = i32_buffer(seq_ids)
+    check(load().sp_attention_decode(handle, layer, ids.buffer_info()[0], len(seq_ids), _ptr(q),
                                      _ptr(out), _ptr(lse), _stream(stream)))
 
 
@@ -145,8 +147,9 @@ def sp_attention_prefill_capped(handle, layer: int, seq_ids: Sequence[int], cu_q
                                 q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, score_cap: float,
                                 out: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """sp_attention_prefill over scores capped by score_cap * tanh(s / score_cap)."""
-    check(load().sp_attention_prefill_capped(handle, layer, i32_array(seq_ids), len(seq_ids),
-                                             i32_array(cu_q), _ptr(q), _ptr(k), _ptr(v),
+    ids, cu = i32_buffer(seq_ids), i32_buffer(cu_q)
+    check(load().sp_attention_prefill_capped(handle, layer, ids.buffer_info()[0], len(seq_ids),
+                                             cu.buffer_info()[0], _ptr(q), _ptr(k), _ptr(v),
                                              float(score_cap), _ptr(out), _ptr(lse), _stream(stream)))
 
 
@@ -154,7 +157,8 @@ def sp_attention_decode_capped(handle, layer: int, seq_ids: Sequence[int], q: to
                                score_cap: float, out: torch.Tensor,
                                lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """sp_attention_decode over scores capped by score_cap * tanh(s / score_cap)."""
-    check(load().sp_attention_decode_capped(handle, layer, i32_array(seq_ids), len(seq_ids), _ptr(q),
+    ids = i32_buffer(seq_ids)
+    check(load().sp_attention_decode_capped(handle, layer, ids.buffer_info()[0], len(seq_ids), _ptr(q),
                                             float(score_cap), _ptr(out), _ptr(lse), _stream(stream)))
 
 
@@ -168,8 +172,10 @@ def sp_append_kv_rope(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequen
     fr = None
     if inv_freq is not None:
         fr = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
-    check(load().sp_append_kv_rope(handle, layer, i32_array(seq_ids), len(seq_ids), i32_array(cu_new),
-                                   None if pos is None else i64_array(pos), _ptr(q),
+    ids, cu = i32_buffer(seq_ids), i32_buffer(cu_new)
+    at = None if pos is None else i64_buffer(pos)
+    check(load().sp_append_kv_rope(handle, layer, ids.buffer_info()[0], len(seq_ids), cu.buffer_info()[0],
+                                   at and at.buffer_info()[0], _ptr(q),
                                    0 if q is None else q.stride(0), _ptr(k), k.stride(0), _ptr(v),
                                    v.stride(0), _ptr(q_out), float(rope_theta), fr, _stream(stream)))
 

@@ -63,6 +63,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P = c_void_p
     I32P, I64P = POINTER(c_int32), POINTER(c_int64)
+    # (P for the host lists of the calls a model makes every step: an address
+    # is marshalled faster than a typed pointer)
     sig = {
         "sp_required_bytes": [POINTER(SpConfig), POINTER(c_size_t), POINTER(c_size_t), POINTER(c_size_t)],
         "sp_cache_create": [POINTER(SpConfig), P, P, P, POINTER(P)],
@@ -70,11 +72,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sp_set_policy": [P, c_int32, POINTER(SpHeadPolicy), P],
         "sp_build_cache": [P, c_int32, c_int32, P, P, c_int64, c_int64, P],
         "sp_append_kv": [P, c_int32, I32P, c_int32, I32P, P, P, P],
-        "sp_attention_prefill": [P, c_int32, I32P, c_int32, I32P, P, P, P, P, P, P],
-        "sp_attention_decode": [P, c_int32, I32P, c_int32, P, P, P, P],
-        "sp_attention_prefill_capped": [P, c_int32, I32P, c_int32, I32P, P, P, P, ctypes.c_float, P, P, P],
-        "sp_attention_decode_capped": [P, c_int32, I32P, c_int32, P, ctypes.c_float, P, P, P],
-        "sp_append_kv_rope": [P, c_int32, I32P, c_int32, I32P, I64P, P, c_int64, P, c_int64, P, c_int64, P,
+        "sp_attention_prefill": [P, c_int32, P, c_int32, P, P, P, P, P, P, P],
+        "sp_attention_decode": [P, c_int32, P, c_int32, P, P, P, P],
+        "sp_attention_prefill_capped": [P, c_int32, P, c_int32, P, P, P, P, ctypes.c_float, P, P, P],
+        "sp_attention_decode_capped": [P, c_int32, P, c_int32, P, ctypes.c_float, P, P, P],
+        "sp_append_kv_rope": [P, c_int32, P, c_int32, P, P, P, c_int64, P, c_int64, P, c_int64, P,
                               c_double, POINTER(c_double), P],
         "sp_attention_decode_static_scratch": [P, c_int32, I32P, c_int32, P, P, P, P],
         "sp_rope_realign": [P, c_int32, I32P, c_int32, c_int32, c_int64, c_int64, c_int64,
@@ -115,17 +117,31 @@ def check(status: int) -> None:
         raise SegPagedError(status, msg)
 
 
-def _host_array(ctype, code, values):
+def _host_buffer(ctype, code, values):
     # one pass in C for sequences of integers; anything else (floats with
     # integer values, numbers that wrap) one by one
     try:
         buf = array.array(code, values)
     except (TypeError, OverflowError):
-        values = [int(x) for x in values]
-        return (ctype * max(1, len(values)))(*values)
+        buf = array.array(code, bytes((ctype * len(values))(*[int(x) for x in values])))
     if not buf:
         buf.append(0)
+    return buf
+
+
+def _host_array(ctype, code, values):
+    buf = _host_buffer(ctype, code, values)
     return (ctype * len(buf)).from_buffer(buf)
+
+
+def i32_buffer(values):
+    """As i32_array, for calls whose arguments are addresses
+    (buffer_info()[0]; the caller keeps the buffer through the call)."""
+    return _host_buffer(c_int32, "i", values)
+
+
+def i64_buffer(values):
+    return _host_buffer(c_int64, "q", values)
 
 
 def i32_array(values):
