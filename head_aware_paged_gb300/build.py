@@ -18,8 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libsegpaged.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["sp_api.cu", "sp_storage.cu", "sp_decode.cu", "sp_prefill.cu", "sp_decode_static.cu",
-           "sp_decode_capped.cu", "sp_decode4.cu", "sp_decode4_capped.cu", "sp_prefill_capped.cu", "sp_dequant.cu",
-           "sp_write.cu", "sp_rope.cu", "sp_transfer.cu", "sp_select.cu", "sp_selftest.cu"]
+           "sp_decode_capped.cu", "sp_decode4.cu", "sp_decode4_capped.cu", "sp_prefill_capped.cu", "sp_prefill_rows.cu",
+           "sp_dequant.cu", "sp_write.cu", "sp_rope.cu", "sp_transfer.cu", "sp_select.cu", "sp_selftest.cu"]
 
 
 def nvcc() -> str:

@@ -26,7 +26,7 @@ struct Layout {
     size_t pol = 0, npages = 0, seqlen = 0, ptab = 0, idx = 0, fstack = 0, status = 0,
            scales = 0, meta_total = 0;
     size_t tiles = 0, tile_ctr = 0, part_o = 0, part_ml = 0, counters = 0, scratch = 0,
-           split_o = 0, split_ml = 0, deq = 0, deq_tab = 0, ws_total = 0;
+           split_o = 0, split_ml = 0, deq = 0, deq_row = 0, ws_total = 0;
     int64_t deq_pages = 0;
     int64_t max_tiles = 0, max_parts = 0, max_counter_units = 0, scratch_ints = 0;
     size_t pool_total = 0;
@@ -108,7 +108,7 @@ Layout make_layout(const sp_config* c) {
                                         std::max<int64_t>(L.max_pages_unit, (int64_t(2) << 30) / (2 * page_bytes)));
         o = align_up(o, 1024);
         L.deq = o;     o = align_up(o + 2 * (size_t)L.deq_pages * page_bytes, 256);
-        L.deq_tab = o; o = align_up(o + (size_t)L.max_counter_units * L.max_pages_unit * 4, 256);
+        L.deq_row = o; o = align_up(o + (size_t)L.max_counter_units * 4, 256);
     }
     L.ws_total = o;
     L.pool_total = 2 * (size_t)c->num_pages * c->page_size * config_row_bytes(c);
@@ -431,7 +431,7 @@ sp_status sp_cache_create(const sp_config* cfg, void* pool, void* meta, void* ws
     c->ws.deq_pages = L.deq_pages;
     c->ws.deq_k = reinterpret_cast<__nv_bfloat16*>(wb + L.deq);
     c->ws.deq_v = c->ws.deq_k + L.deq_pages * cfg->page_size * cfg->head_dim;
-    c->ws.deq_tab = reinterpret_cast<int32_t*>(wb + L.deq_tab);
+    c->ws.deq_row = reinterpret_cast<int32_t*>(wb + L.deq_row);
     std::string err;
     const uint64_t rows = (uint64_t)(g.fp4 ? L.deq_pages : cfg->num_pages) * cfg->page_size;
     // bf16: boxes of 64 elements (one 128-byte swizzle row); FP8: a 128-element
@@ -439,11 +439,11 @@ sp_status sp_cache_create(const sp_config* cfg, void* pool, void* meta, void* ws
     const uint32_t box = g.fp8 ? (uint32_t)cfg->head_dim : 64u;
     const uint64_t rowb = (uint64_t)cfg->head_dim * (g.fp8 ? 1 : 2);
     // (4-bit pages: decode reads them with untiled bulk copies, prefill reads
-    // their bf16 copies in the workspace)
+    // their bf16 copies in the workspace, a tile's 128 rows at a time)
     if (!encode_tmap_2d(&c->tm_kpool, g.fp4 ? c->ws.deq_k : c->kpool, cfg->head_dim, rows, rowb, box,
-                        cfg->page_size, true, &err, g.fp8) ||
+                        g.fp4 ? 128 : cfg->page_size, true, &err, g.fp8) ||
         !encode_tmap_2d(&c->tm_vpool, g.fp4 ? c->ws.deq_v : c->vpool, cfg->head_dim, rows, rowb, box,
-                        cfg->page_size, true, &err, g.fp8)) {
+                        g.fp4 ? 128 : cfg->page_size, true, &err, g.fp8)) {
         delete c;
         return fail(SP_ERR_CUDA, err);
     }

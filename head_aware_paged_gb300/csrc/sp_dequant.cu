@@ -1,13 +1,14 @@
-// sp_dequant.cu -- 4-bit history pages -> bf16 pages in the workspace, ahead of
-// a prefill over them.
+// sp_dequant.cu -- 4-bit history pages -> bf16 rows in the workspace, ahead of
+// a prefill over them.  A unit's slots follow one another there, so a tile of
+// k_prefill is one 128-row box whatever the page size.
 //
 // Every query tile of a chunk reads the same history, so its codes are turned
 // into bf16(code * scale * channel scale) once per call instead of once per
 // work item: a converter inside k_prefill (two warps next to eight softmax
 // warps) took about 8,000 cycles for the K and V of a tile whose products take
 // 2,048, and a fourth warpgroup of converters cost the softmax its registers
-// (2,048 rows after 16,384: 188 us that way, 137 us this way, 128 us on bf16
-// pages).  Bound by memory: 144 bytes read and 512 written a key, most of which
+// (2,048 rows after 16,384: 188 us that way, 121 us this way, 127 us on bf16
+// pages of 64).  Bound by memory: 144 bytes read and 512 written a key, most of which
 // stay in L2 for the kernel that follows.
 #include "sp_device.cuh"
 #include "sp_internal.h"
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(256) k_dequant4(const __grid_constant__ Dequan
             if (threadIdx.x == 0) atomicOr(p.meta.status, kStatusBadPage);
             phys = 0;                                // convert something harmless
         }
-        if (threadIdx.x == 0) p.tab[(int64_t)u * g.max_pages_unit + pg] = blk;
+        if (threadIdx.x == 0 && pg == 0) p.row0[u] = blk * P;
         const float* ks = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
         const float* vs = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
         const int c = threadIdx.x & 7;               // this thread's block of a row

@@ -155,9 +155,10 @@ struct Workspace {
     int32_t* counters;    int64_t max_counter_units;
     float* split_o;       float* split_ml;        // prefill pieces of split items
     int32_t* scratch;     int64_t scratch_ints;   // export / visible-count staging
-    // 4-bit pages: bf16 copies of a prefill's history pages, and their table
+    // 4-bit pages: a prefill's history as bf16 rows (deq_pages pages of them),
+    // and each unit's first row
     __nv_bfloat16* deq_k; __nv_bfloat16* deq_v;  int64_t deq_pages;
-    int32_t* deq_tab;
+    int32_t* deq_row;
 };
 
 }  // namespace sp
@@ -194,7 +195,7 @@ struct sp_cache {
     size_t stage_bytes = 0;                       // size of each buffer
     int stage_next = 0;
     // [capped ? 5 : 0 + (speculative ? 4 : two issuers ? 3 : FP8 ? 2 : D == 128)][log2(P) - 4, or 0]: attributes set
-    bool prefill_checked[10][4] = {};
+    bool prefill_checked[10][5] = {};
     // Caller's event pair armed by sp_set_launch_events for the next
     // attention call (both null when not armed).
     cudaEvent_t launch_ev[2] = {};
@@ -272,7 +273,7 @@ struct DequantParams {
     int32_t layer, unit0, n_units;
     const uint8_t *kpool, *vpool;
     __nv_bfloat16 *k, *v;
-    int32_t* tab;                // [max_batch][hkv][max_pages_unit]
+    int32_t* row0;               // [max_batch][hkv] first row of a unit's copies
     int32_t seq[kMaxCallSeqs];
     int32_t page_off[kMaxDecodeUnits + 1];
 };

@@ -136,11 +136,7 @@ static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_id
     p.out = out;
     p.lse = lse;
     p.cap = cap;
-    p.hist_ptab = nullptr;
-    if (c->geo.fp4) {                          // the history is read from its bf16 copies
-        p.hist_ptab = c->ws.deq_tab;
-        p.geo.num_pages = (int32_t)c->ws.deq_pages;
-    }
+    p.hist_row = c->ws.deq_row;
     p.split_o = reinterpret_cast<float4*>(c->ws.split_o);
     p.split_ml = reinterpret_cast<float2*>(c->ws.split_ml);
     struct Cand { int64_t cost; int32_t unit; int4 item; };   // unit: call sequence * Hkv + KV head
@@ -348,6 +344,8 @@ static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_id
     if (D == 128 && P == PP) e = launch_prefill_t<128, PP, true>(c, p, grid, tq, tk, tv, stream); else
     if (cap.on) {
         e = launch_prefill_capped(c, p, grid, two, tq, tk, tv, stream);
+    } else if (c->geo.fp4) {
+        e = launch_prefill_rows(c, p, grid, two, spec, tq, tk, tv, stream);
     } else if (c->geo.fp8) {   // FP8 pages (head_dim 128, checked at create)
         SP_PF8(16) SP_PF8(32) SP_PF8(64) SP_PF8(128)
         e = cudaErrorInvalidValue;
@@ -390,7 +388,7 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     const int H = c->cfg.num_kv_heads, units = n_seqs * H;
     if (!c->geo.fp4)
         return prefill_units(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse, cap, 0, units, true, true, stream);
-    // 4-bit pages: the units' history becomes bf16 pages in the workspace, as
+    // 4-bit pages: the units' history becomes bf16 rows in the workspace, as
     // many units at a time as fit, and the bf16 kernel reads those
     // (sp_dequant.cu says why).
     std::unique_ptr<DequantParams> dp(new DequantParams());
@@ -401,7 +399,7 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     dp->vpool = reinterpret_cast<const uint8_t*>(c->vpool);
     dp->k = c->ws.deq_k;
     dp->v = c->ws.deq_v;
-    dp->tab = c->ws.deq_tab;
+    dp->row0 = c->ws.deq_row;
     std::copy(seq_ids, seq_ids + n_seqs, dp->seq);
     launch_mark_start(c, stream);
     for (int u0 = 0; u0 < units;) {

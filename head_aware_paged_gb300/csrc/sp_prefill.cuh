@@ -98,9 +98,9 @@ struct PrefillParams {
     float4* split_o;
     float2* split_ml;
     Cap cap;                     // capped scores (instances with CAP)
-    // 4-bit pages: the call's history as bf16 pages in the workspace, and their
-    // table [sequence of the call][KV head][max_pages_unit] (null otherwise)
-    const int32_t* hist_ptab;
+    // instances with ROWS: the first row of each unit's history, [sequence of
+    // the call][KV head]
+    const int32_t* hist_row;
     int32_t seq[kMaxCallSeqs];
     int32_t n_b[kMaxCallSeqs];   // tokens held before the chunk
     int32_t cnt[kMaxCallSeqs];   // chunk rows
@@ -164,8 +164,7 @@ __device__ __forceinline__ Item load_item(const PrefillParams& p, const int4* it
     const int64_t urow = g.unit_row(seq, p.layer, m.kvh);
     m.pol = p.meta.pol[urow];
     m.idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + m.pol.idx_off;
-    m.ptab = p.hist_ptab ? p.hist_ptab + ((int64_t)m.b * g.hkv + m.kvh) * g.max_pages_unit
-                         : p.meta.ptab + urow * g.max_pages_unit;
+    m.ptab = p.meta.ptab + urow * g.max_pages_unit;
     return m;
 }
 
@@ -228,9 +227,12 @@ __device__ __forceinline__ uint32_t lowmask32(int32_t n) {
     return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : ((1u << n) - 1u);
 }
 
-// PT: the page size, or 0 to read it from the geometry (capped scores: one
-// instance for every page size).
-template <int D, int PT, bool F8, bool TWO = false, bool SPEC = false, bool CAP = false>
+// PT: the page size, or 0 to read it from the geometry (capped scores and ROWS:
+// one instance for every page size).  ROWS: a unit's history lies in
+// consecutive rows of tmKp and tmVp (4-bit pages, converted by sp_dequant.cu),
+// so a history tile is one box like a chunk tile, without page look-ups.
+// (2,048 rows after 16,384, every head GLOBAL, page 64: 505 us, 574 page by page.)
+template <int D, int PT, bool F8, bool TWO = false, bool SPEC = false, bool CAP = false, bool ROWS = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -339,10 +341,16 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     tma_load_2d(sQ + t * S::kQBytes + hf * S::kHalfBytes, &tmQ, q_full,
                                 (it.h0 + t) * D + hf * 64, (int32_t)it.row_base);
             ++q_loads;
+            const int32_t row0 = ROWS ? p.hist_row[it.b * g.hkv + it.kvh] : 0;
             // L2 prefetch of K/V tiles kPrefetchTiles ahead of their loads (a
             // prefetch of the next item's Q measured 1-2 % slower)
             auto prefetch_tile = [&](const KvTile& pk) {
-                if (!pk.paged) {
+                if (ROWS && pk.paged) {
+                    for (int hf = 0; hf < S::kHalves; ++hf) {
+                        tma_prefetch_2d(&tmKp, hf * 64, row0 + (int32_t)pk.start);
+                        tma_prefetch_2d(&tmVp, hf * 64, row0 + (int32_t)pk.start);
+                    }
+                } else if (!pk.paged) {
                     const int32_t y = (int32_t)(it.key_row0 + (pk.start - it.n_b));
                     for (int hf = 0; hf < S::kHalves; ++hf) {
                         tma_prefetch_2d(&tmK, it.kvh * D + hf * 64, y);
@@ -380,7 +388,12 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     if (rd > 0 && !mbar_wait(&kv_empty[st], (rd - 1) & 1, abort_flag, status)) { ok = false; break; }
                     stage_keys[st] = kt.nkeys;
                     uint8_t* dst = sKV + st * S::kKVBytes;
-                    if (!kt.paged) {
+                    if (ROWS && kt.paged) {
+                        mbar_arrive_expect_tx(&kv_full[st], S::kKVBytes);
+                        for (int hf = 0; hf < S::kHalves; ++hf)
+                            tma_load_2d(dst + hf * S::kHalfBytes, kv ? &tmVp : &tmKp, &kv_full[st], hf * 64,
+                                        row0 + (int32_t)kt.start);
+                    } else if (!kt.paged) {
                         mbar_arrive_expect_tx(&kv_full[st], S::kKVBytes);
                         const int32_t y = (int32_t)(it.key_row0 + (kt.start - it.n_b));
                         for (int hf = 0; hf < S::kHalves; ++hf)
@@ -769,6 +782,11 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                             vm[w] = b;
                         }
                     }
+                    // Most of a LOCAL ring's tiles are seen whole by a warp's rows:
+                    // only their break and the window's edge need the selects below
+                    // (five short capped chunks: 61 us with selects everywhere, 56).
+                    const bool all_seen = masked ? __all_sync(0xffffffffu, (vm[0] & vm[1] & vm[2] & vm[3]) == 0xffffffffu)
+                                                 : kt.nkeys == 128;
                     if constexpr (CAP) {
                         // A capped score lies in [-cap, cap], so the exponentials
                         // need no running maximum: they are taken against the fixed
@@ -793,7 +811,7 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // here (the same with the loops unrolled and the next columns
                         // loaded ahead: 269 and 289 us; all 128 columns in registers: 272).
                         uint32_t ra[32];
-                        const bool fast = !masked && kt.nkeys == 128;
+                        const bool fast = all_seen;
                         // visibility bits of columns 32 w .. 32 w + 31
                         auto bits = [&](int w) { return w < 2 ? (w ? vm[1] : vm[0]) : w == 2 ? vm[2] : vm[3]; };
                         float far[4] = {0.f, 0.f, 0.f, 0.f};      // largest |visible score|
@@ -899,7 +917,7 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     // for every tile width keeps the loop small.
                     uint32_t sr[128];
                     tmem_ld128(tS, sr);
-                    const bool fast = !masked && kt.nkeys == 128;
+                    const bool fast = all_seen;
                     if (!fast) {
                         // invisible or absent columns -> -inf, once (branch-free)
                         #pragma unroll
@@ -1151,29 +1169,33 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
 static_assert(sizeof(PrefillParams) + 5 * sizeof(CUtensorMap) <= 32764,
               "prefill parameters exceed the kernel parameter space");
 
-template <int D, int P, bool F8 = false, bool TWO = false, bool SPEC = false, bool CAP = false>
+template <int D, int P, bool F8 = false, bool TWO = false, bool SPEC = false, bool CAP = false, bool ROWS = false>
 cudaError_t launch_prefill_t(sp_cache* c, const PrefillParams& p, int grid,
                              const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              cudaStream_t s) {
     using Sh = PfShape<D, F8>;
-    bool& checked = c->prefill_checked[(CAP ? 5 : 0) + (SPEC ? 4 : TWO ? 3 : F8 ? 2 : D == 128)][P == 0 || P == 16 ? 0 : P == 32 ? 1 : P == 64 ? 2 : 3];
+    bool& checked = c->prefill_checked[(CAP ? 5 : 0) + (SPEC ? 4 : TWO ? 3 : F8 ? 2 : D == 128)][ROWS ? 4 : P == 0 || P == 16 ? 0 : P == 32 ? 1 : P == 64 ? 2 : 3];
     if (!checked) {   // once per cache and kernel instance
         cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, P, F8, TWO, SPEC, CAP>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, k_prefill<D, P, F8, TWO, SPEC, CAP, ROWS>);
         if (e != cudaSuccess) return e;
         // The setmaxnreg split assumes exactly kLaunchRegs registers per thread
         // at launch; anything else could leave an increase waiting forever.
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(k_prefill<D, P, F8, TWO, SPEC, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        e = cudaFuncSetAttribute(k_prefill<D, P, F8, TWO, SPEC, CAP, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
         if (e != cudaSuccess) return e;
         checked = true;
     }
-    k_prefill<D, P, F8, TWO, SPEC, CAP><<<grid, kPfThreads, Sh::kSmem, s>>>(p, tq, tk, tv, c->tm_kpool, c->tm_vpool);
+    k_prefill<D, P, F8, TWO, SPEC, CAP, ROWS><<<grid, kPfThreads, Sh::kSmem, s>>>(p, tq, tk, tv, c->tm_kpool, c->tm_vpool);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// History in rows (sp_prefill_rows.cu).
+cudaError_t launch_prefill_rows(sp_cache* c, const PrefillParams& p, int grid, bool two, bool spec,
+                                const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                cudaStream_t s);
 // Capped scores (sp_prefill_capped.cu).
 cudaError_t launch_prefill_capped(sp_cache* c, const PrefillParams& p, int grid, bool two,
                                   const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
