@@ -271,6 +271,7 @@ struct DequantParams {
     Meta meta;
     Geo geo;
     int32_t layer, unit0, n_units;
+    int32_t scaled;              // channel scales other than 1 may be set
     const uint8_t *kpool, *vpool;
     __nv_bfloat16 *k, *v;
     int32_t* row0;               // [max_batch][hkv] first row of a unit's copies

@@ -395,6 +395,7 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     dp->meta = c->meta;
     dp->geo = c->geo;
     dp->layer = layer;
+    dp->scaled = c->h_scaled[layer];
     dp->kpool = reinterpret_cast<const uint8_t*>(c->kpool);
     dp->vpool = reinterpret_cast<const uint8_t*>(c->vpool);
     dp->k = c->ws.deq_k;

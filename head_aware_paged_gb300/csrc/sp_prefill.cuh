@@ -231,7 +231,7 @@ __device__ __forceinline__ uint32_t lowmask32(int32_t n) {
 // one instance for every page size).  ROWS: a unit's history lies in
 // consecutive rows of tmKp and tmVp (4-bit pages, converted by sp_dequant.cu),
 // so a history tile is one box like a chunk tile, without page look-ups.
-// (2,048 rows after 16,384, every head GLOBAL, page 64: 505 us, 574 page by page.)
+// (2,048 rows after 16,384, every head GLOBAL, page 64: 498 us, 567 page by page.)
 template <int D, int PT, bool F8, bool TWO = false, bool SPEC = false, bool CAP = false, bool ROWS = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
 k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
