@@ -251,16 +251,21 @@ Cap make_cap(float score_cap, int head_dim) {
     r.a = (float)a;
     r.b = (float)(2.0 * a);
     r.ref = (float)std::min(a, 118.0 - a);
-    // least maximum error of y (c0 + c1 y^2 + c2 y^4 + c3 y^6) against tanh on
-    // [0, 1/2] (reweighted least squares): 1.3e-7
-    const double c[4] = {0.9999976758624189, -0.33320653872214767, 0.13145132556115224, -0.043372130570534975};
+    // least maximum error of y (c0 + c1 y^2 + ...) against tanh on [0, to]
+    // (reweighted least squares, a linear program): 1.3e-7 each
+    const double to[3] = {0.105, 0.275, 0.5};
+    const double c[3][4] = {{0.99999434430257206, -0.33143050206265212},
+                            {0.99999760489438916, -0.33306901049121052, 0.12634636124134371},
+                            {0.9999976758624189, -0.33320653872214767, 0.13145132556115224, -0.043372130570534975}};
     const double y = 1.0 / ((double)score_cap * std::sqrt((double)head_dim));    // y = x * this
-    double power = a * y;
-    for (int i = 0; i < 4; ++i) {
-        r.poly[i] = (float)(c[i] * power);
-        power *= y * y;
+    for (int n = 0; n < 3; ++n) {
+        double power = a * y;
+        for (int i = 0; i < n + 2; ++i) {
+            r.poly[n][i] = (float)(c[n][i] * power);
+            power *= y * y;
+        }
+        r.limit[n] = (float)(to[n] / y);
     }
-    r.limit = (float)(0.5 / y);
     return r;
 }
 

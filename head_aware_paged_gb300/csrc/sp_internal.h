@@ -65,9 +65,9 @@ struct CallSeqs {
 struct Cap {
     int32_t on;
     float k1, a, b;
-    // prefill: the exponentials' fixed reference; a tanh(y) as an odd polynomial
-    // of the raw product for |y| <= 1/2, |x| <= limit
-    float ref, limit, poly[4];
+    // prefill: the exponentials' fixed reference; a tanh(y) as odd polynomials
+    // of the raw product x, of 2, 3 and 4 terms for |x| <= limit[0 .. 2]
+    float ref, limit[3], poly[3][4];
 };
 Cap make_cap(float score_cap, int head_dim);
 constexpr float kMinScoreCap = 1.f / 64.f, kMaxScoreCap = 64.f;

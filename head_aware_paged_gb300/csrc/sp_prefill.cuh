@@ -38,6 +38,8 @@
 // Every wait is bounded (sp_device.cuh); on a time-out the CTA drains its
 // copies and MMAs, frees TMEM and returns with the status word set.
 #pragma once
+#include <type_traits>
+
 #include "sp_device.cuh"
 #include "sp_internal.h"
 #include "sp_plan.h"
@@ -828,7 +830,9 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                             for (int e = 0; e < 16; ++e)
                                 far[e & 3] = fmax3_abs(far[e & 3], __uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1]));
                         }
-                        const bool wide = __any_sync(0xffffffffu, fmax3(fmaxf(far[0], far[1]), far[2], far[3]) > p.cap.limit);
+                        // the warp's largest (its bits order as integers: it is not negative)
+                        const float top_x = __uint_as_float(__reduce_max_sync(
+                            0xffffffffu, __float_as_uint(fmax3(fmaxf(far[0], far[1]), far[2], far[3]))));
                         uint64_t rsum2[4] = {0ull, 0ull, 0ull, 0ull};
                         auto row = [&](auto&& quarter) {
                             #pragma unroll 1
@@ -851,24 +855,33 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                                 tmem_st16(tS + w * 16, pk);
                             }
                         };
-                        if (!wide) {
+                        auto odd = [&](auto terms, const float (&cf)[4]) {
+                            constexpr int N = decltype(terms)::value;
                             const uint64_t nref = pack_f32x2(-p.cap.ref, -p.cap.ref);
-                            const uint64_t c0 = pack_f32x2(p.cap.poly[0], p.cap.poly[0]);
-                            const uint64_t c1 = pack_f32x2(p.cap.poly[1], p.cap.poly[1]);
-                            const uint64_t c2 = pack_f32x2(p.cap.poly[2], p.cap.poly[2]);
-                            const uint64_t c3 = pack_f32x2(p.cap.poly[3], p.cap.poly[3]);
+                            uint64_t c[N];
+                            #pragma unroll
+                            for (int n = 0; n < N; ++n) c[n] = pack_f32x2(cf[n], cf[n]);
                             row([&](const uint32_t (&sx)[32], float (&pv)[32]) {
                                 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
                                     const uint64_t x = pack_u32x2(sx[2 * e], sx[2 * e + 1]);
                                     const uint64_t tt = mul_f32x2(x, x);
-                                    const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(c3, tt, c2), tt, c1), tt, c0);
+                                    uint64_t y = c[N - 1];
+                                    #pragma unroll
+                                    for (int n = N - 2; n >= 0; --n) y = fma_f32x2(y, tt, c[n]);
                                     float x0, x1;
                                     unpack_f32x2(fma_f32x2(x, y, nref), x0, x1);
                                     pv[2 * e] = fast_exp2(x0);
                                     pv[2 * e + 1] = fast_exp2(x1);
                                 }
                             });
+                        };
+                        if (top_x <= p.cap.limit[0]) {
+                            odd(std::integral_constant<int, 2>(), p.cap.poly[0]);
+                        } else if (top_x <= p.cap.limit[1]) {
+                            odd(std::integral_constant<int, 3>(), p.cap.poly[1]);
+                        } else if (top_x <= p.cap.limit[2]) {
+                            odd(std::integral_constant<int, 4>(), p.cap.poly[2]);
                         } else {
                             const float top = p.cap.a - p.cap.ref;
                             const uint64_t topx2 = pack_f32x2(top, top);

@@ -158,6 +158,36 @@ def test_extreme_scores_decode(d, cap):
     assert cache.status() == 0
 
 
+@pytest.mark.parametrize("cap", [0.5, 1.0, 50.0, 64.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_cap_pointwise(d, cap):
+    """Each row sees one key, so lse is the capped score itself: every warp of
+    32 rows stays below another multiple of the cap.  The score is one product
+    (exact) times 1 / sqrt(d).  Tolerance: 1.3e-7 cap of the approximation;
+    fp32 roundings, in log2 units, of the reference ref and of sums up to ref
+    + 2 a (a = cap log2 e, 2^-24 each, 16 of them); 2^-21 of exp2 and log2."""
+    gpu_ready()
+    tops = [0.02, 0.1, 0.11, 0.2, 0.27, 0.29, 0.45, 0.52, 0.8, 1.5, 4.0, 30.0]
+    n = 32 * len(tops)
+    cache = _mk(1, 1, d, 16, 1, n, 40)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(L, 0, 1)]]))
+    y = torch.cat([torch.linspace(-t, t, 32, dtype=torch.float64) for t in tops])
+    q = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros_like(q)
+    q[:, 0, 1] = (y * cap * math.sqrt(d) / 3).to(torch.bfloat16).cuda()
+    k[:, 0, 1] = 3.0
+    v = W.normal((n, 1, d), 3, device="cuda")
+    out, lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)
+    want = cap * torch.tanh(q[:, 0, 1].double() * 3 / math.sqrt(d) / cap)
+    a = cap * math.log2(math.e)
+    tol = 1.3e-7 * cap + 16 * 2.0 ** -24 * (abs(118 - a) if 118 - a < a else a) + 32 * 2.0 ** -24 * a + 2.0 ** -21
+    worst = ((lse[:, 0].double() - want).abs() / tol).max().item()
+    assert worst <= 1.0, worst
+    # one weight: P / l is 1 but for P's rounding to bf16, then the output's
+    assert ((out.double() - v.double()).abs() <= 2.0 ** -7 * 1.01 * v.double().abs()).all()
+    assert cache.status() == 0
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("cap,qs", [(50.0, 1.0), (2.0, 12.0)])
 def test_nan_query_stays_in_its_row(kv, cap, qs):
