@@ -803,15 +803,19 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // reciprocal of 1 - 2 / (1 + e^2y) would cost more than all the
                         // rest (8K layer: 323 us).  While every |y| of the warp's tile is
                         // at most 1/2 (scores up to half the cap), tanh is an odd
-                        // polynomial of degree 7 (1.3e-7 off at most), five FMA-pipe
-                        // operations on raw scores; otherwise the tile takes the formula,
-                        // its reciprocal by Newton's iteration.
+                        // polynomial (1.3e-7 off at most) of degree 7, 5 or 3, five,
+                        // four or three FMA-pipe operations on raw scores; otherwise
+                        // the tile takes the formula, its reciprocal by Newton's
+                        // iteration.  (8K layer, scores within a tenth of the cap:
+                        // 238 us, 249 with degree 7 always; past half the cap 344.)
                         //
                         // The row is read from TMEM 32 columns at a time in two small
                         // loops, one for the largest |score|, one for P, which takes the
                         // place of columns already read: the instruction cache decides
                         // here (the same with the loops unrolled and the next columns
-                        // loaded ahead: 269 and 289 us; all 128 columns in registers: 272).
+                        // loaded ahead: 269 and 289 us; all 128 columns in registers:
+                        // 272; one loop that checks each 32 columns after the fact and
+                        // takes them again where the degree was too low: 272).
                         uint32_t ra[32];
                         const bool fast = all_seen;
                         // visibility bits of columns 32 w .. 32 w + 31
