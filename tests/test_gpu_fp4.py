@@ -188,6 +188,26 @@ def test_prefill_over_history(P, hq, hkv, n, c, scaled):
     assert cache.status() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,P,n,pages", [(4, 2, 16, 20, 4), (2, 1, 16, 1, 1), (3, 1, 128, 200, 2), (2, 2, 32, 32, 2)])
+def test_prefill_over_a_pool_smaller_than_a_tile(hq, hkv, P, n, pages):
+    """Every page of a small pool in use: the last unit's tile ends behind the
+    converted rows."""
+    gpu_ready()
+    c = 5
+    cache = _mk(hq, hkv, P, 1, n + c, pages)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+    hist = _kv(n, hkv, 3)
+    cache.build(0, 0, *hist)
+    q = W.normal((c, hq, D), 7, device="cuda")
+    k, v = _kv(c, hkv, 8)
+    for cap in (None, 20.0):
+        out, lse = cache.prefill(0, [0], [0, c], q, k, v, score_cap=cap)
+        ref = attend(q.double(), torch.cat([_stored(hist[0]), k.double()]), torch.cat([_stored(hist[1]), v.double()]),
+                     range(n, n + c), [(G, 0, 0, None)] * hkv, cap)
+        check(out, lse, ref, 2.0 ** -8, 0.0, "cap %s" % cap, cap)
+    assert cache.status() == 0
+
+
 def test_prefill_history_converted_in_several_passes():
     """More history than the workspace's bf16 copies hold: groups of units."""
     gpu_ready()
