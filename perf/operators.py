@@ -28,7 +28,6 @@ own = False
 
 DEV = "cuda"
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
-PAGES = {"bf16": 0, "fp8": 1, "fp4": 2}
 ROW_BYTES = {"bf16": 2.0, "fp8": 1.0, "fp4": 0.5625}     # per element, scales included
 
 
@@ -213,11 +212,12 @@ def prepare(case, seed):
     first, total = _layout(case)
     held = _held(case)
     if own:
-        from head_aware_paged_gb300 import GLOBAL, LOCAL, Config, Policy, SegPagedCache
+        from head_aware_paged_gb300 import GLOBAL, KV_BF16, KV_FP4, KV_FP8, LOCAL, Config, Policy, SegPagedCache
         cache = SegPagedCache(Config(
             num_layers=1, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=P, max_seqs=case["seqs"],
             max_seq_len=max(a + b for a, b in zip(hist, new)) + 1, num_pages=max(1, total),
-            max_tokens=max(max(held), cu[-1]), max_batch=case["seqs"], kv_dtype=PAGES[case["pages"]]))
+            max_tokens=max(max(held), cu[-1]), max_batch=case["seqs"],
+            kv_dtype={"bf16": KV_BF16, "fp8": KV_FP8, "fp4": KV_FP4}[case["pages"]]))
         if case["pages"] == "fp8":
             cache.set_kv_scales(0, scales[0].cpu().numpy(), scales[1].cpu().numpy())
         row = [Policy(GLOBAL) if h < case["globals"] else Policy(LOCAL, case["sink"], case["window"]) for h in range(hkv)]
