@@ -215,7 +215,7 @@ def prepare(case, seed):
         from head_aware_paged_gb300 import GLOBAL, KV_BF16, KV_FP4, KV_FP8, LOCAL, Config, Policy, SegPagedCache
         cache = SegPagedCache(Config(
             num_layers=1, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=P, max_seqs=case["seqs"],
-            max_seq_len=max(a + b for a, b in zip(hist, new)) + 1, num_pages=max(1, total),
+            max_seq_len=max([a + b for a, b in zip(hist, new)] + [case["window"], case["sink"]]) + 1, num_pages=max(1, total),
             max_tokens=max(max(held), cu[-1]), max_batch=case["seqs"],
             kv_dtype={"bf16": KV_BF16, "fp8": KV_FP8, "fp4": KV_FP4}[case["pages"]]))
         if case["pages"] == "fp8":
