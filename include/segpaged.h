@@ -199,8 +199,14 @@ sp_status sp_append_kv(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
  * A prompt chunk attends before it is stored (sp_attention_prefill wants its
  * keys rotated already); afterwards this call stores the unrotated rows, q null.
  * One launch, pages included; works for every page type and head class.  The
- * current device must be the cache's.  Captured into a graph, a replay writes
- * the same positions and pages again. */
+ * current device must be the cache's.
+ * Captured into a graph: a call that needs new pages is refused
+ * (SP_ERR_UNSUPPORTED; replays would take them from the free stack again).
+ * Another counts once, when it is captured, and keeps its positions and whether
+ * channel scales were set.  A replay writes them again wherever the head still
+ * keeps them, whatever else was appended or released in between, and no length
+ * shrinks; while a listed sequence holds fewer tokens than at the capture
+ * (released), nothing of it is written and the status word is set. */
 sp_status sp_append_kv_rope(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
                             int32_t n_seqs, const int32_t* cu_new, const int64_t* pos,
                             const void* q, int64_t q_stride, const void* k,

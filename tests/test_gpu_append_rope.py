@@ -305,3 +305,80 @@ def test_refusals_change_nothing():
     assert torch.equal(cache.k_pool(), before)
     assert cache.append_kv_rope(0, [0], [0, 0], q[:0], k[:0], v[:0]).shape == (0, hq, d)
     assert cache.status() == 0
+
+
+def test_captured_call_that_needs_pages_is_refused():
+    """Pages are taken from the free stack when the kernel runs; a replay would
+    take whatever lies there by then.  The refused call changes nothing."""
+    gpu_ready()
+    from head_aware_paged_gb300 import SegPagedError
+    hq, hkv, d, P = 4, 2, 64, 16
+    cache = _mk(hq, hkv, d, P, 2, 128, 40)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G), W.HeadPolicy(L, 4, 20)]]))
+    q, k, v = _fused(80, hq, hkv, d, 4)
+    cache.append_kv_rope(0, [0], [0, 50], q, k, v)
+    free, before = cache.free_pages(), cache.k_pool().clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        with pytest.raises(SegPagedError) as e:
+            cache.append_kv_rope(0, [0], [0, 20], q[50:], k[50:], v[50:])      # 50 + 20 tokens: a fifth page
+        q[:1].clone()
+    assert e.value.status == 3
+    assert cache.seq_len(0, 0) == 50 and cache.free_pages() == free
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_pool(), before)
+    cache.append_kv_rope(0, [0], [0, 20], q[50:], k[50:], v[50:])
+    assert cache.seq_len(0, 0) == 70 and cache.free_pages() == free - 1
+    assert cache.status() == 0
+
+
+def test_replay_after_other_sequences_and_its_own_moved_on():
+    """Between replays other sequences take and release pages and the written one
+    grows past its ring: a replay still writes only its positions that are held,
+    and leaves lengths, tables and every other row alone.  After a release of
+    its sequence it writes nothing and says so."""
+    gpu_ready()
+    from head_aware_paged_gb300 import SegPagedError
+    hq, hkv, d, P = 4, 3, 64, 16
+    cache = _mk(hq * 3, hkv, d, P, 3, 256, 80)
+    pol = [[W.HeadPolicy(G), W.HeadPolicy(L, 4, 20), W.HeadPolicy(R, idx=np.arange(0, 256, 3, dtype=np.int32))]]
+    for s in range(3):
+        cache.set_policy(s, to_c_policies(pol))
+    q, k, v = _fused(200, hq * 3, hkv, d, 4)
+    cache.append_kv_rope(0, [0, 1], [0, 50, 120], q, k, v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = cache.append_kv_rope(0, [0], [0, 10], q[50:60], k[50:60], v[50:60])
+    graph.replay()
+    torch.cuda.synchronize()
+    for grow in (30, 60):                       # to 90 tokens (50 .. 59 still in the ring), to 150 (behind it)
+        cache.release(1)
+        cache.append_kv_rope(0, [2, 0], [0, 40, 40 + grow], q, k, v)
+        cache.append_kv_rope(0, [1], [0, 33], q, k, v)
+        n = cache.seq_len(0, 0)
+        pools = cache.k_pool().clone(), cache.v_pool().clone()
+        tables = [cache.export_table(b, 0, h) for b in range(3) for h in range(hkv)]
+        free = cache.free_pages()
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _close(got, _turn(q[50:60], 50 + np.arange(10)), "replayed")
+        assert torch.equal(cache.k_pool(), pools[0]) and torch.equal(cache.v_pool(), pools[1])
+        assert tables == [cache.export_table(b, 0, h) for b in range(3) for h in range(hkv)]
+        assert cache.free_pages() == free and cache.seq_len(0, 0) == n
+    assert cache.status() == 0
+    cache.release(0)
+    cache.append_kv_rope(0, [1], [0, 60], q, k, v)          # takes the pages that were sequence 0's
+    pools = cache.k_pool().clone(), cache.v_pool().clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k_pool(), pools[0]) and torch.equal(cache.v_pool(), pools[1])
+    with pytest.raises(SegPagedError) as e:
+        cache.status()
+    assert e.value.status == 5
+    assert cache.status() == 0 and cache.export_table(0, 0, 0) == ([], [])
