@@ -431,6 +431,15 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     return SP_OK;
 }
 
+// Does one of `rows` rows of `len` bytes, `stride` bytes apart from `base` on,
+// meet [lo, hi)?
+bool rows_meet(const void* base, int64_t stride, int64_t len, int64_t rows, uintptr_t lo, uintptr_t hi) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base);
+    const int64_t d = (int64_t)(lo - b) - len;          // the first row that ends behind lo
+    const int64_t r = d < 0 ? 0 : d / stride + 1;
+    return r < rows && b + (uintptr_t)(r * stride) < hi;
+}
+
 }  // namespace
 
 }  // namespace sp
@@ -463,6 +472,15 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
          reinterpret_cast<uintptr_t>(q_out)) & 15)
         return fail(SP_ERR_INVALID_ARG, "q, k, v and q_out must be 16-byte aligned");
+    if (q && cu_new[n_seqs] > 0) {
+        // a block reads its rows while others write theirs: no overlap but a row with itself
+        const int64_t rows = cu_new[n_seqs], row = (int64_t)c->cfg.num_q_heads * d;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(q_out), hi = lo + (uintptr_t)(rows * row * 2);
+        const bool in_place = q == q_out && (q_stride == row || rows == 1);
+        if ((!in_place && rows_meet(q, q_stride * 2, row * 2, rows, lo, hi)) ||
+            rows_meet(k, k_stride * 2, kv * 2, rows, lo, hi) || rows_meet(v, v_stride * 2, kv * 2, rows, lo, hi))
+            return fail(SP_ERR_INVALID_ARG, "q_out overlaps q, k or v (it may be q itself if q is contiguous)");
+    }
     if (!inv_freq && (!(rope_theta > 0.0) || !std::isfinite(rope_theta)))
         return fail(SP_ERR_INVALID_ARG, "rope_theta must be positive and finite");
     // frequencies as fractions of a turn, modulo one turn (whole turns a

@@ -195,7 +195,8 @@ sp_status sp_append_kv(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
  *   q [cu_new[n_seqs]] rows of num_q_heads * head_dim elements q_stride apart,
  *     k and v likewise with num_kv_heads (strides in elements, multiples of 8,
  *     at least a row); all 16-byte aligned.  q and q_out may both be null: keys
- *     and values only.  q_out is contiguous; it may be q itself if q is.
+ *     and values only.  q_out is contiguous; it may be q itself if q is, and
+ *     overlaps the inputs in no other way.
  * A prompt chunk attends before it is stored (sp_attention_prefill wants its
  * keys rotated already); afterwards this call stores the unrotated rows, q null.
  * One launch, pages included; works for every page type and head class.  The

@@ -382,3 +382,31 @@ def test_replay_after_other_sequences_and_its_own_moved_on():
         cache.status()
     assert e.value.status == 5
     assert cache.status() == 0 and cache.export_table(0, 0, 0) == ([], [])
+
+
+def test_q_out_may_not_overlap_what_is_read():
+    """q_out may be q itself where q is contiguous; any other overlap with the
+    inputs would be a race and is refused."""
+    gpu_ready()
+    from head_aware_paged_gb300 import SegPagedError
+    hq, hkv, d, n = 4, 2, 64, 10
+    cache = _mk(hq, hkv, d, 16, 1, 128, 20)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+    flat = W.normal((n * (hq + 2 * hkv) * d,), 1, device="cuda")
+    x = flat.view(n, hq + 2 * hkv, d)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    before = flat.clone()
+    size = n * hq * d
+    for q_in, off in ((q, 0), (q, 3 * d), (q, flat.numel() - size), (flat[:size].view(n, hq, d), d)):
+        with pytest.raises(SegPagedError) as e:
+            cache.append_kv_rope(0, [0], [0, n], q_in, k, v, q_out=flat[off:off + size].view(n, hq, d))
+        assert e.value.status == 1 and cache.seq_len(0, 0) == 0
+    assert torch.equal(flat, before)
+    own = q.contiguous()
+    got = cache.append_kv_rope(0, [0], [0, n], own, k, v, q_out=own)
+    _close(got, _turn(q, np.arange(n)), "in place")
+    big = torch.empty(2 * size, dtype=torch.bfloat16, device="cuda")         # side by side: no overlap
+    big[:size] = q.reshape(-1)
+    got = cache.append_kv_rope(0, [0], [0, n], big[:size].view(n, hq, d), k, v, q_out=big[size:].view(n, hq, d))
+    _close(got, _turn(q, np.arange(n, 2 * n)), "side by side")
+    assert cache.status() == 0
