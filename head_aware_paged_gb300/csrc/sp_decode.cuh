@@ -73,8 +73,9 @@ __device__ __forceinline__ int64_t cta_of_item(int64_t x, int64_t T, int G) {
 // A raw product q . k in log2 units of the softmax, capped by a tanh
 // (Cap, sp_internal.h): two MUFU operations on top of the exponential's one,
 // hidden behind the page stream.
-__device__ __forceinline__ float capped_log2(float x, const Cap& cap) {
-    return cap.a - __fdividef(cap.b, 1.f + fast_exp2(x * cap.k1));
+// y: the product times cap.k1.
+__device__ __forceinline__ float capped_log2(float y, const Cap& cap) {
+    return cap.a - __fdividef(cap.b, 1.f + fast_exp2(y));
 }
 
 template <int D, int P, bool F8, bool CAP>
@@ -357,7 +358,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                 for (int nt = 0; nt < NT; ++nt)
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if constexpr (CAP) sc[nt][e] = capped_log2(sc[nt][e], p.cap);
+                        if constexpr (CAP) sc[nt][e] = capped_log2(sc[nt][e] * p.cap.k1, p.cap);
                         else sc[nt][e] *= p.scale_log2;
                         mx[e >> 1] = fmaxf(mx[e >> 1], sc[nt][e]);
                     }
@@ -367,7 +368,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = key0 + nt * 8 + qc + (e & 1);
-                        float v = CAP ? capped_log2(sc[nt][e], p.cap) : sc[nt][e] * p.scale_log2;
+                        float v = CAP ? capped_log2(sc[nt][e] * p.cap.k1, p.cap) : sc[nt][e] * p.scale_log2;
                         if (key < lo || key >= hi) v = -INFINITY;
                         sc[nt][e] = v;
                         mx[e >> 1] = fmaxf(mx[e >> 1], v);

@@ -26,10 +26,11 @@
 //     codes of a K fragment lie in two blocks and of a V fragment in one, so
 //     one 32-bit word holds its scales of a group.  V codes of two keys are
 //     interleaved by two bit selects per eight pairs before the conversion.
-//   * Channel scales: K's are folded into the query (as f16), V's into the
-//     finished sums.  Scores, maxima, sums and outputs are fp32; P and the
-//     scaled queries are rounded to f16 once (2^-12 relative, next to the
-//     output's 2^-9).
+//   * Channel scales: K's are folded into the query, V's into the finished
+//     sums.  Scores, maxima, sums and outputs are fp32; what the matrix
+//     instructions take is f16, rounded once (2^-11 relative at most, next to
+//     the bf16 output's 2^-8): P, and the query under channel scales that are
+//     not powers of two.  A power of two per head keeps the query in f16's range.
 #pragma once
 #include <algorithm>
 
@@ -155,6 +156,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
     float2* unit_ml = entry_ml + 2 * kD4Warps * group;                              // [2 warps][group]
     float* entry_weight = reinterpret_cast<float*>(unit_ml + 2 * kD4Warps * group); // [2 warps][group]
     __shared__ uint64_t full[2 * kD4Warps];          // K and V of each warp's stage landed
+    __shared__ __align__(8) float score_scale[kD4Warps][8 * NH];   // each head's factor of its products
     __shared__ int abort_word, flag_last[2], entry_unit[2 * kD4Warps], list[2 * kD4Warps], n_list;
     volatile int* abort_flag = &abort_word;
 
@@ -273,21 +275,38 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
         const float* ks = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
         const float* vs = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
         if (it > 0) load_q(u);
+        // The query enters the products as f16, times a power of two per head
+        // that takes the largest |q * channel scale| to 2^14 .. 2^15: exactly
+        // where the product has f16's bits and lies within 2^-28 of it, however
+        // small or large the scales and the query are; the scores are multiplied
+        // back in fp32.
         #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
+            float x[8][2][2], top = 0.f;
             #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
                 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(&qraw[nh][kk][e]);
-                    float q0 = __low2float(v2), q1 = __high2float(v2);
+                    x[kk][e][0] = __low2float(v2);
+                    x[kk][e][1] = __high2float(v2);
                     if (p.scaled) {
-                        const int cc = j * 32 + kk * 4 + 2 * e;
-                        q0 *= __ldg(ks + cc);
-                        q1 *= __ldg(ks + cc + 1);
+                        const float2 f = __ldg(reinterpret_cast<const float2*>(ks + j * 32 + kk * 4 + 2 * e));
+                        x[kk][e][0] *= f.x;
+                        x[kk][e][1] *= f.y;
                     }
-                    qb[nh][kk][e] = pack_f16(q0, q1);
+                    top = fmax3_abs(top, x[kk][e][0], x[kk][e][1]);
                 }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = min(max(__float_as_int(top) >> 23, 15), 254);     // 2^(ex - 127) <= top
+            const float up = __int_as_float((268 - ex) << 23), down = __int_as_float((ex - 14) << 23);
+            #pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                #pragma unroll
+                for (int e = 0; e < 2; ++e) qb[nh][kk][e] = pack_f16(x[kk][e][0] * up, x[kk][e][1] * up);
+            // (this lane's query is head gl, its scores are heads 2 j and 2 j + 1's)
+            if (j == 0) score_scale[warp][nh * 8 + gl] = down * (CAP ? p.cap.k1 : p.scale_log2);
             m_run[nh][0] = m_run[nh][1] = -INFINITY;
             l_run[nh][0] = l_run[nh][1] = 0.f;
             #pragma unroll
@@ -295,6 +314,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nh][mt][e] = 0.f;
         }
+        __syncwarp();
         for (; it < stop; ++it) {
             if (dead) continue;
             const uint32_t parity = it & 1;
@@ -339,12 +359,16 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
             __syncwarp();
             if (more) { take(it + 1); load(0); }
             #pragma unroll
-            for (int q = 0; q < kD4Groups; ++q)
+            for (int nh = 0; nh < NH; ++nh) {
+                const float2 f = *reinterpret_cast<const float2*>(&score_scale[warp][nh * 8 + 2 * j]);
                 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh)
+                for (int q = 0; q < kD4Groups; ++q)
                     #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[q][nh][e] = CAP ? capped_log2(sc[q][nh][e], p.cap) : sc[q][nh][e] * p.scale_log2;
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = sc[q][nh][e] * ((e & 1) ? f.y : f.x);
+                        sc[q][nh][e] = CAP ? capped_log2(x, p.cap) : x;
+                    }
+            }
             if (lo > 0 || hi < kFp4ItemSlots) {
                 #pragma unroll
                 for (int q = 0; q < kD4Groups; ++q) {

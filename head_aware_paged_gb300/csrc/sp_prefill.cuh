@@ -210,12 +210,6 @@ __device__ __forceinline__ float fmin_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// max(|a|, |b|, |c|).
-__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
-    float r;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 // max(a, b, c) in one instruction (three-input max.f32, sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

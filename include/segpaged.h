@@ -115,7 +115,7 @@ typedef struct sp_config {
  * x * (1 / channel scale) is what the block quantises, and the stored value is
  * code * scale * channel scale.  Every call that takes a cache takes such a
  * one: decode multiplies code * scale (exact in f16) with q * channel scale
- * in f16, prefill reads bf16(code * scale * channel scale) from copies that it
+ * in f16 (times a power of two per head that keeps it in range), prefill reads bf16(code * scale * channel scale) from copies that it
  * makes in the workspace, sp_rope_realign
  * dequantises, rotates and quantises again with new block scales, and a packed
  * row is its 64 code bytes (two dimensions a byte, the even one low), then its

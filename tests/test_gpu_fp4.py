@@ -388,3 +388,33 @@ def test_graph_replay():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("cap", [None, 50.0])
+@pytest.mark.parametrize("hq,hkv,P", [(8, 2, 64), (24, 2, 16), (3, 3, 32)])
+@pytest.mark.parametrize("which,qs", [("least", 0.05), ("least", 600.0), ("largest", 0.05), ("largest", 600.0),
+                                      ("mixed", 1.0), ("none", 1e-6), ("none", 1e6)])
+def test_decode_at_the_ends_of_the_scale_range(which, qs, hq, hkv, P, cap):
+    """Channel scales of 2^-14 and 128 and everything between, small and large
+    queries.  Powers of two, so that query times scale has bf16's 8 bits: it
+    enters the products exactly, but for elements 2^-28 below the head's largest
+    (mixed scales: 2^-11 of each product is allowed)."""
+    gpu_ready()
+    rng = np.random.default_rng(3)
+    ex = {"least": np.full((hkv, D), -14), "largest": np.full((hkv, D), 7), "mixed": rng.integers(-14, 8, (hkv, D)),
+          "none": np.zeros((hkv, D), int)}[which]
+    ks = np.exp2(ex).astype(np.float32)
+    lens = [1, 2, 3, 70, 500]
+    cache = _mk(hq, hkv, P, len(lens), 512, len(lens) * hkv * (512 // P + 2))
+    if which != "none":
+        cache.set_kv_scales(0, ks, np.ones((hkv, D), np.float32))
+    data = [_kv(n, hkv, 80 + b) for b, n in enumerate(lens)]
+    for b in range(len(lens)):
+        cache.set_policy(b, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+        cache.build(b, 0, *data[b])
+    q = (W.normal((len(lens), hq, D), 99, device="cuda").float() * qs).to(torch.bfloat16)
+    out, lse = cache.decode(0, list(range(len(lens))), q, score_cap=cap)
+    for b, n in enumerate(lens):
+        ref = attend(q[b:b + 1].double(), _stored(data[b][0], ks), _stored(data[b][1]), [n - 1], [(G, 0, 0, None)] * hkv, cap)
+        check(out[b:b + 1], lse[b:b + 1], ref, 2.0 ** -11, 2.0 ** -11 if which == "mixed" else 0.0, "seq %d" % b, cap)
+    assert cache.status() == 0
