@@ -55,11 +55,15 @@ SP_HD int fp4_v_scale(int s, int b) { return kFp4ScaleOff + b * 16 + (s & 3) * 4
 
 #if defined(__CUDACC__)
 
-// Scale code of a block whose largest magnitude is amax.  amax * fl(1/6) is
-// exact wherever amax / 6 is a tie between two scales (fl(1/6) is off by a
-// quarter of half a unit), so the product rounds like the quotient.
+// Scale code of a block whose largest magnitude is amax.  amax / 6 is amax times
+// the rounded sixth, corrected once by its residual: then it is a tie between
+// two scales only where amax is 6 times that tie.  (Any other amax is a step of
+// its own off, two thirds of the quotient's step at least; the product alone,
+// a quarter of a step too large, reached the tie 19/16 from just below.)
 __device__ __forceinline__ uint32_t fp4_scale_code(float amax) {
-    const float f = fminf(amax * 0.16666667163372039794921875f, kFp4MaxScale);
+    constexpr float kSixth = 0.16666667163372039794921875f;
+    const float a = fminf(amax, 6.f * kFp4MaxScale), q = a * kSixth;
+    const float f = __fmaf_rn(__fmaf_rn(-q, 6.f, a), kSixth, q);
     if (f < 6.103515625e-05f) return (uint32_t)__float2int_rn(f * 131072.f);   // below 2^-14: steps of 2^-17
     const uint32_t u = __float_as_uint(f);
     return ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3);            // 3 mantissa bits, ties to even

@@ -418,3 +418,40 @@ def test_decode_at_the_ends_of_the_scale_range(which, qs, hq, hkv, P, cap):
         ref = attend(q[b:b + 1].double(), _stored(data[b][0], ks), _stored(data[b][1]), [n - 1], [(G, 0, 0, None)] * hkv, cap)
         check(out[b:b + 1], lse[b:b + 1], ref, 2.0 ** -11, 2.0 ** -11 if which == "mixed" else 0.0, "seq %d" % b, cap)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("rope_path", [False, True])
+def test_scale_beside_a_tie(rope_path):
+    """Block maxima that are the fp32 number just below 6 * 19/16 (times a power
+    of two): amax / 6 lies below the tie of two scales, its nearest is 9/8.  They
+    come about as x * fp32(1 / channel scale), x and the scale searched for here."""
+    gpu_ready()
+    below = np.nextafter(np.float32(7.125), np.float32(0))
+    pairs = []
+    for m in range(128, 256):
+        x = np.float32(m / 128)
+        want = np.float32(float(below) / float(x))
+        for c in (want, np.nextafter(want, np.float32(0)), np.nextafter(want, np.float32(99))):
+            s = np.float32(1.0 / float(c))
+            for t in (s, np.nextafter(s, np.float32(0)), np.nextafter(s, np.float32(9))):
+                if x * (np.float32(1) / t) == below and len(pairs) < 8 and (not pairs or pairs[-1][0] != x):
+                    pairs.append((x, t))
+    assert len(pairs) == 8
+    cache = _mk(2, 1, 16, 1, 64, 8)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    s = np.ones((1, D), np.float32)
+    n = 24                                       # powers of two from 2^-12 (subnormal scales) to 2^11
+    k = np.zeros((n, 1, D), np.float32)
+    for b, (x, t) in enumerate(pairs):
+        s[0, 16 * b + 3] = t
+        k[:, 0, 16 * b + 3] = x * np.exp2(np.arange(n) - 12)
+    cache.set_kv_scales(0, s, s)
+    kt = torch.tensor(k, device="cuda").to(torch.bfloat16)
+    if rope_path:                                # no rotation: frequency 0
+        cache.append_kv_rope(0, [0], [0, n], None, kt, kt, inv_freq=[0.0] * (D // 2))
+    else:
+        cache.append_kv(0, [0], [0, n], kt, kt)
+    sc = fp4.quantize(f64(kt[:, 0]), s[0])[1]
+    assert (sc[12] == (15 << 3) + 1).all()       # 9/8
+    assert _check_codes(cache, 0, 0, 0, kt, kt, s, s) == n
+    assert cache.status() == 0
