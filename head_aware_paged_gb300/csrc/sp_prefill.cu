@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(128) k_prefill_merge(const __grid_constant__ M
                        pack_bf16(a[e + 4] * inv, a[e + 5] * inv), pack_bf16(a[e + 6] * inv, a[e + 7] * inv));
     if (p.lse && blockIdx.z == 0)
         p.lse[(int64_t)(gr.x + r) * p.hq + gr.y + t] =
-            L > 0.f ? (mx + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+            L == 0.f ? -INFINITY : (mx + __log2f(L)) * 0.69314718055994531f;   // NaN rows: NaN
 }
 
 static_assert(sizeof(MergeParams) <= 32764, "merge parameters exceed the kernel parameter space");

@@ -917,7 +917,7 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         #pragma unroll
                         for (int e2 = 0; e2 < 4; ++e2) unpack_f32x2(rsum2[e2], rsum[2 * e2], rsum[2 * e2 + 1]);
                         l += ((rsum[0] + rsum[1]) + (rsum[2] + rsum[3])) + ((rsum[4] + rsum[5]) + (rsum[6] + rsum[7]));
-                        m = l > 0.f ? p.cap.ref : -INFINITY;
+                        m = l == 0.f ? -INFINITY : p.cap.ref;       // (a NaN row saw something)
                         continue;
                     }
                     // S row of this thread, all 128 columns at once (the softmax
@@ -1162,7 +1162,7 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                 }
                 if (row_ok && p.lse)
                     p.lse[(it.row_base + r) * g.hq + head] =
-                        l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;   // NaN rows: NaN
             }
         }
     }

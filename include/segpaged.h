@@ -246,7 +246,8 @@ sp_status sp_attention_decode(sp_cache* cache, int32_t layer,
  * otherwise); everything else is as for sp_attention_prefill and
  * sp_attention_decode (lse is that of the capped scores).  In all four calls a
  * key that a row does not see, and a row of another sequence, may enter its
- * sums with the weight 0: k and v must be finite (a NaN in q stays in its row).
+ * sums with the weight 0: k and v must be finite (a NaN in q stays in its row,
+ * whose output and lse are NaN).
  * The current device must be the cache's. */
 sp_status sp_attention_prefill_capped(sp_cache* cache, int32_t layer,
                                       const int32_t* seq_ids, int32_t n_seqs,

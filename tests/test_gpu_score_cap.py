@@ -232,3 +232,31 @@ def test_uncapped_calls_keep_their_results_and_refusals():
         with pytest.raises(SegPagedError):
             cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("hist", [0, 7000])
+@pytest.mark.parametrize("cap", [None, 50.0, 2.0])
+def test_nan_query_has_a_nan_lse(cap, hist, kv):
+    """-inf says that a row saw nothing; a NaN row saw something.  Over a long
+    history the items are split and merged."""
+    gpu_ready()
+    hq, d, n = 2, 128, 140
+    cache = _mk(hq, 1, d, 64, 1, hist + n, (hist + n) // 64 + 4, kv)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(R, idx=np.arange(3, hist + n, dtype=np.int32))]]))
+    if hist:
+        cache.build(0, 0, *(W.normal((hist, 1, d), 5 + i, device="cuda") for i in range(2)))
+    q, k, v = (W.normal((n, h, d), 7 + h, device="cuda") for h in (hq, 1, 1))
+    q[[5, 130], 1, 3] = math.nan
+    out, lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)
+    hit = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    hit[[5, 130], 1] = True
+    none = torch.zeros_like(hit)
+    none[:max(0, 3 - hist)] = True
+    assert torch.equal(torch.isnan(lse), hit) and torch.equal(torch.isneginf(lse), none)
+    assert torch.equal(torch.isnan(out).all(-1), hit) and torch.equal(torch.isnan(out).any(-1), hit)
+    assert (out[none] == 0).all()
+    cache.append_kv(0, [0], [0, n], k, v)
+    out, lse = cache.decode(0, [0], q[130:131].contiguous(), score_cap=cap)
+    assert torch.isnan(lse[0]).tolist() == [False, True] and torch.isnan(out[0, 1]).all()
+    assert cache.status() == 0
