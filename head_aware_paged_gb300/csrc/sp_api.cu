@@ -250,7 +250,8 @@ Cap make_cap(float score_cap, int head_dim) {
     r.k1 = (float)(2.0 * log2e / ((double)score_cap * std::sqrt((double)head_dim)));
     r.a = (float)a;
     r.b = (float)(2.0 * a);
-    r.ref = (float)std::min(a, 118.0 - a);
+    // weights 2^(-a - ref) .. 2^(a - ref): 2^-98 at least, 2^86.7 at most
+    r.ref = (float)std::min(a, 98.0 - a);
     // least maximum error of y (c0 + c1 y^2 + ...) against tanh on [0, to]
     // (reweighted least squares, a linear program): 1.3e-7 each
     const double to[3] = {0.105, 0.275, 0.5};

@@ -786,9 +786,12 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     if constexpr (CAP) {
                         // A capped score lies in [-cap, cap], so the exponentials
                         // need no running maximum: they are taken against the fixed
-                        // reference ref = min(a, 118 - a) (a = cap log2 e <= 92.4),
-                        // between 2^-118 and 2^67, which fp32 sums and bf16 P hold at
-                        // full precision, and O is never rescaled.  Invisible columns
+                        // reference ref = min(a, 98 - a) (a = cap log2 e <= 92.4),
+                        // between 2^-98 and 2^87, and O is never rescaled.  fp32's
+                        // normal numbers are shared out: sums of weights times values
+                        // keep full precision for |v| from 2^-28 on, whatever the
+                        // scores, and stay finite for a million keys of |v| up to 2^20
+                        // (2^87 2^20 2^20).  Invisible columns
                         // are zeroed after the exponential (their capped score is
                         // finite too).
                         //

@@ -244,7 +244,9 @@ sp_status sp_attention_decode(sp_cache* cache, int32_t layer,
  * of score_cap * tanh(s / score_cap), s = q . k / sqrt(head_dim), over each
  * head's visible keys.  score_cap in [1/64, 64] (SP_ERR_INVALID_ARG
  * otherwise); everything else is as for sp_attention_prefill and
- * sp_attention_decode (lse is that of the capped scores).  In all four calls a
+ * sp_attention_decode (lse is that of the capped scores).  Prefill's sums are
+ * exact to fp32 for values of 2^-28 <= |v| <= 2^20 at every cap (a row whose
+ * scores all lie near -64 weighs smaller ones in fp32's subnormals).  In all four calls a
  * key that a row does not see, and a row of another sequence, may enter its
  * sums with the weight 0: k and v must be finite (a NaN in q stays in its row,
  * whose output and lse are NaN).

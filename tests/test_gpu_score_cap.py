@@ -260,3 +260,33 @@ def test_nan_query_has_a_nan_lse(cap, hist, kv):
     out, lse = cache.decode(0, [0], q[130:131].contiguous(), score_cap=cap)
     assert torch.isnan(lse[0]).tolist() == [False, True] and torch.isnan(out[0, 1]).all()
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("cap", [1.0, 30.0, 50.0, 64.0])
+@pytest.mark.parametrize("sign,vs", [(-1, 2.0 ** -28), (-1, 2.0 ** 18), (1, 2.0 ** -28), (1, 2.0 ** 18)])
+@pytest.mark.parametrize("d,hq", [(64, 1), (128, 2)])
+def test_small_and_large_values(d, hq, sign, vs, cap):
+    """Every score at -cap or at +cap, values around 2^-28 and 2^18: what weight
+    times value sums to stays inside fp32's normal range."""
+    gpu_ready()
+    n = 300
+    cache = _mk(hq, 1, d, 16, 1, 2 * n, 60)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[:, :, 0] = 1e15
+    q = torch.zeros(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = sign * 1e15
+    v = (W.normal((n, 1, d), 3, device="cuda").float() * vs).to(torch.bfloat16)
+
+    def held(rows, keys, values):
+        ref = attend(q[:len(rows)].double(), keys.double(), values.double(), rows, [(G, 0, 0, None)], cap)
+        return ref[:3] + (torch.zeros_like(ref[3]), ref[4])    # every score is +-cap, exactly
+
+    out, lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)
+    check(out, lse, held(range(n), k, v), 2.0 ** -8, 0.0, "prefill", cap)
+    cache.append_kv(0, [0], [0, n], k, v)
+    out, lse = cache.prefill(0, [0], [0, n], q, k, v, score_cap=cap)          # over history too
+    check(out, lse, held(range(n, 2 * n), torch.cat([k, k]), torch.cat([v, v])), 2.0 ** -8, 0.0, "history", cap)
+    out, lse = cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
+    check(out, lse, held([n - 1], k, v), 2.0 ** -8, 0.0, "decode", cap)
+    assert cache.status() == 0
