@@ -455,3 +455,27 @@ def test_scale_beside_a_tie(rope_path):
     assert (sc[12] == (15 << 3) + 1).all()       # 9/8
     assert _check_codes(cache, 0, 0, 0, kt, kt, s, s) == n
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("at", [0, 40, 63])
+def test_weights_far_below_the_largest(at):
+    """One key e^18 times as heavy as the 63 others of its item, its value zero:
+    the output is theirs alone.  P keeps weights down to half of 2^-24 of 2^7,
+    2^-32 of the largest (a reference at the maximum itself would drop them)."""
+    gpu_ready()
+    n = 64
+    cache = _mk(2, 1, 64, 1, 128, 4)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = torch.zeros(n, 1, D, dtype=torch.bfloat16, device="cuda")
+    k[at, 0, 0] = 6.0
+    v = torch.full_like(k, 6.0)
+    v[at] = 0.0
+    cache.build(0, 0, k, v)
+    q = torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda")
+    q[0, :, 0] = 34.0                            # 34 * 6 / sqrt(128) = 18.03
+    out, lse = cache.decode(0, [0], q)
+    o, z, A, _, S = attend(q.double(), _stored(k), _stored(v), [n - 1], [(G, 0, 0, None)])
+    tol = 2.0 ** -8 * o + 2.0 ** -14 * A + 2.0 ** -32 * S
+    assert (o > 4e-6).all() and ((out.double() - o).abs() <= tol).all()
+    assert ((lse.double() - z).abs() <= 2.0 ** -19 * (1 + z)).all()
+    assert cache.status() == 0
