@@ -101,10 +101,12 @@ Layout make_layout(const sp_config* c) {
     L.split_o = o;  o = align_up(o + (size_t)kPrefillSplitSlots * 2 * 128 * c->head_dim * 4, 256);
     L.split_ml = o; o = align_up(o + (size_t)kPrefillSplitSlots * 2 * 128 * 2 * 4, 256);
     if (c->kv_dtype == SP_KV_FP4_E2M1) {
-        // bf16 K and V of one prefill's history, up to 2 GiB at a time (at
-        // least one unit's, at most the pool's pages)
+        // bf16 K and V of one prefill's history, up to 2 GiB at a time: at least
+        // one unit's, at most what the units of a call (one layer's) can hold,
+        // and at most the pool's pages
         const int64_t page_bytes = (int64_t)c->page_size * c->head_dim * 2;
-        L.deq_pages = std::min<int64_t>(c->num_pages,
+        const int64_t call_pages = std::min<int64_t>(c->num_pages, L.max_counter_units * L.max_pages_unit);
+        L.deq_pages = std::min<int64_t>(call_pages,
                                         std::max<int64_t>(L.max_pages_unit, (int64_t(2) << 30) / (2 * page_bytes)));
         o = align_up(o, 1024);
         L.deq = o;     o = align_up(o + 2 * (size_t)L.deq_pages * page_bytes, 256);

@@ -130,8 +130,9 @@ typedef struct sp_cache sp_cache;  /* opaque host handle */
  *         [page_size / 16][1152] bytes, 16 rows' codes and their scales.
  *   meta: page tables, policies, retrieval lists, free-page stack, status.
  *   ws:   per-call scratch (prefill work list, decode split partials; FP4:
- *         also bf16 copies of a prefill's history, 2 GiB or the whole pool's
- *         rows if that is less, at least one unit's). */
+ *         also bf16 copies of a prefill's history: what max_batch sequences of
+ *         max_seq_len hold in one layer, the whole pool's rows or 2 GiB,
+ *         whichever is least, and at least one unit's). */
 sp_status sp_required_bytes(const sp_config* cfg, size_t* pool_bytes,
                             size_t* meta_bytes, size_t* ws_bytes);
 

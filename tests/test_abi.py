@@ -97,3 +97,18 @@ def test_fp4_config(lib):
         with pytest.raises(SegPagedError) as ei:
             sp_required_bytes(_cfg(kv_dtype=KV_FP4, **bad))
         assert ei.value.status == 3
+
+
+@pytest.mark.parametrize("seqs,tokens,layers,batch", [(1, 8192, 32, 1), (1, 32768, 32, 1), (4, 8192, 16, 2)])
+def test_fp4_cache_is_smaller_than_the_other_page_types(lib, seqs, tokens, layers, batch):
+    """Pool and workspace together.  A prefill reads one layer: the bf16 copies
+    of its history do not grow with the pool of all layers."""
+    from head_aware_paged_gb300 import KV_BF16, KV_FP4, KV_FP8, sp_required_bytes
+    cfg = dict(num_layers=layers, num_q_heads=32, num_kv_heads=8, max_seqs=seqs, max_seq_len=tokens, max_tokens=8192,
+               max_batch=batch, num_pages=seqs * layers * 8 * tokens // 64)
+    size = {kv: sp_required_bytes(_cfg(kv_dtype=kv, **cfg)) for kv in (KV_BF16, KV_FP8, KV_FP4)}
+    total = {kv: b[0] + b[2] for kv, b in size.items()}
+    assert total[KV_FP4] < total[KV_FP8] < total[KV_BF16]
+    layer = batch * 8 * (tokens // 64 + 1) * 64 * 128 * 2 * 2        # a call's history, K and V in bf16
+    assert size[KV_FP4][2] - size[KV_BF16][2] <= layer + 4096
+    assert size[KV_FP4][2] - size[KV_BF16][2] >= layer - 2 * 64 * 128 * 2 * 8 * batch
