@@ -781,7 +781,11 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                     // Most of a LOCAL ring's tiles are seen whole by a warp's rows:
                     // only their break and the window's edge need the selects below
                     // (five short capped chunks: 61 us with selects everywhere, 56).
-                    const bool all_seen = masked ? __all_sync(0xffffffffu, (vm[0] & vm[1] & vm[2] & vm[3]) == 0xffffffffu)
+                    // A chunk's own tiles are not asked without a cap (8K layer 190.3
+                    // us with the vote, 189.9), nor any tile in the instance for long
+                    // items: with the vote its CTAs' sweeps drift apart (128K layers
+                    // of 3 and 4 GLOBAL heads: 20 % more DRAM reads, 0.6 % more time).
+                    const bool all_seen = masked ? !SPEC && (CAP || kt.paged) && __all_sync(0xffffffffu, (vm[0] & vm[1] & vm[2] & vm[3]) == 0xffffffffu)
                                                  : kt.nkeys == 128;
                     if constexpr (CAP) {
                         // A capped score lies in [-cap, cap], so the exponentials
