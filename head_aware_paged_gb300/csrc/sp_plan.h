@@ -93,6 +93,11 @@ SP_HD Plan make_plan(const UnitPol& u, const int32_t* idx, int64_t n_b, int64_t 
     return pl;
 }
 
+// No plan whose last row sits at position n - 1 has more tiles: its segments
+// cover n positions at most, ring segments up to two pages more, and each of
+// the five may end in a part of a tile.
+SP_HD int64_t plan_tiles_bound(int64_t n) { return n / kTileKeys + 8; }
+
 // Tile t (0 <= t < pl.ntiles) of a plan.
 SP_HD KvTile plan_tile(const Plan& pl, const UnitPol& u, int64_t t, int64_t i_lo,
                        int64_t i_hi) {

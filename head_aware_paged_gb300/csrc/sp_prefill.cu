@@ -117,6 +117,26 @@ int64_t prefill_max_tiles(const sp_config* c) {
     return ((int64_t)c->max_tokens / 128 + c->max_batch + 1) * c->num_q_heads + 512;
 }
 
+// An item counts its key tiles in 20 bits.  Checked before the call's first
+// launch: a refused call has launched nothing.
+static sp_status check_tiles(const sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                             const int32_t* cu_q) {
+    constexpr int64_t kMaxTiles = int64_t(1) << 20;
+    for (int b = 0; b < n_seqs; ++b) {
+        const int64_t n_b = c->h_seqlen[(size_t)seq_ids[b] * c->cfg.num_layers + layer];
+        const int64_t cb = cu_q[b + 1] - cu_q[b];
+        if (cb == 0 || plan_tiles_bound(n_b + cb) < kMaxTiles) continue;
+        for (int h = 0; h < c->cfg.num_kv_heads; ++h) {
+            const UnitPol& u = c->h_pol[((size_t)seq_ids[b] * c->cfg.num_layers + layer) * c->cfg.num_kv_heads + h];
+            const int32_t* idx = c->h_idx[seq_ids[b]].data() + u.idx_off;
+            for (int64_t r = 0; r < cb; r += 128)
+                if (make_plan(u, idx, n_b, n_b + r, n_b + std::min(cb, r + 128) - 1, c->cfg.page_size).ntiles >= kMaxTiles)
+                    return fail(SP_ERR_UNSUPPORTED, "more than 2^20 key tiles for one row block");
+        }
+    }
+    return SP_OK;
+}
+
 // The call's units [unit0, unit1) (call sequence * hkv + KV head); `first` and
 // `last` of the call's launches carry its launch events.
 static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
@@ -165,8 +185,6 @@ static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_id
                 const int64_t i_lo = n_b + rb * 128;
                 const int64_t i_hi = n_b + std::min(cb, rb * 128 + 128) - 1;
                 const Plan pl = make_plan(u, idx, n_b, i_lo, i_hi, P);
-                if (pl.ntiles >= (int64_t(1) << 20))
-                    return fail(SP_ERR_UNSUPPORTED, "more than 2^20 key tiles for one row block");
                 // Time model for the assignment, measured per CTA with clock64
                 // traces: every K/V tile costs about the same whatever its
                 // width (the softmax treats a whole tile), and an item adds the
@@ -215,6 +233,7 @@ static sp_status prefill_units(sp_cache* c, int32_t layer, const int32_t* seq_id
         }
         slots += np;
     }
+    // (prefill_max_tiles has room for every call that the entry points let pass)
     if ((int64_t)cands.size() + (c->num_sms + 4) / 4 > c->ws.max_tiles)
         return fail(SP_ERR_UNSUPPORTED, "prefill work list larger than the workspace");
     // Order.  When the call's K/V is larger than about half of L2: unit by
@@ -385,6 +404,8 @@ sp_status prefill_impl(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
                        const __nv_bfloat16* v, __nv_bfloat16* out, float* lse,
                        const Cap& cap, cudaStream_t stream) {
     if (cu_q[n_seqs] == 0) return SP_OK;
+    const sp_status checked = check_tiles(c, layer, seq_ids, n_seqs, cu_q);
+    if (checked != SP_OK) return checked;
     const int H = c->cfg.num_kv_heads, units = n_seqs * H;
     if (!c->geo.fp4)
         return prefill_units(c, layer, seq_ids, n_seqs, cu_q, q, k, v, out, lse, cap, 0, units, true, true, stream);
