@@ -593,6 +593,8 @@ sp_status sp_build_cache(sp_cache* c, int32_t seq, int32_t layer, const void* k,
         return fail(SP_ERR_INVALID_ARG, "row_stride must be >= kv_heads*head_dim and a multiple of 8");
     if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
         return fail(SP_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     const int64_t cnt = n_tokens;
     return write_tokens(c, layer, &seq, 1, &cnt, static_cast<const __nv_bfloat16*>(k),
                         static_cast<const __nv_bfloat16*>(v), row_stride,
@@ -615,6 +617,8 @@ sp_status sp_append_kv(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32
     }
     if (cu_new[n_seqs] > c->cfg.max_tokens)
         return fail(SP_ERR_INVALID_ARG, "more new tokens than max_tokens");
+    s = check_device(c);
+    if (s != SP_OK) return s;
     return write_tokens(c, layer, seq_ids, n_seqs, counts.data(),
                         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                         (int64_t)c->cfg.num_kv_heads * c->cfg.head_dim,
@@ -747,6 +751,8 @@ sp_status sp_set_launch_events(sp_cache* c, void* start_event, void* end_event) 
 sp_status sp_release_seq(sp_cache* c, int32_t seq, void* stream) {
     if (!c) return fail(SP_ERR_INVALID_ARG, "null handle");
     if (!valid_seq(c, seq)) return fail(SP_ERR_INVALID_ARG, "sequence id out of range");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     int64_t held = 0;
     const size_t base = unit_index(c, seq, 0, 0);
     const int NU = c->cfg.num_layers * c->cfg.num_kv_heads;
@@ -804,6 +810,8 @@ sp_status sp_rope_realign(sp_cache* c, int32_t layer, const int32_t* seq_ids, in
     if (delta < -(int64_t(1) << 40) || delta > (int64_t(1) << 40))
         return fail(SP_ERR_INVALID_ARG, "delta out of range (|delta| <= 2^40)");
     if (pos_lo == pos_hi || delta == 0) return SP_OK;   // nothing moves
+    s = check_device(c);
+    if (s != SP_OK) return s;
     std::unique_ptr<RopeParams> pp(new RopeParams());
     RopeParams& p = *pp;
     p.meta = c->meta;
@@ -858,6 +866,10 @@ sp_status sp_pack_seq(sp_cache* c, int32_t seq, void* dst, size_t dst_bytes, siz
     if (!c || !packed_bytes) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_seq(c, seq)) return fail(SP_ERR_INVALID_ARG, "sequence id out of range");
     if (!c->h_policy_set[seq]) return fail(SP_ERR_INVALID_ARG, "sequence has no policy");
+    if (dst) {                                         // (a size query is host work)
+        const sp_status on_device = check_device(c);
+        if (on_device != SP_OK) return on_device;
+    }
     const int L = c->cfg.num_layers, H = c->cfg.num_kv_heads, d = c->cfg.head_dim;
     const int P = c->cfg.page_size, U = L * H;
     int64_t idx_total = 0;
@@ -936,6 +948,8 @@ sp_status sp_unpack_seq(sp_cache* c, int32_t seq, const void* src, size_t src_by
         if (c->h_seqlen[(size_t)seq * c->cfg.num_layers + l] != 0)
             return fail(SP_ERR_INVALID_ARG, "sequence holds tokens; release it first");
     if (src_bytes < sizeof(PackHeader)) return fail(SP_ERR_INVALID_ARG, "src shorter than a header");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     PackHeader ph;
     cudaError_t e = cudaMemcpyAsync(&ph, src, sizeof(ph), cudaMemcpyDeviceToHost, st);
@@ -1017,6 +1031,8 @@ sp_status sp_export_table(sp_cache* c, int32_t seq, int32_t layer, int32_t kv_he
     if (!c || !npages || !page_ids || !slot_pos) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_seq(c, seq) || !valid_layer(c, layer) || kv_head < 0 || kv_head >= c->cfg.num_kv_heads)
         return fail(SP_ERR_INVALID_ARG, "unit out of range");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     const int32_t np = c->h_npages[unit_index(c, seq, layer, kv_head)];
     *npages = np;
     if (np > cap) return fail(SP_ERR_INVALID_ARG, "cap smaller than the unit's page count");
@@ -1045,6 +1061,8 @@ sp_status sp_visible_count(sp_cache* c, int32_t seq, int32_t layer, int32_t kv_h
     for (int k = 0; k < n; ++k)
         if (positions[k] < held - 1 || positions[k] >= held + c->cfg.max_tokens)
             return fail(SP_ERR_INVALID_ARG, "position outside [held-1, held+max_tokens)");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int64_t* d_pos = reinterpret_cast<int64_t*>(c->ws.scratch);
     int32_t* d_out = c->ws.scratch + 2 * 65536;

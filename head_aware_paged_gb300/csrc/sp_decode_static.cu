@@ -72,10 +72,10 @@ extern "C" sp_status sp_attention_decode_static_scratch(sp_cache* c, int32_t lay
                     "decode needs " + std::to_string(o_bytes + ml_bytes + ctr_bytes) +
                         " bytes of scratch; the built-in array holds " +
                         std::to_string(kStaticScratchBytes) + " (use sp_attention_decode)");
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (dev != c->device) return fail(SP_ERR_INVALID_ARG, "current device is not the cache's device");
+    s = check_device(c);
+    if (s != SP_OK) return s;
+    const int dev = c->device;
+    cudaError_t e = cudaSuccess;
     if (dev < 0 || dev >= kMaxDevices) return fail(SP_ERR_UNSUPPORTED, "device index above 63");
 
     std::lock_guard<std::mutex> lock(g_mu);

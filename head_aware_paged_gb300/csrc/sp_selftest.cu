@@ -58,6 +58,8 @@ extern "C" sp_status sp_selftest_bounded_wait(sp_cache* c, int64_t limit_cycles,
     if (mode < 0 || mode > 2) return fail(SP_ERR_INVALID_ARG, "mode must be 0, 1 or 2");
     if (limit_cycles < 1000 || limit_cycles > kWaitCycles)
         return fail(SP_ERR_INVALID_ARG, "limit_cycles must lie in [1000, 2e9]");
+    const sp_status on_device = check_device(c);
+    if (on_device != SP_OK) return on_device;
     k_wait_selftest<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(c->meta.status, limit_cycles, mode);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "self-test launch");

@@ -27,6 +27,8 @@
  *     asynchronous unless marked "synchronous".  All calls that touch one
  *     cache must be issued in stream order (one stream, or with events).
  *   - One cache handle must not be used from two host threads at once.
+ *   - A call that launches work on a cache wants the cache's device (the
+ *     current one at its creation) to be current (SP_ERR_INVALID_ARG otherwise).
  *   - Tensors are bf16 (2-byte elements), row-major and contiguous unless a
  *     stride is given:  q / out [tokens][num_q_heads][head_dim];
  *     k / v [tokens][num_kv_heads][head_dim]; lse [tokens][num_q_heads] fp32
@@ -200,8 +202,7 @@ sp_status sp_append_kv(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
  *     overlaps the inputs in no other way.
  * A prompt chunk attends before it is stored (sp_attention_prefill wants its
  * keys rotated already); afterwards this call stores the unrotated rows, q null.
- * One launch, pages included; works for every page type and head class.  The
- * current device must be the cache's.
+ * One launch, pages included; works for every page type and head class.
  * Captured into a graph: a call that needs new pages is refused
  * (SP_ERR_UNSUPPORTED; replays would take them from the free stack again).
  * Another counts once, when it is captured, and keeps its positions and whether
@@ -250,8 +251,7 @@ sp_status sp_attention_decode(sp_cache* cache, int32_t layer,
  * scores all lie near -64 weighs smaller ones in fp32's subnormals).  In all four calls a
  * key that a row does not see, and a row of another sequence, may enter its
  * sums with the weight 0: k and v must be finite (a NaN in q stays in its row,
- * whose output and lse are NaN).
- * The current device must be the cache's. */
+ * whose output and lse are NaN). */
 sp_status sp_attention_prefill_capped(sp_cache* cache, int32_t layer,
                                       const int32_t* seq_ids, int32_t n_seqs,
                                       const int32_t* cu_q, const void* q,
@@ -278,7 +278,7 @@ sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
  *     SP_ERR_UNSUPPORTED before any launch (use sp_attention_decode).
  *   - The first call on each device looks up the array's device address
  *     (cudaGetSymbolAddress, with that device current); make that first call
- *     before any stream capture.  The current device must be the cache's.
+ *     before any stream capture.
  *   - Every call shares the one array; the tickets are cleared at the start of
  *     each call.  Calls that overlap on the GPU (other streams, other caches)
  *     race on the array and must not be issued concurrently.
