@@ -201,9 +201,14 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Bits of a start for 1 / d, less d's: twice the bits of 1.0, less what
-// centres the error (12.5 % at most over d's mantissa).
-constexpr uint32_t kRcpStart = 0x7EF311C7u;
+// A start for 1 / d: the number whose bits are kRcpStart less those of d.  With
+// d = 1 + f (a power of two only shifts) and kRcpStart = twice the bits of 1.0
+// less s 2^23, that number is r = 1 - (f + s) / 2 while f + s <= 1, and
+// d r = (1 + f)(1 - (f + s) / 2) runs from 1 - s / 2 at f = 0 up to
+// (3 - s)^2 / 8 at f = (1 - s) / 2 and back to 1 - s / 2 at f = 1 - s (beyond,
+// with r = (3 - f - s) / 4, the same ends again).  Both errors are equal where
+// s^2 - 10 s + 1 = 0: s = 5 - sqrt(24), an error of s / 2 = 5.1 % at most.
+constexpr uint32_t kRcpStart = 0x7F000000u - (uint32_t)(0.10102051443364381 * 8388608.0 + 0.5);
 // min(a, b), NaN if either is.
 __device__ __forceinline__ float fmin_nan(float a, float b) {
     float r;
@@ -901,9 +906,8 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                                     // past 2^30 tanh is 1 in fp32 already (and a NaN stays one)
                                     const float z0 = fast_exp2(fmin_nan(x0, 30.f)), z1 = fast_exp2(fmin_nan(x1, 30.f));
                                     const uint64_t d = add_f32x2(pack_f32x2(z0, z1), one);
-                                    // start: the exponent and mantissa fields subtracted from
-                                    // twice those of 1 (within 12.5 %), then three steps
-                                    // r (2 - d r), each squaring the error
+                                    // start within 5.1 %, then three steps r (2 - d r), each
+                                    // squaring the error (4.3e-11 after them)
                                     float d0, d1;
                                     unpack_f32x2(d, d0, d1);
                                     const uint64_t dn = mul_f32x2(d, neg);
