@@ -25,6 +25,10 @@
 //     unnormalised partial (o, m, l); the last CTA to finish the unit (atomic
 //     ticket, no waiting) merges them: m* = max m_s, l* = sum 2^(m_s-m*) l_s,
 //     O = sum 2^(m_s-m*) o_s / l*.
+//
+// Scores, maxima, sums and partials are fp32; what the matrix instructions take
+// is rounded once: P to bf16 (2^-8 of a weight; f16, 2^-11, on FP8 pages, with
+// the query and code * scale in f16 too).  The output is bf16 like them.
 #pragma once
 #include <algorithm>
 

@@ -12,6 +12,10 @@
 // stay in L2 for the kernel that follows; a short history is a launch and one
 // chain of loads, so a thread issues all of a page's at once (with them in a
 // loop over rows, every head GLOBAL: 505 instead of 498 us for the call).
+//
+// code * scale has 6 significant bits, exact in bf16; a channel scale that is not
+// a power of two makes it 2^-8 relative, the step of the rows that the chunk
+// itself brings.
 #include "sp_device.cuh"
 #include "sp_internal.h"
 

@@ -814,6 +814,10 @@ k_prefill(const __grid_constant__ PrefillParams p, const __grid_constant__ CUten
                         // the tile takes the formula, its reciprocal by Newton's
                         // iteration.  (8K layer, scores within a tenth of the cap:
                         // 238 us, 249 with degree 7 always; past half the cap 344.)
+                        // The choice is a warp's, so the last bits of a row (inside
+                        // those 1.3e-7 of the cap) go with the rows beside it.  P is
+                        // rounded to bf16 (2^-8 of a weight), which the matrix
+                        // instructions take and whose exponent holds 2^-98 .. 2^87.
                         //
                         // The row is read from TMEM 32 columns at a time in two small
                         // loops, one for the largest |score|, one for P, which takes the

@@ -8,9 +8,12 @@
 // in fp32, rounded once: to bf16 (queries, bf16 pages) or to the page's codes.
 // Far positions: the host gives w_i as a fraction of a turn in 64-bit fixed
 // point, so p * w_i modulo 2^64 is the angle modulo a turn, reduced by the
-// multiplication's own overflow; what is left is the frequency's rounding in
-// double, about p w_i 2^-54 turns (2^-34 at a million radians).  One (cos, sin)
-// per token and pair serves every head.
+// multiplication's own overflow.  An angle is off by the frequency's rounding in
+// double, about p w_i 2^-54 turns (2^-34 at a million radians), by 2^-33 turns
+// for the last bit of p w_i and as much where it is cut to 32 bits, and, the
+// largest part, by 2^-26 turns (1e-7 radians) where it becomes an fp32 number of
+// half turns; sincospif adds its own rounding.  One (cos, sin) per token and pair
+// serves every head.
 //
 // Bound by memory: 4 bytes a q element, 2 + the page type's size a stored
 // k / v element; a token that a head does not keep is not read.  Measured,
@@ -410,8 +413,9 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     p.kpool = c->kpool; p.vpool = c->vpool;
     std::memcpy(p.turn, turn, sizeof(p.turn));
     // Four tokens a block share its set-up once that still fills the GPU (8,192
-    // rows: 29.1 us with four, 31.1 with two, 34.5 with eight); a short call
-    // spreads one token's heads over two blocks instead.
+    // rows, one head of eight GLOBAL, launches included: 27.0 us with four, 28.9
+    // with two, 32.9 with eight, for which the arrays of four do not do); a short
+    // call spreads one token's heads over two blocks instead.
     p.tok = rows >= 4 * c->num_sms ? kMaxTok : 1;
     p.row_blocks = (rows + p.tok - 1) / p.tok;
     const int items = (q ? c->cfg.num_q_heads : H) * c->cfg.head_dim / 16;
