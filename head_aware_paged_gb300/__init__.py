@@ -76,6 +76,13 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _row_stride(x: torch.Tensor) -> int:
+    """Elements between the rows of x [rows, heads, head_dim]; a single row may
+    carry any stride, which says nothing."""
+    n, h, d = x.shape
+    return x.stride(0) if n > 1 else h * d
+
+
 # ---------------------------------------------------------------- C-ABI names
 
 def sp_required_bytes(cfg: Config):
@@ -176,8 +183,8 @@ def sp_append_kv_rope(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequen
     at = None if pos is None else i64_buffer(pos)
     check(load().sp_append_kv_rope(handle, layer, ids.buffer_info()[0], len(seq_ids), cu.buffer_info()[0],
                                    at and at.buffer_info()[0], _ptr(q),
-                                   0 if q is None else q.stride(0), _ptr(k), k.stride(0), _ptr(v),
-                                   v.stride(0), _ptr(q_out), float(rope_theta), fr, _stream(stream)))
+                                   0 if q is None else _row_stride(q), _ptr(k), _row_stride(k), _ptr(v),
+                                   _row_stride(v), _ptr(q_out), float(rope_theta), fr, _stream(stream)))
 
 
 def sp_attention_decode_static_scratch(handle, layer: int, seq_ids: Sequence[int],
@@ -429,8 +436,9 @@ class SegPagedCache:
         for x, heads in ((k, c.num_kv_heads), (v, c.num_kv_heads)) if q is None else \
                 ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
             n, h, d = x.shape
-            assert x.dtype is torch.bfloat16 and x.is_cuda and h == heads and d == c.head_dim and \
-                n >= cu_new[-1] and x.stride()[1:] == (d, 1), \
+            _, per_head, per_element = x.stride()
+            assert x.dtype is torch.bfloat16 and x.is_cuda and h == heads and \
+                d == c.head_dim and n >= cu_new[-1] and (h == 1 or per_head == d) and per_element == 1, \
                 "q, k, v: bf16 [rows, heads, head_dim] on the device, heads contiguous"
         assert len(cu_new) == len(seq_ids) + 1 and (pos is None or len(pos) == len(seq_ids))
         assert inv_freq is None or len(inv_freq) == c.head_dim // 2

@@ -410,3 +410,30 @@ def test_q_out_may_not_overlap_what_is_read():
     got = cache.append_kv_rope(0, [0], [0, n], big[:size].view(n, hq, d), k, v, q_out=big[size:].view(n, hq, d))
     _close(got, _turn(q, np.arange(n, 2 * n)), "side by side")
     assert cache.status() == 0
+
+
+def test_strides_of_single_rows_and_single_heads():
+    """A dimension of one element may have any stride: one token taken out of a
+    heads-first layout, one KV head out of a sequence-first one."""
+    gpu_ready()
+    hq, hkv, d, n = 4, 2, 64, 9
+    cache = _mk(hq, hkv, d, 16, 1, 64, 8)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+    q, k, v = (W.normal((h, 1, d), h, device="cuda").transpose(0, 1) for h in (hq, hkv, hkv))
+    assert q.stride(0) == d and q.shape == (1, hq, d)
+    got = cache.append_kv_rope(0, [0], [0, 1], q, k, v)
+    assert torch.equal(got, q)                                   # position 0
+    got = cache.append_kv_rope(0, [0], [0, 1], q, k, v)
+    _close(got, _turn(q, [1]), "one token")
+    p, pg, sl = _rows(cache, 0, 1)
+    _close(cache.k_pool()[pg, sl], _turn(torch.cat([k, k]), [0, 1])[:, 1], "keys")
+    one = _mk(1, 1, d, 16, 1, 64, 8)
+    one.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    q, k, v = (W.normal((1, n, d), 5 + i, device="cuda").transpose(0, 1) for i in range(3))
+    assert k.stride(1) == n * d and k.shape == (n, 1, d)
+    got = one.append_kv_rope(0, [0], [0, n], q, k, v)
+    _close(got, _turn(q, np.arange(n)), "one head")
+    p, pg, sl = _rows(one, 0, 0)
+    _close(one.k_pool()[pg, sl], _turn(k, np.arange(n))[:, 0], "keys of one head")
+    assert torch.equal(one.v_pool()[pg, sl], v[:, 0])
+    assert cache.status() == 0 and one.status() == 0
