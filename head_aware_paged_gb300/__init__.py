@@ -369,6 +369,7 @@ class SegPagedCache:
         self._meta_raw, self.meta = self._aligned(meta_b, device)
         self._ws_raw, self.ws = self._aligned(ws_b, device)
         self._halves = None          # K and V views of the pool
+        self._index = self.pool.get_device()
         self.handle = sp_cache_create(cfg, self.pool, self.meta, self.ws)
 
     @staticmethod
@@ -437,9 +438,9 @@ class SegPagedCache:
                 ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
             n, h, d = x.shape
             _, per_head, per_element = x.stride()
-            assert x.dtype is torch.bfloat16 and x.is_cuda and h == heads and \
+            assert x.dtype is torch.bfloat16 and x.get_device() == self._index and h == heads and \
                 d == c.head_dim and n >= cu_new[-1] and (h == 1 or per_head == d) and per_element == 1, \
-                "q, k, v: bf16 [rows, heads, head_dim] on the device, heads contiguous"
+                "q, k, v: bf16 [rows, heads, head_dim] on the cache's device, heads contiguous"
         assert len(cu_new) == len(seq_ids) + 1 and (pos is None or len(pos) == len(seq_ids))
         assert inv_freq is None or len(inv_freq) == c.head_dim // 2
         if q is None:
@@ -447,7 +448,8 @@ class SegPagedCache:
         elif q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         else:
-            assert q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype is q.dtype
+            assert q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype is q.dtype and \
+                q_out.get_device() == self._index, "q_out: contiguous, of q's shape and type, on the cache's device"
         sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out, pos, rope_theta, inv_freq,
                           stream)
         return q_out

@@ -437,3 +437,16 @@ def test_strides_of_single_rows_and_single_heads():
     _close(one.k_pool()[pg, sl], _turn(k, np.arange(n))[:, 0], "keys of one head")
     assert torch.equal(one.v_pool()[pg, sl], v[:, 0])
     assert cache.status() == 0 and one.status() == 0
+
+
+def test_tensors_elsewhere_are_refused():
+    """Host memory is not read or written by a kernel."""
+    gpu_ready()
+    hq, hkv, d = 4, 2, 64
+    cache = _mk(hq, hkv, d, 16, 1, 64, 8)
+    cache.set_policy(0, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+    q, k, v = (W.normal((3, h, d), h, device="cuda") for h in (hq, hkv, hkv))
+    for bad in (dict(q=q.cpu()), dict(k=k.cpu()), dict(v=v.cpu()), dict(q_out=torch.empty_like(q, device="cpu"))):
+        with pytest.raises(AssertionError):
+            cache.append_kv_rope(0, [0], [0, 3], bad.get("q", q), bad.get("k", k), bad.get("v", v), q_out=bad.get("q_out"))
+    assert cache.seq_len(0, 0) == 0 and cache.status() == 0
