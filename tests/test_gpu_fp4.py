@@ -479,3 +479,63 @@ def test_weights_far_below_the_largest(at):
     assert (o > 4e-6).all() and ((out.double() - o).abs() <= tol).all()
     assert ((lse.double() - z).abs() <= 2.0 ** -19 * (1 + z)).all()
     assert cache.status() == 0
+
+
+def test_offsets_past_32_bits():
+    """A pool whose K half is longer than 4 GiB, read and written at its end."""
+    gpu_ready()
+    hq, hkv, P, n, B = 8, 2, 64, 131072, 234
+    pages = B * hkv * (n // P) + 8
+    assert (pages - 8) * P * 72 > 1 << 32
+    cache = _mk(hq, hkv, P, B, n + 64, pages, batch=2)
+    k, v = _kv(n, hkv, 3)
+    for b in range(B):
+        cache.set_policy(b, to_c_policies([[W.HeadPolicy(G)] * hkv]))
+        cache.build(b, 0, k if b < B - 1 else torch.roll(k, 1, 0).contiguous(), v)
+    ids = cache.export_table(B - 1, 0, hkv - 1)[0]
+    assert min(ids) * P * 72 >= 1 << 32
+    ks, vs = torch.roll(_stored(k), 1, 0), _stored(v)
+    pol = [(G, 0, 0, None)] * hkv
+    q = W.normal((3, hq, D), 7, device="cuda")
+    out, lse = cache.decode(0, [B - 1], q[:1].contiguous())
+    check(out, lse, attend(q[:1].double(), ks, vs, [n - 1], pol), 2.0 ** -11, 0.0, "decode")
+    kn, vn = _kv(3, hkv, 8)
+    out, lse = cache.prefill(0, [B - 1], [0, 3], q, kn, vn)
+    check(out, lse, attend(q.double(), torch.cat([ks, kn.double()]), torch.cat([vs, vn.double()]), range(n, n + 3), pol),
+          2.0 ** -8, 0.0, "prefill")
+    low = cache.k_pool()[:64].clone()
+    cache.append_kv_rope(0, [B - 1], [0, 3], None, kn, vn, inv_freq=[0.0] * 64)         # a new page, no rotation
+    ks, vs = torch.cat([ks, _stored(kn)]), torch.cat([vs, _stored(vn)])
+    out, lse = cache.decode(0, [B - 1], q[2:].contiguous())
+    check(out, lse, attend(q[2:].double(), ks, vs, [n + 2], pol), 2.0 ** -11, 0.0, "after the write")
+    assert torch.equal(cache.k_pool()[:64], low)
+    assert cache.status() == 0
+
+
+def test_two_graphs_share_the_workspace():
+    """Two captured steps of one cache, replayed in turns in stream order, give
+    what the calls gave: no state is left in the workspace."""
+    gpu_ready()
+    hq, hkv = 8, 2
+    cache = _mk(hq, hkv, 16, 3, 3000, 3 * hkv * 200)
+    for b, n in enumerate((2500, 31, 700)):
+        cache.set_policy(b, to_c_policies([[W.HeadPolicy(G), W.HeadPolicy(L, 4, 300)]]))
+        cache.build(b, 0, *_kv(n, hkv, b))
+    q, k, v = W.normal((40, hq, D), 1, device="cuda"), *_kv(40, hkv, 9)
+    calls = [lambda: [*cache.decode(0, [0, 1, 2], q[:3].contiguous(), score_cap=30.0), *cache.prefill(0, [1], [0, 40], q, k, v)],
+             lambda: [*cache.prefill(0, [2, 0], [0, 17, 40], q, k, v), *cache.decode(0, [2], q[7:8].contiguous())]]
+    want = [[x.clone() for x in c()] for c in calls]
+    s = torch.cuda.Stream()
+    graphs, got = [], []
+    for c in calls:
+        s.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            got.append(c())
+    for i in (0, 1, 1, 0, 0, 1):
+        for t in got[i]:
+            t.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    assert cache.status() == 0

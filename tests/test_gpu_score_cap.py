@@ -290,3 +290,30 @@ def test_small_and_large_values(d, hq, sign, vs, cap):
     out, lse = cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
     check(out, lse, held([n - 1], k, v), 2.0 ** -8, 0.0, "decode", cap)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+@pytest.mark.parametrize("kv,d,hq,hkv", [("bf16", 64, 6, 3), ("bf16", 64, 4, 2), ("bf16", 128, 3, 3), ("bf16", 128, 8, 2),
+                                         ("fp8", 128, 8, 2), ("fp8", 128, 3, 3), ("fp4", 128, 3, 3), ("fp4", 128, 8, 2)])
+def test_every_page_size(kv, d, hq, hkv, P):
+    """Each instance at each page size: history that ends inside a page, rings
+    that wrap inside a tile."""
+    gpu_ready()
+    n, c, cap = 333, 70, 20.0
+    cache = _mk(hq, hkv, d, P, 1, n + c, hkv * ((n + c) // P + 4), kv)
+    pols = _pols(hkv, n + c)
+    pt = [pol_tuple(p) for p in pols]
+    ks = np.full((hkv, d), 2.0 ** -6, np.float32)
+    if kv == "fp8":
+        cache.set_kv_scales(0, ks, ks)
+    cache.set_policy(0, to_c_policies([pols]))
+    hist = [W.normal((n, hkv, d), 5 + i, device="cuda") for i in range(2)]
+    cache.build(0, 0, *hist)
+    q, k, v = (W.normal((c, h, d), 7 + i, device="cuda") for i, h in enumerate((hq, hkv, hkv)))
+    hk, hv = _held(hist[0], kv, ks), _held(hist[1], kv, ks)
+    out, lse = cache.prefill(0, [0], [0, c], q, k, v, score_cap=cap)
+    ref = attend(q.double(), torch.cat([hk, k.double()]), torch.cat([hv, v.double()]), range(n, n + c), pt, cap)
+    check(out, lse, ref, 2.0 ** -8, 0.0, "prefill", cap)
+    out, lse = cache.decode(0, [0], q[:1].contiguous(), score_cap=cap)
+    check(out, lse, attend(q[:1].double(), hk, hv, [n - 1], pt, cap), 2.0 ** -8 if kv == "bf16" else 2.0 ** -11, 0.0, "decode", cap)
+    assert cache.status() == 0
