@@ -29,6 +29,10 @@
  *   - One cache handle must not be used from two host threads at once.
  *   - A call that launches work on a cache wants the cache's device (the
  *     current one at its creation) to be current (SP_ERR_INVALID_ARG otherwise).
+ *   - A call captured into a CUDA graph takes its lists, lengths, policies and
+ *     whether channel scales were set from the moment of its capture; sequences
+ *     that it names must not be released between then and its last replay
+ *     (sp_append_kv_rope says what a replayed write does otherwise).
  *   - Tensors are bf16 (2-byte elements), row-major and contiguous unless a
  *     stride is given:  q / out [tokens][num_q_heads][head_dim];
  *     k / v [tokens][num_kv_heads][head_dim]; lse [tokens][num_q_heads] fp32
