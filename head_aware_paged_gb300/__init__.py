@@ -176,15 +176,95 @@ def sp_append_kv_rope(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequen
                       stream=None) -> None:
     """Rotate q into q_out and k on its way into the pages (see the C header).
     q, k, v [rows, heads, head_dim] with any row stride the header allows."""
-    fr = None
-    if inv_freq is not None:
-        fr = (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
+    fr = _frequencies(inv_freq)
     ids, cu = i32_buffer(seq_ids), i32_buffer(cu_new)
     at = None if pos is None else i64_buffer(pos)
     check(load().sp_append_kv_rope(handle, layer, ids.buffer_info()[0], len(seq_ids), cu.buffer_info()[0],
                                    at and at.buffer_info()[0], _ptr(q),
                                    0 if q is None else _row_stride(q), _ptr(k), _row_stride(k), _ptr(v),
                                    _row_stride(v), _ptr(q_out), float(rope_theta), fr, _stream(stream)))
+
+
+def _frequencies(inv_freq):
+    if inv_freq is None:
+        return None
+    return (ctypes.c_double * max(1, len(inv_freq)))(*[float(x) for x in inv_freq])
+
+
+def sp_append_kv_rope_axes(handle, layer: int, seq_ids: Sequence[int], cu_new: Sequence[int],
+                           q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                           axis_pos: torch.Tensor, axis_of: Sequence[int],
+                           q_out: Optional[torch.Tensor] = None, pos: Optional[Sequence[int]] = None,
+                           rope_theta: float = 10000.0, inv_freq: Optional[Sequence[float]] = None,
+                           stream=None) -> None:
+    """sp_append_kv_rope with angles of axis_pos [axes, rows] (int64, on the device,
+    any strides): pair i of the dimensions turns by the position on axis axis_of[i]."""
+    ids, cu, of = i32_buffer(seq_ids), i32_buffer(cu_new), i32_buffer(axis_of)
+    at = None if pos is None else i64_buffer(pos)
+    check(load().sp_append_kv_rope_axes(
+        handle, layer, ids.buffer_info()[0], len(seq_ids), cu.buffer_info()[0], at and at.buffer_info()[0],
+        _ptr(q), 0 if q is None else _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(q_out),
+        _ptr(axis_pos), axis_pos.stride(0), axis_pos.stride(1), axis_pos.shape[0], of.buffer_info()[0],
+        float(rope_theta), _frequencies(inv_freq), _stream(stream)))
+
+
+def sp_rope_axes(q: Optional[torch.Tensor], k: Optional[torch.Tensor], axis_pos: torch.Tensor,
+                 axis_of: Sequence[int], rope_theta: float = 10000.0,
+                 inv_freq: Optional[Sequence[float]] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotate q and k [rows, heads, head_dim] (bf16, rows any stride apart, on the
+    current device; either may be None) to the positions axis_pos [axes, rows]
+    (int64): pair i turns by the position on axis axis_of[i].  Returns (q_out, k_out)."""
+    first = k if q is None else q
+    rows, _, d = first.shape
+    index = first.get_device()
+    assert len(axis_of) == d // 2 and (inv_freq is None or len(inv_freq) == d // 2)
+    assert axis_pos.dtype is torch.int64 and axis_pos.get_device() == index and axis_pos.dim() == 2 and \
+        axis_pos.shape[1] >= rows, "axis_pos: int64 [axes, rows] on the device of q and k"
+    outs = []
+    for x, out in ((q, q_out), (k, k_out)):
+        if x is None:
+            outs.append(None)
+            continue
+        _, per_head, per_element = x.stride()
+        assert x.dtype is torch.bfloat16 and x.get_device() == index and x.shape[0] == rows and x.shape[2] == d and \
+            (x.shape[1] == 1 or per_head == d) and per_element == 1, \
+            "q, k: bf16 [rows, heads, head_dim] on one device, heads contiguous"
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            assert out.is_contiguous() and out.shape == x.shape and out.dtype is x.dtype and \
+                out.get_device() == index, "outputs: contiguous, of their input's shape, type and device"
+        outs.append(out)
+    of = i32_buffer(axis_of)
+    check(load().sp_rope_axes(
+        _ptr(q), 0 if q is None else _row_stride(q), 0 if q is None else q.shape[1],
+        _ptr(k), 0 if k is None else _row_stride(k), 0 if k is None else k.shape[1], d, rows,
+        _ptr(axis_pos), axis_pos.stride(0), axis_pos.stride(1), axis_pos.shape[0], of.buffer_info()[0],
+        float(rope_theta), _frequencies(inv_freq), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)))
+    return tuple(outs)
+
+
+def sp_page_bounds_bytes(cfg: Config) -> int:
+    n = c_size_t()
+    check(load().sp_page_bounds_bytes(byref(cfg.to_c()), byref(n)))
+    return n.value
+
+
+def sp_attach_page_bounds(handle, buffer: Optional[torch.Tensor]) -> None:
+    check(load().sp_attach_page_bounds(handle, _ptr(buffer)))
+
+
+def sp_attention_decode_select(handle, layer: int, seq_ids: Sequence[int], q: torch.Tensor, top_pages: int,
+                               sink_pages: int, recent_pages: int, out: torch.Tensor,
+                               lse: Optional[torch.Tensor] = None, pages: Optional[torch.Tensor] = None,
+                               score_cap: float = 0.0, stream=None) -> None:
+    """sp_attention_decode in which GLOBAL heads read their first sink_pages, their
+    newest recent_pages and the top_pages others with the highest scores."""
+    ids = i32_buffer(seq_ids)
+    check(load().sp_attention_decode_select(handle, layer, ids.buffer_info()[0], len(seq_ids), _ptr(q), top_pages,
+                                            sink_pages, recent_pages, float(score_cap), _ptr(out), _ptr(lse),
+                                            _ptr(pages), _stream(stream)))
 
 
 def sp_attention_decode_static_scratch(handle, layer: int, seq_ids: Sequence[int],
@@ -433,6 +513,13 @@ class SegPagedCache:
         sequence holds, or from pos[b] on (held ones are overwritten in place).
         q (or None), k, v [rows, heads, head_dim] bf16, rows any stride apart
         (views of one fused projection).  Returns the rotated queries."""
+        q_out = self._rope_rows(seq_ids, cu_new, q, k, v, pos, q_out, inv_freq)
+        sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out, pos, rope_theta, inv_freq,
+                          stream)
+        return q_out
+
+    def _rope_rows(self, seq_ids, cu_new, q, k, v, pos, q_out, inv_freq):
+        """The checks of the rope appends; q_out, or a new tensor for it."""
         c = self.cfg
         for x, heads in ((k, c.num_kv_heads), (v, c.num_kv_heads)) if q is None else \
                 ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)):
@@ -450,8 +537,20 @@ class SegPagedCache:
         else:
             assert q_out.is_contiguous() and q_out.shape == q.shape and q_out.dtype is q.dtype and \
                 q_out.get_device() == self._index, "q_out: contiguous, of q's shape and type, on the cache's device"
-        sp_append_kv_rope(self.handle, layer, seq_ids, cu_new, q, k, v, q_out, pos, rope_theta, inv_freq,
-                          stream)
+        return q_out
+
+    def append_kv_rope_axes(self, layer: int, seq_ids, cu_new, q, k, v, axis_pos, axis_of, pos=None, q_out=None,
+                            rope_theta: float = 10000.0, inv_freq=None, stream=None):
+        """append_kv_rope with angles of positions on several axes
+        (sp_append_kv_rope_axes): axis_pos [axes, rows] int64 on the cache's device,
+        pair i of the dimensions turns by the position on axis axis_of[i].  pos still
+        says where the tokens are stored."""
+        q_out = self._rope_rows(seq_ids, cu_new, q, k, v, pos, q_out, inv_freq)
+        assert axis_pos.dtype is torch.int64 and axis_pos.get_device() == self._index and axis_pos.dim() == 2 and \
+            axis_pos.shape[1] >= cu_new[-1], "axis_pos: int64 [axes, rows] on the cache's device"
+        assert len(axis_of) == self.cfg.head_dim // 2
+        sp_append_kv_rope_axes(self.handle, layer, seq_ids, cu_new, q, k, v, axis_pos, axis_of, q_out, pos,
+                               rope_theta, inv_freq, stream)
         return q_out
 
     def prefill(self, layer: int, seq_ids, cu_q, q, k, v, out=None, lse=None, want_lse=True,
@@ -483,6 +582,49 @@ class SegPagedCache:
         else:
             sp_attention_decode_capped(self.handle, layer, seq_ids, q, score_cap, out, lse, stream)
         return out, lse
+
+    def attach_page_bounds(self) -> None:
+        """Keep bounds of every page's keys from now on (for decode_select); the
+        cache must hold no tokens."""
+        raw, buf = self._aligned(sp_page_bounds_bytes(self.cfg), self.device)
+        sp_attach_page_bounds(self.handle, buf)
+        self._bounds_raw, self._bounds = raw, buf
+
+    def page_bounds(self):
+        """Views of the attached bounds: codes [num_pages, 2, head_dim] int8 (upper,
+        lower) and their steps [num_pages] fp32, by physical page; what a page that
+        is not a full one of a GLOBAL head holds means nothing."""
+        n, d = self.cfg.num_pages, self.cfg.head_dim
+        at = (n * 2 * d + 255) // 256 * 256
+        return self._bounds[:n * 2 * d].view(torch.int8).view(n, 2, d), self._bounds[at:at + 4 * n].view(torch.float32)
+
+    def decode_select(self, layer: int, seq_ids, q, top_pages: int, sink_pages: int = 1, recent_pages: int = 1,
+                      out=None, lse=None, pages=None, want_lse=True, want_pages=True,
+                      score_cap: Optional[float] = None, stream=None):
+        """decode in which a GLOBAL head reads its first sink_pages, its newest
+        recent_pages and the top_pages others whose bounds promise the largest scores
+        for this query (sp_attention_decode_select; attach_page_bounds first).
+        Returns (out, lse, pages): pages [sequences, kv_heads, sink + recent + top]
+        int32, the kept pages in ascending order, -1 behind them."""
+        c = self.cfg
+        assert q.dtype is torch.bfloat16 and q.is_contiguous() and q.get_device() == self._index and \
+            tuple(q.shape) == (len(seq_ids), c.num_q_heads, c.head_dim), \
+            "q: bf16 [sequences, heads, head_dim], contiguous, on the cache's device"
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+        shape = (q.shape[0], c.num_kv_heads, max(0, top_pages + sink_pages + recent_pages))
+        if pages is None and want_pages:
+            pages = torch.empty(shape, dtype=torch.int32, device=q.device)
+        for x, s, t in ((out, q.shape, torch.bfloat16), (lse, q.shape[:2], torch.float32), (pages, shape, torch.int32)):
+            assert x is None or (x.is_contiguous() and x.shape == s and x.dtype is t and
+                                 x.get_device() == self._index), "out, lse, pages: contiguous, on the cache's device"
+        if score_cap is not None and not score_cap > 0:
+            raise ValueError("score_cap must be positive")
+        sp_attention_decode_select(self.handle, layer, seq_ids, q, top_pages, sink_pages, recent_pages, out, lse, pages,
+                                   score_cap or 0.0, stream)
+        return out, lse, pages
 
     def rope_realign(self, layer: int, seq_ids, delta: int, kv_head: int = -1, pos_lo: int = 0,
                      pos_hi: int = 1 << 62, rope_theta: float = 10000.0, stream=None) -> None:

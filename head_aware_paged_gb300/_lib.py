@@ -23,6 +23,8 @@ KV_BF16, KV_FP8, KV_FP4 = 0, 1, 4
 EXPORTS = ("sp_required_bytes", "sp_cache_create", "sp_cache_destroy", "sp_set_policy",
            "sp_build_cache", "sp_append_kv", "sp_attention_prefill", "sp_attention_decode",
            "sp_attention_prefill_capped", "sp_attention_decode_capped", "sp_append_kv_rope",
+           "sp_append_kv_rope_axes", "sp_rope_axes", "sp_page_bounds_bytes", "sp_attach_page_bounds",
+           "sp_attention_decode_select",
            "sp_attention_decode_static_scratch", "sp_rope_realign", "sp_pack_seq",
            "sp_unpack_seq", "sp_select_workspace_bytes", "sp_select_heavy_hitters",
            "sp_select_heavy_hitters_top_p", "sp_set_kv_scales",
@@ -78,6 +80,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sp_attention_decode_capped": [P, c_int32, P, c_int32, P, ctypes.c_float, P, P, P],
         "sp_append_kv_rope": [P, c_int32, P, c_int32, P, P, P, c_int64, P, c_int64, P, c_int64, P,
                               c_double, POINTER(c_double), P],
+        "sp_append_kv_rope_axes": [P, c_int32, P, c_int32, P, P, P, c_int64, P, c_int64, P, c_int64, P, P, c_int64,
+                                   c_int64, c_int32, P, c_double, POINTER(c_double), P],
+        "sp_rope_axes": [P, c_int64, c_int32, P, c_int64, c_int32, c_int32, c_int64, P, c_int64, c_int64, c_int32,
+                         P, c_double, POINTER(c_double), P, P, P],
+        "sp_page_bounds_bytes": [POINTER(SpConfig), POINTER(c_size_t)],
+        "sp_attach_page_bounds": [P, P],
+        "sp_attention_decode_select": [P, c_int32, P, c_int32, P, c_int32, c_int32, c_int32, ctypes.c_float, P, P,
+                                       P, P],
         "sp_attention_decode_static_scratch": [P, c_int32, I32P, c_int32, P, P, P, P],
         "sp_rope_realign": [P, c_int32, I32P, c_int32, c_int32, c_int64, c_int64, c_int64,
                             c_double, P],

@@ -9,6 +9,7 @@
 #include <memory>
 #include <mutex>
 
+#include "sp_bounds.cuh"
 #include "sp_device.cuh"
 #include "sp_internal.h"
 #include "sp_prefill.h"
@@ -74,7 +75,7 @@ Layout make_layout(const sp_config* c) {
     Layout L;
     const int64_t S = c->max_seqs, NL = c->num_layers, H = c->num_kv_heads;
     const int64_t units = S * NL * H;
-    L.max_pages_unit = (int32_t)((c->max_seq_len + c->page_size - 1) / c->page_size + 1);
+    L.max_pages_unit = max_unit_pages(c);
     size_t o = 0;
     L.pol = o;     o = align_up(o + units * sizeof(UnitPol), 256);
     L.npages = o;  o = align_up(o + units * 4, 256);
@@ -206,7 +207,13 @@ sp_status write_tokens(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t 
     if (s != SP_OK || rows == 0) return s;
     cudaError_t e = launch_scatter(c, cs, layer, k, v, row_stride, max_items, stream);
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
-    return SP_OK;
+    if (!c->bounds.codes) return SP_OK;
+    std::vector<int64_t> lo(n_seqs), hi(n_seqs);
+    for (int b = 0; b < n_seqs; ++b) {
+        lo[b] = cs.n_old[b];
+        hi[b] = lo[b] + counts[b];
+    }
+    return update_bounds(c, layer, seqs, n_seqs, lo.data(), hi.data(), stream);
 }
 
 // Rows a unit holding n tokens keeps (the retained set of the slot rules):
@@ -241,6 +248,10 @@ UnitPol encode_unit(int64_t kind, int64_t sink, int64_t window, int32_t idx_off,
 size_t align_to(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
+
+int32_t max_unit_pages(const sp_config* c) {
+    return (int32_t)((c->max_seq_len + c->page_size - 1) / c->page_size + 1);
+}
 
 bool valid_cap(float score_cap) { return score_cap >= kMinScoreCap && score_cap <= kMaxScoreCap; }
 
@@ -653,9 +664,12 @@ static sp_status attention_prefill(sp_cache* c, int32_t layer, const int32_t* se
                         static_cast<__nv_bfloat16*>(out), lse, cap, static_cast<cudaStream_t>(stream));
 }
 
+// Which pages of the GLOBAL heads a decode keeps (sp_attention_decode_select).
+struct Choice { int32_t first, newest, top; int32_t* pages; };
+
 static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
                                   const void* q, void* out, float* lse, const Cap& cap,
-                                  void* stream) {
+                                  void* stream, const Choice* choice = nullptr) {
     if (!c || !q || !out) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     sp_status s = check_seq_list(c, seq_ids, n_seqs);
@@ -676,6 +690,8 @@ static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq
     p->cap = cap;
     p->scaled = c->h_scaled[layer];
     const int P = c->cfg.page_size, slots = decode_item_slots(c->geo);
+    const int32_t cap_pages = choice ? choice->first + choice->newest + choice->top : INT32_MAX;
+    bool fewer = false;                                // does any GLOBAL head drop a page?
     for (int b = 0; b < n_seqs; ++b) {
         const int seq = seq_ids[b];
         const int64_t n = c->h_seqlen[(size_t)seq * c->cfg.num_layers + layer];
@@ -684,7 +700,12 @@ static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq
         p->tq[b] = (int32_t)(n - 1);
         for (int h = 0; h < c->cfg.num_kv_heads; ++h) {
             const UnitPol& u = c->h_pol[unit_index(c, seq, layer, h)];
-            total += decode_items(decode_ranges(u, host_idx(c, seq, u), n - 1, P), slots);
+            int64_t t = n - 1;
+            if (choice && u.kind == kGlobal) {
+                t = kept_slots(n, P, cap_pages) - 1;
+                fewer = fewer || t < n - 1;
+            }
+            total += decode_items(decode_ranges(u, host_idx(c, seq, u), t, P), slots);
             p->item_off[b * c->cfg.num_kv_heads + h + 1] = (int32_t)total;
         }
     }
@@ -698,7 +719,36 @@ static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq
     p->counters = c->ws.counters;
     p->scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
     launch_mark_start(c, static_cast<cudaStream_t>(stream));
-    cudaError_t e = launch_decode(c, *p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaSuccess;
+    if (choice && (fewer || choice->pages)) {
+        std::unique_ptr<ChooseParams> cp(new ChooseParams());
+        cp->meta = c->meta;
+        cp->geo = c->geo;
+        cp->layer = layer;
+        cp->n_seqs = n_seqs;
+        cp->first = choice->first;
+        cp->newest = choice->newest;
+        cp->top = choice->top;
+        cp->cap = cap_pages;
+        cp->q = p->q;
+        cp->codes = c->bounds.codes;
+        cp->step = c->bounds.step;
+        cp->score = c->bounds.score;
+        cp->kept = c->bounds.kept;
+        cp->tickets = c->bounds.tickets;
+        cp->pages = choice->pages;
+        for (int b = 0; b < n_seqs; ++b) {
+            cp->seq[b] = p->seq[b];
+            cp->n[b] = p->tq[b] + 1;
+        }
+        e = launch_choose(c, *cp, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "page choice launch");
+    }
+    if (fewer) {
+        p->kept = c->bounds.kept;
+        p->kept_cap = cap_pages;
+    }
+    e = launch_decode(c, *p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     launch_mark_end(c, static_cast<cudaStream_t>(stream));
     return SP_OK;
@@ -736,6 +786,26 @@ sp_status sp_attention_decode_capped(sp_cache* c, int32_t layer, const int32_t* 
     return no_throw([&] {
         return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
                                 make_cap(score_cap, c->cfg.head_dim), stream);
+    });
+}
+
+sp_status sp_attention_decode_select(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                                     const void* q, int32_t top_pages, int32_t sink_pages,
+                                     int32_t recent_pages, float score_cap, void* out, float* lse,
+                                     int32_t* pages, void* stream) {
+    if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
+    if (!c->bounds.codes) return fail(SP_ERR_INVALID_ARG, "no page bounds: call sp_attach_page_bounds first");
+    constexpr int32_t kMost = 1 << 20;
+    if (top_pages < 0 || sink_pages < 0 || recent_pages < 1 || top_pages > kMost || sink_pages > kMost ||
+        recent_pages > kMost)
+        return fail(SP_ERR_INVALID_ARG, "need top_pages >= 0, sink_pages >= 0 and recent_pages >= 1, each at most 2^20");
+    if (score_cap != 0.f && !valid_cap(score_cap))
+        return fail(SP_ERR_INVALID_ARG, "score_cap must be 0 or lie in [1/64, 64]");
+    if (reinterpret_cast<uintptr_t>(pages) & 3) return fail(SP_ERR_INVALID_ARG, "pages must be 4-byte aligned");
+    return no_throw([&] {
+        const Choice choice{sink_pages, recent_pages, top_pages, pages};
+        return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
+                                score_cap != 0.f ? make_cap(score_cap, c->cfg.head_dim) : Cap{}, stream, &choice);
     });
 }
 
@@ -858,7 +928,11 @@ sp_status sp_rope_realign(sp_cache* c, int32_t layer, const int32_t* seq_ids, in
     }
     cudaError_t e = flush();
     if (e != cudaSuccess) return cuda_fail(e, "rope launch");
-    return SP_OK;
+    if (!c->bounds.codes) return SP_OK;
+    std::vector<int64_t> lo(n_seqs, pos_lo), hi(n_seqs);
+    for (int b = 0; b < n_seqs; ++b)
+        hi[b] = std::min<int64_t>(pos_hi, c->h_seqlen[(size_t)seq_ids[b] * c->cfg.num_layers + layer]);
+    return update_bounds(c, layer, seq_ids, n_seqs, lo.data(), hi.data(), st);
 }
 
 sp_status sp_pack_seq(sp_cache* c, int32_t seq, void* dst, size_t dst_bytes, size_t* packed_bytes,
@@ -1022,6 +1096,11 @@ sp_status sp_unpack_seq(sp_cache* c, int32_t seq, const void* src, size_t src_by
     tp.payload = const_cast<uint8_t*>(sb + ph.payload_off);
     e = launch_transfer(c, tp, st);
     if (e != cudaSuccess) return cuda_fail(e, "unpack launch");
+    const int64_t from = 0;
+    for (int l = 0; l < L; ++l) {
+        s = update_bounds(c, l, &seq, 1, &from, &nl[l], st);
+        if (s != SP_OK) return s;
+    }
     return SP_OK;
 }
 

@@ -32,6 +32,7 @@
 #pragma once
 #include <algorithm>
 
+#include "sp_bounds.cuh"
 #include "sp_internal.h"
 #include "sp_device.cuh"
 
@@ -146,7 +147,12 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                     const int64_t row = g.unit_row(seq, p.layer, h);
                     const UnitPol pol = p.meta.pol[row];
                     const int32_t* idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off;
-                    const SlotRanges rg = decode_ranges(pol, idx, p.tq[b], P);
+                    // chosen pages lie end to end in a table of their own
+                    const bool chosen = p.kept && pol.kind == kGlobal;
+                    const int64_t t = chosen ? kept_slots((int64_t)p.tq[b] + 1, P, p.kept_cap) - 1 : p.tq[b];
+                    const int32_t* tab = chosen ? p.kept + (int64_t)u * g.max_pages_unit
+                                                : p.meta.ptab + row * g.max_pages_unit;
+                    const SlotRanges rg = decode_ranges(pol, idx, t, P);
                     int64_t j = x - p.item_off[u];
                     int64_t pidx = 0, lo = 0, hi = 0;
                     for (int q = 0; q < rg.count; ++q) {
@@ -159,7 +165,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                         }
                         j -= np;
                     }
-                    int32_t page = p.meta.ptab[row * g.max_pages_unit + pidx];
+                    int32_t page = tab[pidx];
                     if (page < 0 || page >= g.num_pages) {
                         atomicOr(p.meta.status, kStatusBadPage);
                         page = 0; lo = hi = 0;          // load something harmless, use nothing

@@ -84,9 +84,11 @@ __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_
     const uint32_t P = (uint32_t)g.page, lp = 31 - __clz(P);
     const int b = u / g.hkv, h = u - b * g.hkv;
     const int seq = p.seq[b];
-    const int32_t t = p.tq[b];
     const int64_t row = g.unit_row(seq, p.layer, h);
     const UnitPol pol = p.meta.pol[row];
+    // chosen pages lie end to end in a table of their own
+    const bool chosen = p.kept && pol.kind == kGlobal;
+    const int32_t t = chosen ? (int32_t)kept_slots((int64_t)p.tq[b] + 1, (int)P, p.kept_cap) - 1 : p.tq[b];
     // the visible ranges of decode_ranges (sp_rules.h), in 32 bits
     int32_t lo[3] = {0, 0, 0}, hi[3] = {0, 0, 0};
     if (pol.kind == kGlobal) {
@@ -123,7 +125,7 @@ __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_
     // that has one is read in its place
     Item4 it;
     it.visible = (uint32_t)l | ((uint32_t)e << 8);
-    const int32_t* tab = p.meta.ptab + row * g.max_pages_unit;
+    const int32_t* tab = chosen ? p.kept + (int64_t)u * g.max_pages_unit : p.meta.ptab + row * g.max_pages_unit;
     #pragma unroll
     for (int k = 0; k < kD4Groups; ++k) {
         if (P >= kFp4ItemSlots && k > 0) { it.g[k] = it.g[0] + k; continue; }   // one page holds the item

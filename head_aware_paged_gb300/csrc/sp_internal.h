@@ -97,6 +97,10 @@ struct DecodeParams {
     Cap cap;                     // capped scores (cap.on = 0: as they are)
     int32_t scaled;              // 4-bit pages: channel scales other than 1 may be set
     int32_t per, rem;            // 4-bit pages: items of a CTA, CTAs that take one more (launcher)
+    // Pages chosen for the call (null: none): unit u's GLOBAL head reads the physical
+    // pages kept[u * max_pages_unit ..], at most kept_cap, as if they were all.
+    const int32_t* kept;
+    int32_t kept_cap;
     int32_t nst;                 // pipeline stages (set by the launcher)
     int32_t owners;              // consumer warps that own stages (divides nst)
     int32_t merge_floats;        // merge buffer floats (set by the launcher)
@@ -161,6 +165,16 @@ struct Workspace {
     int32_t* deq_row;
 };
 
+// Page bounds (sp_bounds.cuh) and the scratch of the choice of pages, in the
+// buffer of sp_attach_page_bounds; codes is null while there is none.
+struct PageBounds {
+    int8_t* codes = nullptr;        // [num_pages][upper, lower][d]
+    float* step = nullptr;          // [num_pages]
+    uint32_t* score = nullptr;      // [max_batch][hkv][max_pages_unit] order-preserving keys
+    int32_t* kept = nullptr;        // the same: physical pages kept, in order
+    int32_t* tickets = nullptr;     // [max_batch][hkv], zero between calls
+};
+
 }  // namespace sp
 
 struct sp_cache {
@@ -173,6 +187,7 @@ struct sp_cache {
     __nv_bfloat16* vpool = nullptr;
     sp::Meta meta;
     sp::Workspace ws;
+    sp::PageBounds bounds;
     CUtensorMap tm_kpool;   // [num_pages*P rows][d], box {64 or d, P}, 128B swizzle
     CUtensorMap tm_vpool;
     CUtensorMap tm_kpool_half;   // FP8 pages of P >= 64: the same with box {d, P / 2}
@@ -215,6 +230,7 @@ cudaError_t stage_copy(sp_cache* c, int slot, void* dst, size_t bytes, cudaStrea
 // none listed twice.
 bool valid_layer(const sp_cache* c, int32_t layer);
 bool valid_cap(float score_cap);
+int32_t max_unit_pages(const sp_config* c);      // entries of a unit's page table
 sp_status check_seq_list(const sp_cache* c, const int32_t* seq_ids, int32_t n_seqs);
 
 // Armed launch events (sp_set_launch_events): the start is recorded right
@@ -280,6 +296,28 @@ struct DequantParams {
 };
 cudaError_t launch_dequant4(const sp_cache* c, const DequantParams& p, cudaStream_t s);
 cudaError_t launch_rope(const sp_cache* c, const RopeParams& p, cudaStream_t s);
+// The choice of a decode's pages (sp_choose.cu).
+struct ChooseParams {
+    Meta meta;
+    Geo geo;
+    int32_t layer, n_seqs;
+    int32_t first, newest, top, cap;   // pages always kept, chosen ones; cap is their sum
+    int32_t chunk;                     // candidates of a block (launcher)
+    const __nv_bfloat16* q;
+    const int8_t* codes;
+    const float* step;
+    uint32_t* score;
+    int32_t* kept;
+    int32_t* tickets;
+    int32_t* pages;                    // [n_seqs][hkv][cap] page numbers, or null
+    int32_t seq[kMaxCallSeqs], n[kMaxCallSeqs];
+};
+cudaError_t launch_choose(const sp_cache* c, ChooseParams& p, cudaStream_t s);
+// Bounds of the pages that a write of positions [lo[b], hi[b]) of sequence seqs[b]
+// touched, where the cache has them (sp_bounds.cu); the lengths are those after
+// the write.
+sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_seqs,
+                        const int64_t* lo, const int64_t* hi, cudaStream_t stream);
 cudaError_t launch_transfer(const sp_cache* c, const TransferParams& p, cudaStream_t s);
 
 }  // namespace sp

@@ -33,12 +33,11 @@
 // moved on: one that needs new pages is refused, and a captured launch asks the
 // device what each sequence holds by then, before it writes a row or a length
 // (an instance of its own: 28.5 instead of 26.9 us replaying the 8,192 rows).
-#include <cmath>
 #include <cstring>
 #include <memory>
+#include <vector>
 
-#include "sp_device.cuh"
-#include "sp_internal.h"
+#include "sp_rotate.cuh"
 
 namespace sp {
 
@@ -61,27 +60,11 @@ struct WriteParams {
     __nv_bfloat16* q_out;
     void *kpool, *vpool;
     uint64_t turn[64];                     // frequency, in 2^-64 turns a position
+    Axes axes;                             // positions that the angles are taken of, where not the token's own
     int32_t seq[MAXS], n_old[MAXS], n_new[MAXS], pos[MAXS], row0[MAXS + 1];
     int32_t off[MAXU + 1];                 // prefix of the units' new pages
 };
 
-// Eight elements of each half, rotated; fp32.  cs: this chunk's first (cos,
-// sin, cos, sin) of two frequencies, the next two nc further.
-__device__ __forceinline__ void rotate8(const uint4& xa, const uint4& yb, const float4* cs, int nc,
-                                        float* x, float* y) {
-    const uint32_t xw[4] = {xa.x, xa.y, xa.z, xa.w}, yw[4] = {yb.x, yb.y, yb.z, yb.w};
-    #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 u = *reinterpret_cast<const __nv_bfloat162*>(&xw[e]);
-        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&yw[e]);
-        const float x0 = __low2float(u), x1 = __high2float(u), y0 = __low2float(v), y1 = __high2float(v);
-        const float4 c = cs[e * nc];
-        x[2 * e] = x0 * c.x - y0 * c.y;
-        y[2 * e] = y0 * c.x + x0 * c.y;
-        x[2 * e + 1] = x1 * c.z - y1 * c.w;
-        y[2 * e + 1] = y1 * c.z + x1 * c.w;
-    }
-}
 __device__ __forceinline__ void plain8(const uint4& a, float* x) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
     #pragma unroll
@@ -90,9 +73,6 @@ __device__ __forceinline__ void plain8(const uint4& a, float* x) {
         x[2 * e] = __low2float(u);
         x[2 * e + 1] = __high2float(u);
     }
-}
-__device__ __forceinline__ uint4 bf16x8(const float* x) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 // N elements times their channels' reciprocal scales.
 template <int N>
@@ -161,8 +141,8 @@ __device__ __forceinline__ bool row_at(const PR& p, int b, int h, int32_t t, int
 
 // (Five blocks an SM, four for 4-bit pages: with more registers and fewer blocks
 // 28.5 instead of 24.8 us, and 40.2 instead of 31.7 us.)
-// GRAPH: the instance for captured calls.
-template <int KV, bool GRAPH, typename PR>
+// GRAPH: the instance for captured calls.  AXES: angles of positions on several axes.
+template <int KV, bool GRAPH, bool AXES, typename PR>
 __global__ void __launch_bounds__(kWriteThreads, KV == kFp4 ? 4 : 5)
 k_write_rope(const __grid_constant__ PR p) {
     const Geo& g = p.geo;
@@ -200,6 +180,7 @@ k_write_rope(const __grid_constant__ PR p) {
     // angles, [token][pair of a chunk][chunk]: lanes read neighbouring chunks
     __shared__ float4 cs[kMaxTok * 32];
     __shared__ int32_t tok_b[kMaxTok], tok_t[kMaxTok], tok_n[kMaxTok];
+    __shared__ int64_t tok_p[AXES ? kMaxTok * kMaxAxes : 1];             // [token][axis]
     const int D = g.d, half = D / 2;
     const int r0 = (int)blockIdx.x * p.tok, nt = min(p.tok, p.rows - r0);
     // queries: two chunk pairs a pass (four 16-byte loads in flight a thread),
@@ -223,6 +204,11 @@ k_write_rope(const __grid_constant__ PR p) {
         }
     };
     fetch(first);
+    if constexpr (AXES) {
+        const int t = tid / kMaxAxes - 8, a = tid % kMaxAxes;            // (warp 0 looks up the sequences)
+        if (t >= 0 && t < nt && a < p.axes.n)
+            tok_p[t * kMaxAxes + a] = __ldg(p.axes.pos + a * p.axes.axis_stride + (int64_t)(r0 + t) * p.axes.row_stride);
+    }
     if (tid < nt) {
         int a = 0, z = p.n_seqs - 1;                     // sequence with row0[b] <= row < row0[b + 1]
         while (a < z) {
@@ -243,11 +229,8 @@ k_write_rope(const __grid_constant__ PR p) {
     __syncthreads();
     for (int e = tid; e < nt * half; e += kWriteThreads) {
         const int t = e / half, f = e % half;
-        const uint64_t turns = (uint64_t)(uint32_t)tok_t[t] * p.turn[f];
-        // nearest 2^-32 turn, as a signed number of half turns
-        const float x = (float)(int32_t)(uint32_t)((turns + 0x80000000ull) >> 32) * 4.6566128730773926e-10f;
-        float2* c = reinterpret_cast<float2*>(cs + (t * 4 + ((f & 7) >> 1)) * nc + (f >> 3)) + (f & 1);
-        sincospif(x, &c->y, &c->x);
+        const uint64_t at = AXES ? (uint64_t)tok_p[t * kMaxAxes + p.axes.of[f]] : (uint64_t)(uint32_t)tok_t[t];
+        reinterpret_cast<float2*>(cs + (t * 4 + ((f & 7) >> 1)) * nc + (f >> 3))[f & 1] = cos_sin(at * p.turn[f]);
     }
     __syncthreads();
     for (int e0 = first; e0 < q_all; e0 += 2 * stride) {
@@ -349,18 +332,19 @@ typedef WriteParams<kSmallSeqs, kSmallUnits> SmallWrite;
 typedef WriteParams<kMaxCallSeqs, kMaxDecodeUnits> LargeWrite;
 static_assert(sizeof(LargeWrite) <= 32764, "write parameters exceed the kernel parameter space");
 
-template <bool GRAPH, typename PR>
+template <bool GRAPH, bool AXES, typename PR>
 void launch_write(const Geo& g, const PR& p, dim3 grid, cudaStream_t stream) {
-    if (g.fp4) k_write_rope<kFp4, GRAPH><<<grid, kWriteThreads, 0, stream>>>(p);
-    else if (g.fp8) k_write_rope<kFp8, GRAPH><<<grid, kWriteThreads, 0, stream>>>(p);
-    else k_write_rope<kBf16, GRAPH><<<grid, kWriteThreads, 0, stream>>>(p);
+    if (g.fp4) k_write_rope<kFp4, GRAPH, AXES><<<grid, kWriteThreads, 0, stream>>>(p);
+    else if (g.fp8) k_write_rope<kFp8, GRAPH, AXES><<<grid, kWriteThreads, 0, stream>>>(p);
+    else k_write_rope<kBf16, GRAPH, AXES><<<grid, kWriteThreads, 0, stream>>>(p);
 }
 
 template <typename PR>
 sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_seqs,
                      const int32_t* cu, const int64_t* pos, const __nv_bfloat16* q, int64_t q_stride,
                      const __nv_bfloat16* k, int64_t k_stride, const __nv_bfloat16* v,
-                     int64_t v_stride, __nv_bfloat16* q_out, const uint64_t* turn, cudaStream_t stream) {
+                     int64_t v_stride, __nv_bfloat16* q_out, const uint64_t* turn, const Axes* axes,
+                     cudaStream_t stream) {
     std::unique_ptr<PR> pp(new PR());
     PR& p = *pp;
     const int H = c->cfg.num_kv_heads, L = c->cfg.num_layers, P = c->cfg.page_size;
@@ -412,6 +396,7 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     p.q = q; p.k = k; p.v = v; p.q_out = q_out;
     p.kpool = c->kpool; p.vpool = c->vpool;
     std::memcpy(p.turn, turn, sizeof(p.turn));
+    if (axes) p.axes = *axes;
     // Four tokens a block share its set-up once that still fills the GPU (8,192
     // rows, one head of eight GLOBAL, launches included: 27.0 us with four, 28.9
     // with two, 32.9 with eight, for which the arrays of four do not do); a short
@@ -422,8 +407,8 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
     const int split = p.tok == 1 && rows < 2 * c->num_sms && items > kWriteThreads ? 2 : 1;
     const int table = p.new_pages ? (n_seqs * H + kWriteThreads / 32 - 1) / (kWriteThreads / 32) : 0;
     const dim3 grid((unsigned)(p.row_blocks + table), (unsigned)split);
-    if (graph) launch_write<true>(c->geo, p, grid, stream);
-    else launch_write<false>(c->geo, p, grid, stream);
+    if (axes) graph ? launch_write<true, true>(c->geo, p, grid, stream) : launch_write<false, true>(c->geo, p, grid, stream);
+    else graph ? launch_write<true, false>(c->geo, p, grid, stream) : launch_write<false, false>(c->geo, p, grid, stream);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "write launch");
     c->h_free -= demand;
@@ -432,16 +417,10 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
         for (int h = 0; h < H; ++h)
             c->h_npages[((size_t)seqs[b] * L + layer) * H + h] += p.off[b * H + h + 1] - p.off[b * H + h];
     }
-    return SP_OK;
-}
-
-// Does one of `rows` rows of `len` bytes, `stride` bytes apart from `base` on,
-// meet [lo, hi)?
-bool rows_meet(const void* base, int64_t stride, int64_t len, int64_t rows, uintptr_t lo, uintptr_t hi) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(base);
-    const int64_t d = (int64_t)(lo - b) - len;          // the first row that ends behind lo
-    const int64_t r = d < 0 ? 0 : d / stride + 1;
-    return r < rows && b + (uintptr_t)(r * stride) < hi;
+    if (!c->bounds.codes) return SP_OK;
+    std::vector<int64_t> lo(p.pos, p.pos + n_seqs), hi(lo);
+    for (int b = 0; b < n_seqs; ++b) hi[b] += cu[b + 1] - cu[b];
+    return update_bounds(c, layer, seqs, n_seqs, lo.data(), hi.data(), stream);
 }
 
 }  // namespace
@@ -450,11 +429,11 @@ bool rows_meet(const void* base, int64_t stride, int64_t len, int64_t rows, uint
 
 using namespace sp;
 
-extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
-                                       const int32_t* cu_new, const int64_t* pos, const void* q,
-                                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                                       int64_t v_stride, void* q_out, double rope_theta,
-                                       const double* inv_freq, void* stream) {
+// axes: null, or the positions that the angles are taken of (checked).
+static sp_status launch_append_rope(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                                    const int32_t* cu_new, const int64_t* pos, const void* q, int64_t q_stride,
+                                    const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                                    const Axes* axes, double rope_theta, const double* inv_freq, void* stream) {
     if (!c || !cu_new) return fail(SP_ERR_INVALID_ARG, "null argument");
     if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
     sp_status s = check_seq_list(c, seq_ids, n_seqs);
@@ -464,7 +443,7 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
         if (cu_new[b + 1] < cu_new[b]) return fail(SP_ERR_INVALID_ARG, "cu_new must be non-decreasing");
     if (cu_new[n_seqs] > c->cfg.max_tokens) return fail(SP_ERR_INVALID_ARG, "more new tokens than max_tokens");
     if (cu_new[n_seqs] > 0) {                    // (without rows there may be no tensors)
-        if (!k || !v) return fail(SP_ERR_INVALID_ARG, "null argument");
+        if (!k || !v || (axes && !axes->pos)) return fail(SP_ERR_INVALID_ARG, "null argument");
         if ((q == nullptr) != (q_out == nullptr))
             return fail(SP_ERR_INVALID_ARG, "give both q and q_out or neither");
     }
@@ -484,19 +463,11 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
         if ((!in_place && rows_meet(q, q_stride * 2, row * 2, rows, lo, hi)) ||
             rows_meet(k, k_stride * 2, kv * 2, rows, lo, hi) || rows_meet(v, v_stride * 2, kv * 2, rows, lo, hi))
             return fail(SP_ERR_INVALID_ARG, "q_out overlaps q, k or v (it may be q itself if q is contiguous)");
+        if (axes && axes_meet(*axes, rows, lo, hi)) return fail(SP_ERR_INVALID_ARG, "q_out overlaps the positions");
     }
-    if (!inv_freq && (!(rope_theta > 0.0) || !std::isfinite(rope_theta)))
-        return fail(SP_ERR_INVALID_ARG, "rope_theta must be positive and finite");
-    // frequencies as fractions of a turn, modulo one turn (whole turns a
-    // position rotate nothing), in 2^-64 turns
     uint64_t turn[64] = {};
-    const double two_pi = 6.283185307179586476925286766559;
-    for (int i = 0; i < d / 2; ++i) {
-        const double w = inv_freq ? inv_freq[i] : std::pow(rope_theta, -2.0 * i / d);
-        if (!(std::fabs(w) <= 65536.0)) return fail(SP_ERR_INVALID_ARG, "frequencies must be finite, at most 2^16");
-        const double f = w / two_pi, frac = f - std::floor(f);      // [0, 1]
-        turn[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
-    }
+    s = turns_of(rope_theta, inv_freq, d, turn);
+    if (s != SP_OK) return s;
     s = check_device(c);
     if (s != SP_OK) return s;
     auto* qp = static_cast<const __nv_bfloat16*>(q);
@@ -507,8 +478,37 @@ extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t
     return no_throw([&] {
         if (n_seqs <= kSmallSeqs && n_seqs * c->cfg.num_kv_heads <= kSmallUnits)
             return write_rope<SmallWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
-                                          v_stride, qo, turn, st);
+                                          v_stride, qo, turn, axes, st);
         return write_rope<LargeWrite>(c, layer, seq_ids, n_seqs, cu_new, pos, qp, q_stride, kp, k_stride, vp,
-                                      v_stride, qo, turn, st);
+                                      v_stride, qo, turn, axes, st);
     });
+}
+
+extern "C" sp_status sp_append_kv_rope(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                                       const int32_t* cu_new, const int64_t* pos, const void* q,
+                                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, void* q_out, double rope_theta,
+                                       const double* inv_freq, void* stream) {
+    if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
+    const sp_status s = check_device(c);
+    if (s != SP_OK) return s;
+    return launch_append_rope(c, layer, seq_ids, n_seqs, cu_new, pos, q, q_stride, k, k_stride, v, v_stride,
+                              q_out, nullptr, rope_theta, inv_freq, stream);
+}
+
+extern "C" sp_status sp_append_kv_rope_axes(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                                            const int32_t* cu_new, const int64_t* pos, const void* q,
+                                            int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                            int64_t v_stride, void* q_out, const int64_t* axis_pos,
+                                            int64_t axis_stride, int64_t row_stride, int32_t n_axes,
+                                            const int32_t* axis_of, double rope_theta, const double* inv_freq,
+                                            void* stream) {
+    if (!c) return fail(SP_ERR_INVALID_ARG, "null argument");
+    Axes axes{};
+    sp_status s = axes_of(axis_pos, axis_stride, row_stride, n_axes, axis_of, c->cfg.head_dim, axes);
+    if (s != SP_OK) return s;
+    s = check_device(c);
+    if (s != SP_OK) return s;
+    return launch_append_rope(c, layer, seq_ids, n_seqs, cu_new, pos, q, q_stride, k, k_stride, v, v_stride,
+                              q_out, &axes, rope_theta, inv_freq, stream);
 }

@@ -221,6 +221,40 @@ sp_status sp_append_kv_rope(sp_cache* cache, int32_t layer, const int32_t* seq_i
                             void* q_out, double rope_theta, const double* inv_freq,
                             void* stream);
 
+/* The same with angles of positions on several axes (time, height and width of a
+ * video's patches, for one): pair (i, i + head_dim/2) turns by P(axis_of[i], row) *
+ * w_i, w_i as above.  Where the tokens are stored (pos) and where they stand for
+ * the rotation are then two things: pos still counts tokens.
+ *   axis_pos: DEVICE array of int64 positions, element (axis, row) at axis *
+ *     axis_stride + row * row_stride (strides in elements, >= 0; 8-byte aligned;
+ *     rows are those of q, k and v).  Any int64 is a position: p * w is reduced
+ *     modulo a turn in 64-bit fixed point (off by |p w| 2^-53 turns at most).
+ *   n_axes: 1 .. 4; axis_of: host array [head_dim / 2] of axes in [0, n_axes).
+ * q_out may not overlap the positions.  A call captured into a graph reads the
+ * positions when it is replayed. */
+sp_status sp_append_kv_rope_axes(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
+                                 int32_t n_seqs, const int32_t* cu_new, const int64_t* pos,
+                                 const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride,
+                                 void* q_out, const int64_t* axis_pos, int64_t axis_stride,
+                                 int64_t row_stride, int32_t n_axes, const int32_t* axis_of,
+                                 double rope_theta, const double* inv_freq, void* stream);
+
+/* The rotation alone, rows to rows: q_out and k_out get q and k rotated to their
+ * positions on the axes (as in sp_append_kv_rope_axes, the same roundings).  No cache
+ * is involved: a prompt's chunk is rotated by this call, attends
+ * (sp_attention_prefill) and is stored (sp_append_kv).  q [rows] of num_q_heads *
+ * head_dim elements q_stride apart, k likewise (strides in elements, multiples of
+ * 8, at least a row); q_out and k_out contiguous; all 16-byte aligned.  A side with
+ * 0 heads is left out.  An output may be its own input if that is contiguous and
+ * overlaps nothing else.  head_dim 64 or 128 (SP_ERR_UNSUPPORTED otherwise), at
+ * most 1024 heads a side, rows below 2^31.  Runs on the current device. */
+sp_status sp_rope_axes(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k,
+                       int64_t k_stride, int32_t num_kv_heads, int32_t head_dim, int64_t rows,
+                       const int64_t* axis_pos, int64_t axis_stride, int64_t row_stride,
+                       int32_t n_axes, const int32_t* axis_of, double rope_theta,
+                       const double* inv_freq, void* q_out, void* k_out, void* stream);
+
 /* EXECUTE, prefill (runtime article section 4): causal attention of a chunk.
  * Rows cu_q[b] .. cu_q[b+1]-1 of q belong to sequence seq_ids[b] and sit at
  * absolute positions n_b .. n_b + c_b - 1, where n_b is what (seq, layer)
@@ -265,6 +299,46 @@ sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
                                      const int32_t* seq_ids, int32_t n_seqs,
                                      const void* q, float score_cap, void* out,
                                      float* lse, void* stream);
+
+/* Decode over chosen pages: a GLOBAL head reads, of the pages that hold what it
+ * sees, the first sink_pages, the newest recent_pages and the top_pages others with
+ * the highest scores for this query (ties: the lower page); all of them while there
+ * are no more than sink_pages + recent_pages + top_pages.  LOCAL and RETRIEVAL heads
+ * read what sp_attention_decode reads.  Everything else is as there; score_cap as
+ * for sp_attention_decode_capped, 0 for scores as they are.
+ *
+ * A page's score comes from bounds of its keys, kept for every full page of a
+ * GLOBAL head: in each dimension c the largest and smallest of its stored keys
+ * (code * scales, rounded to fp32), on the grid of s = 2^e, the least e in [-50, 50]
+ * with max |key| <= 127 * 2^e: hi_c = ceil(max / s), lo_c = floor(min / s), at most
+ * +-127.  A query head's elements are rounded to a grid t = 2^f chosen the same way,
+ * x_c = round(q_c / t), ties to even.  The head's score is
+ * s t sum_c max(x_c hi_c, x_c lo_c), an upper bound of the rounded query's products
+ * with the page's keys; the page's is the largest of the KV head's query heads.
+ * Scores are exact (whole numbers times powers of two): which pages are kept does
+ * not depend on the order of sums.  A NaN key does not count; with a NaN in q the
+ * pages kept are any, and the row's output is NaN.
+ *   pages: DEVICE array [n_seqs][num_kv_heads][sink_pages + recent_pages + top_pages]
+ *     of the kept pages' numbers (page j holds the tokens from j * page_size on) in
+ *     ascending order, -1 behind the last and for LOCAL and RETRIEVAL heads; nullable.
+ *   recent_pages >= 1 (the newest page has no bounds until it is full), the others
+ *   >= 0; each at most 2^20.
+ *
+ * The bounds live in a caller-owned device buffer (256-byte aligned, at least
+ * sp_page_bounds_bytes bytes: 2 * head_dim + 4 per page, and scratch of the choice),
+ * attached while no sequence holds tokens (SP_ERR_INVALID_ARG otherwise; null
+ * detaches; synchronous).  From then on every call that writes keys (sp_build_cache,
+ * sp_append_kv, the rope forms, sp_rope_realign, sp_unpack_seq) also computes the
+ * bounds of the full pages that it touched, in one more launch; attach the buffer
+ * before capturing such calls.  Two decodes of one cache share the scratch, as they share the
+ * workspace: stream order. */
+sp_status sp_page_bounds_bytes(const sp_config* cfg, size_t* bytes);
+sp_status sp_attach_page_bounds(sp_cache* cache, void* buffer);
+sp_status sp_attention_decode_select(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
+                                     int32_t n_seqs, const void* q, int32_t top_pages,
+                                     int32_t sink_pages, int32_t recent_pages,
+                                     float score_cap, void* out, float* lse, int32_t* pages,
+                                     void* stream);
 
 /* Decode without any device allocation by the caller for scratch: the same
  * computation as sp_attention_decode, but the split-KV scratch (partial
