@@ -667,6 +667,60 @@ static sp_status attention_prefill(sp_cache* c, int32_t layer, const int32_t* se
 // Which pages of the GLOBAL heads a decode keeps (sp_attention_decode_select).
 struct Choice { int32_t first, newest, top; int32_t* pages; };
 
+// The decode over chosen pages in one launch, where that serves: done is set then.
+static sp_status decode_kept(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
+                             const void* q, void* out, float* lse, float score_cap, const Choice& choice,
+                             void* stream, bool& done) {
+    if (!q || !out) return fail(SP_ERR_INVALID_ARG, "null argument");
+    if (!valid_layer(c, layer)) return fail(SP_ERR_INVALID_ARG, "layer out of range");
+    sp_status s = check_seq_list(c, seq_ids, n_seqs);
+    if (s != SP_OK) return s;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 3)
+        return fail(SP_ERR_INVALID_ARG, "q and out must be 4-byte aligned");
+    s = check_device(c);
+    if (s != SP_OK) return s;
+    std::unique_ptr<KeptParams> pp(new KeptParams);      // (its lists are filled as far as they are used)
+    KeptParams& p = *pp;
+    const int P = c->cfg.page_size, H = c->cfg.num_kv_heads;
+    p.first = choice.first;
+    p.newest = choice.newest;
+    p.top = choice.top;
+    p.cap = choice.first + choice.newest + choice.top;
+    for (int b = 0; b < n_seqs; ++b) {
+        const int64_t n = c->h_seqlen[(size_t)seq_ids[b] * c->cfg.num_layers + layer];
+        if (n < 1) return fail(SP_ERR_INVALID_ARG, "decode needs the query's own token appended first");
+        p.seq[b] = seq_ids[b];
+        p.n[b] = (int32_t)n;
+        const int64_t nb = cdiv64(n, P);
+        if (nb <= p.cap) continue;
+        for (int h = 0; h < H; ++h)
+            if (c->h_pol[unit_index(c, seq_ids[b], layer, h)].kind == kGlobal &&
+                (p.cap > kKeptPages || nb - choice.first - choice.newest > kKeptCandidates))
+                return SP_OK;
+    }
+    p.meta = c->meta;
+    p.geo = c->geo;
+    p.layer = layer;
+    p.n_seqs = n_seqs;
+    p.scaled = c->h_scaled[layer];
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.pages = choice.pages;
+    p.codes = c->bounds.codes;
+    p.step = c->bounds.step;
+    p.kpool = reinterpret_cast<const uint8_t*>(c->kpool);
+    p.vpool = reinterpret_cast<const uint8_t*>(c->vpool);
+    p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
+    p.score_cap = score_cap != 0.f ? make_cap(score_cap, c->cfg.head_dim) : Cap{};
+    launch_mark_start(c, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_kept(c, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+    launch_mark_end(c, static_cast<cudaStream_t>(stream));
+    done = true;
+    return SP_OK;
+}
+
 static sp_status attention_decode(sp_cache* c, int32_t layer, const int32_t* seq_ids, int32_t n_seqs,
                                   const void* q, void* out, float* lse, const Cap& cap,
                                   void* stream, const Choice* choice = nullptr) {
@@ -804,6 +858,9 @@ sp_status sp_attention_decode_select(sp_cache* c, int32_t layer, const int32_t* 
     if (reinterpret_cast<uintptr_t>(pages) & 3) return fail(SP_ERR_INVALID_ARG, "pages must be 4-byte aligned");
     return no_throw([&] {
         const Choice choice{sink_pages, recent_pages, top_pages, pages};
+        bool done = false;
+        const sp_status s = decode_kept(c, layer, seq_ids, n_seqs, q, out, lse, score_cap, choice, stream, done);
+        if (s != SP_OK || done) return s;
         return attention_decode(c, layer, seq_ids, n_seqs, q, out, lse,
                                 score_cap != 0.f ? make_cap(score_cap, c->cfg.head_dim) : Cap{}, stream, &choice);
     });

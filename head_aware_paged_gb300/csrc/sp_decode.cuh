@@ -71,6 +71,26 @@ struct DecodeShape {
                                       + 16 /*barrier alignment*/ + 1024 /*base alignment*/;
 };
 
+// A decode over chosen pages is launched while k_choose runs: its table is there
+// after this.
+__device__ __forceinline__ void wait_for_choice() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Launches a decode kernel, early where pages are being chosen for it.
+template <typename... A>
+cudaError_t launch_after_choice(const DecodeParams& p, void (*kernel)(A...), int grid, int threads, int smem,
+                                cudaStream_t s, const A&... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = p.kept ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ int64_t cta_of_item(int64_t x, int64_t T, int G) {
     return (x * G + G - 1) / T;
 }
@@ -149,6 +169,7 @@ k_decode(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtenso
                     const int32_t* idx = p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off;
                     // chosen pages lie end to end in a table of their own
                     const bool chosen = p.kept && pol.kind == kGlobal;
+                    if (chosen) wait_for_choice();
                     const int64_t t = chosen ? kept_slots((int64_t)p.tq[b] + 1, P, p.kept_cap) - 1 : p.tq[b];
                     const int32_t* tab = chosen ? p.kept + (int64_t)u * g.max_pages_unit
                                                 : p.meta.ptab + row * g.max_pages_unit;
@@ -644,8 +665,7 @@ cudaError_t launch_decode_t(const sp_cache* c, DecodeParams& p, int grid, cudaSt
     // the tensor maps' box is one stage's keys: a whole page, or half a page
     const CUtensorMap& tk = Sh::kSub == 2 ? c->tm_kpool_half : c->tm_kpool;
     const CUtensorMap& tv = Sh::kSub == 2 ? c->tm_vpool_half : c->tm_vpool;
-    k_decode<D, P, F8, CAP><<<grid, kDecodeThreads, smem, s>>>(p, tk, tv);
-    return cudaGetLastError();
+    return launch_after_choice(p, k_decode<D, P, F8, CAP>, grid, kDecodeThreads, smem, s, p, tk, tv);
 }
 
 // The instance for the cache's page type, head_dim and page size.

@@ -88,6 +88,7 @@ __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_
     const UnitPol pol = p.meta.pol[row];
     // chosen pages lie end to end in a table of their own
     const bool chosen = p.kept && pol.kind == kGlobal;
+    if (chosen) wait_for_choice();
     const int32_t t = chosen ? (int32_t)kept_slots((int64_t)p.tq[b] + 1, (int)P, p.kept_cap) - 1 : p.tq[b];
     // the visible ranges of decode_ranges (sp_rules.h), in 32 bits
     int32_t lo[3] = {0, 0, 0}, hi[3] = {0, 0, 0};
@@ -667,9 +668,8 @@ cudaError_t launch_decode4_t(const sp_cache* c, DecodeParams& p, int grid, cudaS
         e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    k_decode4<NH, CAP><<<grid, kD4Threads, smem, s>>>(p, reinterpret_cast<const uint8_t*>(c->kpool),
-                                                      reinterpret_cast<const uint8_t*>(c->vpool));
-    return cudaGetLastError();
+    return launch_after_choice(p, k_decode4<NH, CAP>, grid, kD4Threads, smem, s, p,
+                               reinterpret_cast<const uint8_t*>(c->kpool), reinterpret_cast<const uint8_t*>(c->vpool));
 }
 
 template <bool CAP>

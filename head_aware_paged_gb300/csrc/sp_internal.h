@@ -313,6 +313,29 @@ struct ChooseParams {
     int32_t seq[kMaxCallSeqs], n[kMaxCallSeqs];
 };
 cudaError_t launch_choose(const sp_cache* c, ChooseParams& p, cudaStream_t s);
+// A decode over chosen pages in one launch (sp_kept.cuh): units of at most kKeptPages
+// kept pages out of kKeptCandidates.
+constexpr int kKeptPages = 2048, kKeptCandidates = 4096;
+struct KeptParams {
+    Meta meta;
+    Geo geo;
+    int32_t layer, n_seqs;
+    int32_t first, newest, top, cap;   // pages always kept, chosen ones; cap is their sum
+    int32_t scaled;                    // channel scales other than 1 may be set
+    int32_t log_ranks;                 // blocks a unit (launcher)
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    float* lse;
+    int32_t* pages;                    // [n_seqs][hkv][cap] page numbers, or null
+    const int8_t* codes;
+    const float* step;
+    const uint8_t *kpool, *vpool;
+    float scale_log2;                  // log2(e) / sqrt(d)
+    Cap score_cap;
+    int32_t seq[kMaxCallSeqs], n[kMaxCallSeqs];
+};
+cudaError_t launch_kept(const sp_cache* c, KeptParams& p, cudaStream_t s);
+cudaError_t launch_kept_capped(const KeptParams& p, cudaStream_t s);
 // Bounds of the pages that a write of positions [lo[b], hi[b]) of sequence seqs[b]
 // touched, where the cache has them (sp_bounds.cu); the lengths are those after
 // the write.

@@ -1,0 +1,641 @@
+// sp_kept.cuh -- choice and attention of a decode over chosen pages in one launch.
+//
+// A unit (sequence, KV head) reads a few dozen pages here, so what costs time is not
+// the stream but everything around it: a second launch, the look-ups, the merge.
+// A cluster of blocks therefore takes one unit from its query to its output:
+//   1. scores: the blocks share the candidates; every block reads the others' keys
+//      from their shared memory (one cluster barrier) and makes the same choice
+//      (sp_choose.cuh), so no list has to travel back;
+//   2. attention: the unit's visible slots in groups of 16 (a group lies inside a page
+//      whatever the page size), a neighbouring run of them per warp.  There is no
+//      staging: a lane loads its operands' bytes of K and V straight into registers,
+//      the next step's K as soon as the scores are taken and its V after the products;
+//   3. merge: the warps' (o, m, l) in shared memory, the blocks' over the cluster, each
+//      block a part of the output.
+// LOCAL and RETRIEVAL heads, and GLOBAL ones that keep everything, skip the first step.
+//
+// Keys are the M side of m16n8k16 and the query heads the N side, as in
+// sp_decode4.cuh:
+//     S^T = K Q^T      16 keys x 8 heads per group, D / 16 steps
+//     O^T = V^T P^T    16 dimensions x 8 heads, D / 16 tiles
+// The reduction over dimensions may run in any order, so a lane's 16-byte pieces of a
+// key's row serve as they come; V's rows of two keys are interleaved by byte
+// permutations.  P^T goes through two 8 x 8 register transposes.
+//
+// Scores, maxima, sums and partials are fp32; P is rounded to bf16 (2^-9 of a weight;
+// FP8 and 4-bit pages: f16, 2^-12), the query under channel scales to f16.
+#pragma once
+#include <algorithm>
+#include <atomic>
+
+#include "sp_choose.cuh"
+#include "sp_decode4.cuh"
+
+namespace sp {
+
+namespace {
+
+constexpr int kKeptWarps = 4;
+constexpr int kKeptThreads = kKeptWarps * 32;
+
+enum { kRowsBf16, kRowsFp8, kRowsFp4 };
+
+// What a lane holds of a step's NG groups, and the products' operands from it.
+// Lane (gl, j): slots gl and gl + 8 of K, slots 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of V.
+template <int KV, int D>
+struct Rows;
+
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// bf16: a row in 64-byte pieces, 16 bytes of each a lane.
+template <int D>
+struct Rows<kRowsBf16, D> {
+    static constexpr int NP = D * 2 / 64, NG = 4 / NP, NS = D / 128 ? 2 : 1;   // pieces, groups a step, chunk sets of V
+    static constexpr int kGroupBytes = 16 * D * 2;
+    uint4 k[NG][2][NP], v[NG][4][NS];
+    __device__ __forceinline__ void load_k(int q, const uint8_t* grp, int gl, int j) {
+        #pragma unroll
+        for (int r = 0; r < 2; ++r)
+            #pragma unroll
+            for (int i = 0; i < NP; ++i) k[q][r][i] = ld_stream16(grp + (gl + 8 * r) * (D * 2) + 64 * i + 16 * j);
+    }
+    __device__ __forceinline__ void load_v(int q, const uint8_t* grp, int gl, int j) {
+        #pragma unroll
+        for (int r = 0; r < 4; ++r)
+            #pragma unroll
+            for (int i = 0; i < NS; ++i)
+                v[q][r][i] = ld_stream16(grp + (2 * j + (r & 1) + 8 * (r >> 1)) * (D * 2) + (gl + 8 * i) * 16);
+    }
+    __device__ __forceinline__ void clear_k(int q) {
+        #pragma unroll
+        for (int r = 0; r < 2; ++r)
+            #pragma unroll
+            for (int i = 0; i < NP; ++i) k[q][r][i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void clear_v(int q) {
+        #pragma unroll
+        for (int r = 0; r < 4; ++r)
+            #pragma unroll
+            for (int i = 0; i < NS; ++i) v[q][r][i] = make_uint4(0, 0, 0, 0);
+    }
+    // dimension of element e of step s's operand registers (0, 1: the first, 2, 3: the second)
+    __device__ static int q_dim(int s, int e, int j) { return 32 * (s >> 1) + 8 * j + 4 * (s & 1) + e; }
+    __device__ __forceinline__ void k_step(int q, int s, uint32_t (&a)[4]) const {
+        const uint4 &x = k[q][0][s >> 1], &y = k[q][1][s >> 1];
+        a[0] = (s & 1) ? x.z : x.x;
+        a[1] = (s & 1) ? y.z : y.x;
+        a[2] = (s & 1) ? x.w : x.y;
+        a[3] = (s & 1) ? y.w : y.y;
+    }
+    // dimension of tile t, row half i
+    __device__ static int v_dim(int t, int i, int gl) { return 8 * (gl + 8 * (t >> 2)) + 2 * (t & 3) + i; }
+    template <typename F>
+    __device__ __forceinline__ void v_tiles(int q, int, int, F&& f) const {
+        #pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+            uint32_t w[4];
+            #pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = word(v[q][r][t >> 2], t & 3);
+            const uint32_t a[4] = {prmt(w[0], w[1], 0x5410u), prmt(w[0], w[1], 0x7632u), prmt(w[2], w[3], 0x5410u),
+                                   prmt(w[2], w[3], 0x7632u)};
+            f(t, a);
+        }
+    }
+    // slots of this lane's rows of S^T
+    __device__ static int slot_a(int gl) { return gl; }
+};
+
+// FP8: codes become f16 (exact).
+template <>
+struct Rows<kRowsFp8, 128> {
+    static constexpr int NG = 2;
+    static constexpr int kGroupBytes = 16 * 128;
+    uint4 k[NG][2][2], v[NG][4];
+    __device__ __forceinline__ void load_k(int q, const uint8_t* grp, int gl, int j) {
+        #pragma unroll
+        for (int r = 0; r < 2; ++r)
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) k[q][r][i] = ld_stream16(grp + (gl + 8 * r) * 128 + 64 * i + 16 * j);
+    }
+    __device__ __forceinline__ void load_v(int q, const uint8_t* grp, int gl, int j) {
+        #pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = ld_stream16(grp + (2 * j + (r & 1) + 8 * (r >> 1)) * 128 + gl * 16);
+    }
+    __device__ __forceinline__ void clear_k(int q) {
+        #pragma unroll
+        for (int r = 0; r < 2; ++r) k[q][r][0] = k[q][r][1] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void clear_v(int q) {
+        #pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ static int q_dim(int s, int e, int j) { return 64 * (s >> 2) + 16 * j + 4 * (s & 3) + e; }
+    __device__ __forceinline__ void k_step(int q, int s, uint32_t (&a)[4]) const {
+        f16x2x2_of_e4m3x4(word(k[q][0][s >> 2], s & 3), a[0], a[2]);
+        f16x2x2_of_e4m3x4(word(k[q][1][s >> 2], s & 3), a[1], a[3]);
+    }
+    __device__ static int v_dim(int t, int i, int gl) { return 16 * gl + 2 * t + i; }
+    template <typename F>
+    __device__ __forceinline__ void v_tiles(int q, int, int, F&& f) const {
+        #pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t x[4];
+            #pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = word(v[q][r], w);
+            uint32_t a[4], b[4];
+            f16x2x2_of_e4m3x4(prmt(x[0], x[1], 0x5140u), a[0], a[1]);
+            f16x2x2_of_e4m3x4(prmt(x[2], x[3], 0x5140u), a[2], a[3]);
+            f16x2x2_of_e4m3x4(prmt(x[0], x[1], 0x7362u), b[0], b[1]);
+            f16x2x2_of_e4m3x4(prmt(x[2], x[3], 0x7362u), b[2], b[3]);
+            f(2 * w, a);
+            f(2 * w + 1, b);
+        }
+    }
+    __device__ static int slot_a(int gl) { return gl; }
+};
+
+// 4-bit pages: the places of sp_fp4.cuh are those that these operands want.
+template <>
+struct Rows<kRowsFp4, 128> {
+    static constexpr int NG = 4;
+    static constexpr int kGroupBytes = kFp4GroupBytes;
+    uint4 k[NG][2];
+    uint2 v[NG][4];
+    uint32_t ks[NG], vs[NG];
+    __device__ __forceinline__ void load_k(int q, const uint8_t* grp, int gl, int j) {
+        k[q][0] = ld_stream16(grp + gl * 64 + j * 16);
+        k[q][1] = ld_stream16(grp + (gl + 8) * 64 + j * 16);
+        ks[q] = ld_stream4(grp + kFp4ScaleOff + (gl * 4 + j) * 4);
+    }
+    __device__ __forceinline__ void load_v(int q, const uint8_t* grp, int gl, int j) {
+        #pragma unroll
+        for (int t = 0; t < 4; ++t) v[q][t] = ld_stream8(grp + (j + 4 * t) * 64 + (gl ^ ((j & 2) << 1)) * 8);
+        vs[q] = ld_stream4(grp + kFp4ScaleOff + gl * 16 + j * 4);
+    }
+    __device__ __forceinline__ void clear_k(int q) {
+        k[q][0] = k[q][1] = make_uint4(0, 0, 0, 0);
+        ks[q] = 0;
+    }
+    __device__ __forceinline__ void clear_v(int q) {
+        #pragma unroll
+        for (int t = 0; t < 4; ++t) v[q][t] = make_uint2(0, 0);
+        vs[q] = 0;
+    }
+    __device__ static int q_dim(int s, int e, int j) { return 32 * j + 4 * s + e; }
+    __device__ __forceinline__ void k_step(int q, int s, uint32_t (&a)[4]) const {
+        // word s / 2 of both rows: 8 dimensions, two steps; the scale of its block as f16, twice
+        const uint32_t fa = prmt(ks[q], 0u, (s >> 2) ? 0x4141u : 0x4040u) << 7;
+        const uint32_t fb = prmt(ks[q], 0u, (s >> 2) ? 0x4343u : 0x4242u) << 7;
+        uint32_t x[4], y[4];
+        fp4_word_f16(word(k[q][0], s >> 1), x[0], x[1], x[2], x[3]);
+        fp4_word_f16(word(k[q][1], s >> 1), y[0], y[1], y[2], y[3]);
+        a[0] = hmul2(x[2 * (s & 1)], fa);
+        a[1] = hmul2(y[2 * (s & 1)], fb);
+        a[2] = hmul2(x[2 * (s & 1) + 1], fa);
+        a[3] = hmul2(y[2 * (s & 1) + 1], fb);
+    }
+    __device__ static int v_dim(int t, int i, int gl) { return 16 * gl + 2 * t + i; }
+    template <typename F>
+    __device__ __forceinline__ void v_tiles(int q, int, int, F&& f) const {
+        const uint32_t f0 = prmt(vs[q], 0u, 0x4140u) << 7, f1 = prmt(vs[q], 0u, 0x4342u) << 7;
+        constexpr uint32_t kLow = 0x0F0F0F0Fu;
+        #pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t x[4];
+            #pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = w ? v[q][t].y : v[q][t].x;
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            fp4_word_f16((x[0] & kLow) | ((x[1] << 4) & ~kLow), a0[0], a0[1], a0[2], a0[3]);
+            fp4_word_f16(((x[0] >> 4) & kLow) | (x[1] & ~kLow), a1[0], a1[1], a1[2], a1[3]);
+            fp4_word_f16((x[2] & kLow) | ((x[3] << 4) & ~kLow), a2[0], a2[1], a2[2], a2[3]);
+            fp4_word_f16(((x[2] >> 4) & kLow) | (x[3] & ~kLow), a3[0], a3[1], a3[2], a3[3]);
+            #pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t a[4] = {hmul2(a0[t], f0), hmul2(a1[t], f0), hmul2(a2[t], f1), hmul2(a3[t], f1)};
+                f(4 * w + t, a);
+            }
+        }
+    }
+    __device__ static int slot_a(int gl) { return (gl >> 1) + 4 * (gl & 1); }
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared-memory address `local` of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(const void* local, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+// One block of 128 threads a cluster rank.  Registers: three blocks an SM at NH = 1.
+template <int KV, int D, int NH, bool CAP>
+__global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __grid_constant__ KeptParams p) {
+    using R = Rows<KV, D>;
+    constexpr int NG = R::NG, MT = D / 16, KS = D / 16, HF = D + 4;   // groups a step, tiles, steps, a head's floats
+    extern __shared__ __align__(16) float parts[];    // [warps][group][HF], then [group][D] and the weights
+    __shared__ QueryCodes<D, NH> qc;
+    __shared__ ChooseShared<kKeptWarps> sh;
+    __shared__ uint32_t list[kKeptCandidates];
+    __shared__ int32_t kept[kKeptPages];
+    __shared__ __align__(8) float score_scale[8 * NH];
+    const Geo& g = p.geo;
+    const int group = g.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, j = lane & 3;
+    const int u = (int)(blockIdx.x >> p.log_ranks), ranks = 1 << p.log_ranks, rank = blockIdx.x & (ranks - 1);
+    const int b = u / g.hkv, h = u - b * g.hkv, seq = p.seq[b], lp = 31 - __clz(g.page);
+    const int64_t row = g.unit_row(seq, p.layer, h);
+    const UnitPol pol = p.meta.pol[row];
+    const int32_t* tab = p.meta.ptab + row * g.max_pages_unit;
+    const __nv_bfloat16* q0 = p.q + ((int64_t)b * g.hq + h * group) * D;
+    int32_t* pages = p.pages && rank == 0 ? p.pages + (int64_t)u * p.cap : nullptr;
+    const int n = p.n[b], nb = (n + g.page - 1) >> lp;
+    const bool chosen = pol.kind == kGlobal && nb > p.cap;
+
+    if (chosen) {
+        for (int i = tid; i < p.first + p.newest; i += kKeptThreads) {
+            const int at = i < p.first ? i : i + p.top, pg = i < p.first ? i : nb - p.newest + (i - p.first);
+            kept[at] = tab[pg];
+            if (pages) pages[at] = pg;
+        }
+        if (p.top > 0) {
+            const int m = nb - p.first - p.newest;    // candidates, more than p.top
+            const int per = ((m + ranks - 1) / ranks + kTilePages - 1) & ~(kTilePages - 1);
+            const int c0 = min(rank * per, m), c1 = min(c0 + per, m);
+            score_pages<D, NH, kKeptWarps>(p, qc, tab, q0, c0, c1, [&](int c, uint32_t k) { list[c] = k; });
+            if (ranks > 1) {
+                cluster_sync();
+                for (int c = tid; c < m; c += kKeptThreads) {
+                    const int owner = c / per;
+                    if (owner != rank) list[c] = ld_peer(peer_smem(&list[c], owner));
+                }
+            }
+            __syncthreads();
+            choose_top(sh, m, p.top, [&](int c) { return list[c]; }, [&](int at, int c) {
+                kept[p.first + at] = tab[p.first + c];
+                if (pages) pages[p.first + at] = p.first + c;
+            });
+        }
+    } else if (pages) {
+        for (int i = tid; i < p.cap; i += kKeptThreads) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
+    }
+
+    // The query as the products' operand.  bf16 pages: as it is.  Others: f16, times a
+    // power of two per head that takes the largest |q * channel scale| to 2^14 .. 2^15
+    // (sp_decode4.cuh says why); the scores are multiplied back in fp32.
+    const float* kscale = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
+    const float unit_scale = CAP ? p.score_cap.k1 : p.scale_log2;
+    uint32_t qb[NH][KS][2];
+    #pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+        const int head = 8 * nh + gl;
+        float top = 0.f;
+        #pragma unroll
+        for (int s = 0; s < KS; ++s)
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t w = head < group
+                    ? *reinterpret_cast<const uint32_t*>(q0 + head * D + R::q_dim(s, 2 * e, j)) : 0u;
+                qb[nh][s][e] = w;
+                if constexpr (KV != kRowsBf16) {
+                    const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(&w);
+                    float x = __low2float(v2), y = __high2float(v2);
+                    if (p.scaled) {
+                        const float2 f = __ldg(reinterpret_cast<const float2*>(kscale + R::q_dim(s, 2 * e, j)));
+                        x *= f.x;
+                        y *= f.y;
+                    }
+                    top = fmax3_abs(top, x, y);
+                }
+            }
+        float factor = 1.f;
+        if constexpr (KV != kRowsBf16) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = min(max(__float_as_int(top) >> 23, 15), 254);     // 2^(ex - 127) <= top
+            const float up = __int_as_float((268 - ex) << 23);
+            factor = __int_as_float((ex - 14) << 23);
+            #pragma unroll
+            for (int s = 0; s < KS; ++s)
+                #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162*>(&qb[nh][s][e]);
+                    float x = __low2float(v2), y = __high2float(v2);
+                    if (p.scaled) {
+                        const float2 f = __ldg(reinterpret_cast<const float2*>(kscale + R::q_dim(s, 2 * e, j)));
+                        x *= f.x;
+                        y *= f.y;
+                    }
+                    qb[nh][s][e] = pack_f16(x * up, y * up);
+                }
+        }
+        // (this lane's query is head gl, its scores are heads 2 j and 2 j + 1's)
+        if (warp == 0 && j == 0) score_scale[head] = factor * unit_scale;
+    }
+    __syncthreads();
+
+    // The unit's visible slots, in groups of 16; this warp's run [w0, w1) of them.
+    int32_t lo[3], ng[3], hi[3];
+    int total = 0;
+    {
+        const int64_t t = chosen ? kept_slots(n, g.page, p.cap) - 1 : n - 1;
+        const SlotRanges rg = decode_ranges(pol, p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off, t, g.page);
+        #pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            lo[i] = (int32_t)rg.lo[i];
+            hi[i] = (int32_t)rg.hi[i];
+            ng[i] = hi[i] > lo[i] ? ((hi[i] - 1) >> 4) - (lo[i] >> 4) + 1 : 0;
+            total += ng[i];
+        }
+    }
+    const int runs = ranks * kKeptWarps, run = rank * kKeptWarps + warp;
+    const int w0 = (int)((int64_t)total * run / runs), w1 = (int)((int64_t)total * (run + 1) / runs);
+    // Lane i of a batch of 32: group w0 + batch + i's place in the pool (in groups)
+    // and its visible slots, low | high << 8 (0: none).
+    uint32_t place = 0, seen = 0;
+    int batch = -32;
+    auto look_up = [&](int i) {
+        int at = i;
+        place = seen = 0;
+        #pragma unroll
+        for (int r = 0; r < 3; ++r) {
+            if (at >= 0 && at < ng[r]) {
+                const int32_t slot = ((lo[r] >> 4) + at) << 4, pg = slot >> lp;
+                const int32_t page = chosen ? kept[pg] : tab[pg];
+                if (page < 0 || page >= g.num_pages) {
+                    atomicOr(p.meta.status, kStatusBadPage);
+                } else {
+                    place = (((uint32_t)page << lp) + (uint32_t)(slot & (g.page - 1))) >> 4;
+                    seen = (uint32_t)max(lo[r] - slot, 0) | ((uint32_t)min(hi[r] - slot, 16) << 8);
+                }
+            }
+            at -= ng[r];
+        }
+    };
+    R rows;
+    uint32_t vis[NG], vat[NG];                        // visible slots; places, for V
+    auto take = [&](int i) {                          // groups w0 + i ...: look-ups, loads of K
+        if (i >= batch + 32) {
+            batch += 32;
+            if (w0 + batch + lane < w1) look_up(w0 + batch + lane); else place = seen = 0;
+        }
+        #pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            vis[q] = __shfl_sync(0xffffffffu, seen, i + q - batch);
+            vat[q] = __shfl_sync(0xffffffffu, place, i + q - batch);
+            if (vis[q]) rows.load_k(q, p.kpool + (int64_t)vat[q] * R::kGroupBytes, gl, j);
+            else rows.clear_k(q);
+        }
+    };
+    auto take_v = [&] {
+        #pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            if (vis[q]) rows.load_v(q, p.vpool + (int64_t)vat[q] * R::kGroupBytes, gl, j);
+            else rows.clear_v(q);                     // (weight 0 times what the registers held would not do)
+        }
+    };
+    float o[NH][MT][4], m_run[NH][2], l_run[NH][2];
+    #pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+        m_run[nh][0] = m_run[nh][1] = -INFINITY;
+        l_run[nh][0] = l_run[nh][1] = 0.f;
+        #pragma unroll
+        for (int t = 0; t < MT; ++t)
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) o[nh][t][e] = 0.f;
+    }
+    const int mine = w1 - w0;
+    if (mine > 0) { take(0); take_v(); }
+    for (int i = 0; i < mine; i += NG) {
+        float sc[NG][NH][4];
+        #pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            #pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) sc[q][nh][e] = 0.f;
+            #pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                uint32_t a[4];
+                rows.k_step(q, s, a);
+                #pragma unroll
+                for (int nh = 0; nh < NH; ++nh) {
+                    if constexpr (KV == kRowsBf16) mma_bf16_16816(sc[q][nh], a, qb[nh][s][0], qb[nh][s][1]);
+                    else mma_f16_16816(sc[q][nh], a, qb[nh][s][0], qb[nh][s][1]);
+                }
+            }
+        }
+        uint32_t now[NG];
+        #pragma unroll
+        for (int q = 0; q < NG; ++q) now[q] = vis[q];
+        const bool more = i + NG < mine;
+        if (more) take(i + NG);
+        const int sa = R::slot_a(gl), sb = sa + 8;
+        float mx[NH][2];
+        bool grew = false;
+        #pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const float2 f = *reinterpret_cast<const float2*>(&score_scale[8 * nh + 2 * j]);
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) mx[nh][e] = -INFINITY;
+            #pragma unroll
+            for (int q = 0; q < NG; ++q) {
+                const int from = now[q] & 0xFF, to = now[q] >> 8;
+                const bool in_a = sa >= from && sa < to, in_b = sb >= from && sb < to;
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = sc[q][nh][e] * ((e & 1) ? f.y : f.x);
+                    if constexpr (CAP) x = capped_log2(x, p.score_cap);
+                    x = (e < 2 ? in_a : in_b) ? x : -INFINITY;
+                    sc[q][nh][e] = x;
+                    mx[nh][e & 1] = fmaxf(mx[nh][e & 1], x);
+                }
+            }
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) grew = grew || mx[nh][e] > m_run[nh][e] + kRefAbove;
+        }
+        // the exponentials' reference, raised only when a score passes it by kRefAbove
+        if (__any_sync(0xffffffffu, grew)) {
+            #pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+                #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = mx[nh][e];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    const float m_new = fmaxf(m_run[nh][e], x - kRefBelow);
+                    const float alpha = fast_exp2(m_run[nh][e] - (m_new == -INFINITY ? 0.f : m_new));
+                    m_run[nh][e] = m_new;
+                    l_run[nh][e] *= alpha;
+                    #pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        o[nh][t][e] *= alpha;
+                        o[nh][t][2 + e] *= alpha;
+                    }
+                }
+        }
+        uint32_t pb[NG][NH][2];
+        #pragma unroll
+        for (int q = 0; q < NG; ++q)
+            #pragma unroll
+            for (int nh = 0; nh < NH; ++nh) {
+                float w[4];
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float ref = m_run[nh][e & 1] == -INFINITY ? 0.f : m_run[nh][e & 1];
+                    w[e] = fast_exp2(sc[q][nh][e] - ref);
+                    l_run[nh][e & 1] += w[e];
+                }
+                if constexpr (KV == kRowsBf16) {
+                    pb[q][nh][0] = transpose8x8(pack_bf16(w[0], w[1]));
+                    pb[q][nh][1] = transpose8x8(pack_bf16(w[2], w[3]));
+                } else {
+                    pb[q][nh][0] = transpose8x8(pack_f16(w[0], w[1]));
+                    pb[q][nh][1] = transpose8x8(pack_f16(w[2], w[3]));
+                }
+            }
+        #pragma unroll
+        for (int q = 0; q < NG; ++q)
+            rows.v_tiles(q, gl, j, [&](int t, const uint32_t (&a)[4]) {
+                #pragma unroll
+                for (int nh = 0; nh < NH; ++nh) {
+                    if constexpr (KV == kRowsBf16) mma_bf16_16816(o[nh][t], a, pb[q][nh][0], pb[q][nh][1]);
+                    else mma_f16_16816(o[nh][t], a, pb[q][nh][0], pb[q][nh][1]);
+                }
+            });
+        if (more) take_v();
+    }
+
+    // ------------------------------- merge -------------------------------
+    float* mine_o = parts + warp * group * HF;
+    float* block_o = parts + kKeptWarps * group * HF;               // [group][D]
+    float2* warp_ml = reinterpret_cast<float2*>(block_o + group * D);   // [warps][group]
+    float2* block_ml = warp_ml + kKeptWarps * group;                // [group]
+    const float* vscale = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
+    #pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+        #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = l_run[nh][e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int head = 8 * nh + 2 * j + e;
+            if (head >= group) continue;
+            #pragma unroll
+            for (int t = 0; t < MT; ++t)
+                *reinterpret_cast<float2*>(mine_o + head * HF + R::v_dim(t, 0, gl)) =
+                    make_float2(o[nh][t][e], o[nh][t][2 + e]);
+            if (gl == 0) warp_ml[warp * group + head] = make_float2(m_run[nh][e], l);
+        }
+    __syncthreads();
+    __nv_bfloat16* out = p.out + ((int64_t)b * g.hq + h * group) * D;
+    float* lse = p.lse ? p.lse + (int64_t)b * g.hq + h * group : nullptr;
+    // a unit without a visible token: O = 0, LSE = -inf
+    auto finish = [&](int r, int c, float acc, float m, float l) {
+        if (KV != kRowsBf16 && p.scaled) acc *= __ldg(vscale + c);
+        out[r * D + c] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+        if (c == 0 && lse) lse[r] = (m + __log2f(l)) * 0.69314718055994531f;
+    };
+    for (int e = tid; e < group * D; e += kKeptThreads) {
+        const int r = e / D, c = e % D;
+        float m = -INFINITY, l = 0.f, acc = 0.f;
+        #pragma unroll
+        for (int w = 0; w < kKeptWarps; ++w) m = fmaxf(m, warp_ml[w * group + r].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        #pragma unroll
+        for (int w = 0; w < kKeptWarps; ++w) {
+            const float2 ml = warp_ml[w * group + r];
+            const float f = fast_exp2(ml.x - ref);
+            l += f * ml.y;
+            acc += f * parts[(w * group + r) * HF + c];
+        }
+        if (ranks == 1) {
+            finish(r, c, acc, m, l);
+        } else {
+            block_o[e] = acc;
+            if (c == 0) block_ml[r] = make_float2(m, l);
+        }
+    }
+    if (ranks == 1) return;
+    cluster_sync();
+    for (int e = rank * kKeptThreads + tid; e < group * D; e += ranks * kKeptThreads) {
+        const int r = e / D, c = e % D;
+        float m = -INFINITY, l = 0.f, acc = 0.f;
+        for (int i = 0; i < ranks; ++i) m = fmaxf(m, __uint_as_float(ld_peer(peer_smem(&block_ml[r].x, i))));
+        const float ref = m == -INFINITY ? 0.f : m;
+        for (int i = 0; i < ranks; ++i) {
+            const float f = fast_exp2(__uint_as_float(ld_peer(peer_smem(&block_ml[r].x, i))) - ref);
+            l += f * __uint_as_float(ld_peer(peer_smem(&block_ml[r].y, i)));
+            acc += f * __uint_as_float(ld_peer(peer_smem(&block_o[e], i)));
+        }
+        finish(r, c, acc, m, l);
+    }
+    cluster_sync();                                   // no block leaves while another reads its parts
+}
+
+template <int KV, int D, int NH, bool CAP>
+cudaError_t launch_kept_t(const KeptParams& p, cudaStream_t s) {
+    const int group = p.geo.group;
+    const int smem = (kKeptWarps * group * (D + 4) + group * D + 2 * (kKeptWarps + 1) * group) * 4;
+    auto kernel = k_kept<KV, D, NH, CAP>;
+    static std::atomic<uint64_t> ready{0};            // devices on which the attributes are set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        constexpr int kMost = (kKeptWarps * 8 * NH * (D + 4) + 8 * NH * D + 2 * (kKeptWarps + 1) * 8 * NH) * 4;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 1u << p.log_ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.n_seqs * p.geo.hkv) << p.log_ranks);
+    cfg.blockDim = dim3(kKeptThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool CAP>
+cudaError_t launch_kept_any(const KeptParams& p, cudaStream_t s) {
+    const bool wide = p.geo.group > 8;
+    if (p.geo.fp4) return wide ? launch_kept_t<kRowsFp4, 128, 2, CAP>(p, s) : launch_kept_t<kRowsFp4, 128, 1, CAP>(p, s);
+    if (p.geo.fp8) return wide ? launch_kept_t<kRowsFp8, 128, 2, CAP>(p, s) : launch_kept_t<kRowsFp8, 128, 1, CAP>(p, s);
+    if (p.geo.d == 128)
+        return wide ? launch_kept_t<kRowsBf16, 128, 2, CAP>(p, s) : launch_kept_t<kRowsBf16, 128, 1, CAP>(p, s);
+    return wide ? launch_kept_t<kRowsBf16, 64, 2, CAP>(p, s) : launch_kept_t<kRowsBf16, 64, 1, CAP>(p, s);
+}
+
+}  // namespace
+
+}  // namespace sp

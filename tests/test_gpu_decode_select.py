@@ -170,18 +170,19 @@ def test_pages_and_outputs(kv, d, P, hq, hkv):
 
 
 @pytest.mark.parametrize("kv,P", [("bf16", 64), ("fp8", 16), ("fp4", 32)])
-def test_all_pages_kept_is_decode(kv, P):
+def test_all_pages_kept(kv, P):
+    """More pages asked for than there are: plain attention over everything that
+    is seen; the outputs do not depend on which of them are asked for."""
     gpu_ready()
     hkv, hq, d = 8, 32, 128
+    pols = _classes(hkv)
     c = _mk(hq, hkv, d, P, 2, 1000, kv=kv)
     for s in range(2):
-        c.set_policy(s, to_c_policies([_classes(hkv)]))
+        c.set_policy(s, to_c_policies([pols]))
         c.build(s, 0, _keys(700 + 200 * s, hkv, d, s), W.normal((700 + 200 * s, hkv, d), s + 5, device="cuda"))
     q = W.normal((2, hq, d), 9, device="cuda")
     for cap in (None, 30.0):
-        want = c.decode(0, [0, 1], q, score_cap=cap)
-        got = c.decode_select(0, [0, 1], q, 1000, score_cap=cap)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        want = _check_select(c, [0, 1], pols, q, 1000, 1, 1, cap=cap)
         got = c.decode_select(0, [0, 1], q, 1000, score_cap=cap, want_pages=False, want_lse=False)
         assert torch.equal(got[0], want[0]) and got[1] is None and got[2] is None
 
