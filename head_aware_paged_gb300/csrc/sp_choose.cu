@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kChooseThreads = 256;
 constexpr int kChooseWarps = kChooseThreads / 32;
+static_assert(kListKeys <= 17 * kChooseThreads, "a block's registers hold the list");
 
 // NH: steps of 8 query heads (group <= 8 NH).
 template <int D, int NH>
@@ -57,8 +58,12 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose(const __grid_constant
     if (p.top == 0) return;
     const bool alone = m <= p.chunk, listed = m <= kListKeys;
     uint32_t* key = p.score + (int64_t)u * g.max_pages_unit;
-    score_pages<D, NH, kChooseWarps>(p, qc, tab, p.q + ((int64_t)b * g.hq + h * g.group) * D, c0, c1,
-                                     [&](int c, uint32_t k) { if (alone && listed) list[c] = k; else key[c] = k; });
+    int32_t id[kTiles];
+    first_pages<kChooseWarps>(tab, p.first, c0, c1, id);
+    score_pages<D, NH, kChooseWarps>(p, qc, tab, p.q + ((int64_t)b * g.hq + h * g.group) * D, c0, c1, id, [] {},
+                                     [&](int c, uint32_t k, int half) {
+                                         if (half == 0) (alone && listed ? list : key)[c] = k;
+                                     });
     if (!alone) {
         __threadfence();
         __syncthreads();
@@ -73,10 +78,12 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose(const __grid_constant
             for (int c = tid; c < m; c += kChooseThreads) list[c] = __ldcg(key + c);
     }
     __syncthreads();
-    choose_top(sh, m, p.top, [&](int c) { return listed ? list[c] : __ldcg(key + c); }, [&](int at, int c) {
+    auto take = [&](int at, int c) {
         kept[p.first + at] = tab[p.first + c];
         if (pages) pages[p.first + at] = p.first + c;
-    });
+    };
+    if (listed) choose_top<17, kChooseWarps>(sh, m, p.top, [&](int c) { return list[c]; }, take);
+    else choose_top<0, kChooseWarps>(sh, m, p.top, [&](int c) { return __ldcg(key + c); }, take);
 }
 
 }  // namespace

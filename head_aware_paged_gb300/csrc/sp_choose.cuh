@@ -37,20 +37,35 @@ struct QueryCodes {
     float step[8 * NH];
 };
 
-// Keys of candidates [c0, c1) (page first + c of the unit), kTilePages a warp and
-// pass; emit(c, key) is called by one lane each.  NH: steps of 8 query heads.  Every
-// thread of the block takes part (one barrier).
-template <int D, int NH, int WARPS, typename P, typename F>
+// Physical pages of this lane's candidates in its warp's first kTiles tiles of
+// [c0, c1) (candidate c is page first + c of the unit).
+constexpr int kTiles = 2;
+template <int WARPS>
+__device__ __forceinline__ void first_pages(const int32_t* tab, int first, int c0, int c1, int32_t (&id)[kTiles]) {
+    #pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int c = c0 + ((threadIdx.x >> 5) + t * WARPS) * kTilePages + (threadIdx.x & 15);
+        id[t] = c < c1 ? tab[first + c] : 0;
+    }
+}
+
+// Keys of candidates [c0, c1): a warp takes every WARPS-th tile, kTiles of them in
+// flight, the first ones' pages given.  emit(c, key, half) is called for each by
+// two lanes, half 0 and 1; ready() once before the first.  NH: steps of 8 query
+// heads.  Every thread of the block takes part (one barrier).
+template <int D, int NH, int WARPS, typename P, typename G, typename F>
 __device__ __forceinline__ void score_pages(const P& p, QueryCodes<D, NH>& qc, const int32_t* tab, const __nv_bfloat16* q,
-                                            int c0, int c1, F&& emit) {
+                                            int c0, int c1, int32_t (&id)[kTiles], G&& ready, F&& emit) {
     constexpr int NC = 2 * D / 64;                    // 64-byte pieces of a page's bounds
+    constexpr int kStep = WARPS * kTilePages;
     const Geo& g = p.geo;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, j = lane & 3;
-    uint4 x[NC][2];
-    float st[2];
-    auto load = [&](int base) {
-        const int c = base + warp * kTilePages + (lane & 15);
-        int32_t page = c < c1 ? tab[p.first + c] : 0;
+    struct Tile { uint4 x[NC][2]; float st[2]; };
+    auto page_of = [&](int base) {                    // of this lane's candidate of a tile
+        const int c = base + (lane & 15);
+        return c < c1 ? tab[p.first + c] : 0;
+    };
+    auto load = [&](Tile& t, int32_t page) {
         if (page < 0 || page >= g.num_pages) {
             atomicOr(p.meta.status, kStatusBadPage);
             page = 0;
@@ -60,25 +75,40 @@ __device__ __forceinline__ void score_pages(const P& p, QueryCodes<D, NH>& qc, c
             const int32_t pg = __shfl_sync(0xffffffffu, page, gl + 8 * r);
             const uint4* src = reinterpret_cast<const uint4*>(p.codes + (int64_t)pg * 2 * D) + j;
             #pragma unroll
-            for (int i = 0; i < NC; ++i) x[i][r] = __ldg(src + 4 * i);
-            st[r] = __ldg(p.step + pg);
+            for (int i = 0; i < NC; ++i) t.x[i][r] = __ldg(src + 4 * i);
+            t.st[r] = __ldg(p.step + pg);
         }
     };
-    load(c0);
-    for (int r = warp; r < 8 * NH; r += WARPS) {      // the query heads' codes
-        float v[D / 32], top = 0.f;
+    Tile tile[kTiles];
+    const int base0 = c0 + warp * kTilePages;
+    // the query heads' codes (a head that is not there: whatever the memory held, not used)
+    float v[(8 * NH + WARPS - 1) / WARPS][D / 32];
+    #pragma unroll
+    for (int k = 0; k * WARPS < 8 * NH; ++k)
         #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            v[i] = r < g.group ? __bfloat162float(q[r * D + lane * (D / 32) + i]) : 0.f;
-            top = fmaxf(top, fabsf(v[i]));
+            const int r = warp + k * WARPS;
+            v[k][i] = r < g.group ? __bfloat162float(q[r * D + lane * (D / 32) + i]) : 0.f;
         }
+    #pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        if (base0 + t * kStep < c1) load(tile[t], id[t]);
+        id[t] = page_of(base0 + (t + kTiles) * kStep);
+    }
+    #pragma unroll
+    for (int k = 0; k * WARPS < 8 * NH; ++k) {
+        const int r = warp + k * WARPS;
+        if (r >= g.group) break;
+        float top = 0.f;
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(v[k][i]));
+        // (of floats that are not negative, the largest is the largest pattern)
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         const int e = grid_exponent(top);
         const float up = grid_step(-e);
         #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            const int code = (int)rintf(fminf(fmaxf(v[i] * up, -127.f), 127.f));
+            const int code = (int)rintf(fminf(fmaxf(v[k][i] * up, -127.f), 127.f));
             qc.code[r][lane * (D / 32) + i] = (uint8_t)max(code, 0);
             qc.code[r][D + lane * (D / 32) + i] = (uint8_t)min(code, 0);
         }
@@ -94,30 +124,39 @@ __device__ __forceinline__ void score_pages(const P& p, QueryCodes<D, NH>& qc, c
         #pragma unroll
         for (int e = 0; e < 2; ++e) qs[nh][e] = qc.step[8 * nh + 2 * j + e];
     }
-    for (int base = c0; base < c1; base += WARPS * kTilePages) {
+    ready();
+    auto score = [&](const Tile& t, int base) {
         float best[2] = {-INFINITY, -INFINITY};
         #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
             int s[4] = {0, 0, 0, 0};
             #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                mma_s8_16832(s, x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, qb[nh][i].x, qb[nh][i].y);
-                mma_s8_16832(s, x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, qb[nh][i].z, qb[nh][i].w);
+                mma_s8_16832(s, t.x[i][0].x, t.x[i][1].x, t.x[i][0].y, t.x[i][1].y, qb[nh][i].x, qb[nh][i].y);
+                mma_s8_16832(s, t.x[i][0].z, t.x[i][1].z, t.x[i][0].w, t.x[i][1].w, qb[nh][i].z, qb[nh][i].w);
             }
             #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (8 * nh + 2 * j + (e & 1) < g.group)
-                    best[e >> 1] = fmaxf(best[e >> 1], (float)s[e] * (qs[nh][e & 1] * st[e >> 1]));
+                    best[e >> 1] = fmaxf(best[e >> 1], (float)s[e] * (qs[nh][e & 1] * t.st[e >> 1]));
         }
-        if (base + WARPS * kTilePages < c1) load(base + WARPS * kTilePages);
         #pragma unroll
         for (int r = 0; r < 2; ++r) {
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
         }
-        const int c = base + warp * kTilePages + gl + 8 * j;
-        if (j < 2 && c < c1) emit(c, score_key(j ? best[1] : best[0]));
-    }
+        const int c = base + gl + 8 * (j & 1);
+        if (c < c1) emit(c, score_key((j & 1) ? best[1] : best[0]), j >> 1);
+    };
+    for (int base = base0; base < c1; base += kTiles * kStep)
+        #pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int at = base + t * kStep, next = at + kTiles * kStep;
+            if (at >= c1) break;
+            score(tile[t], at);
+            if (next < c1) load(tile[t], id[t]);
+            id[t] = page_of(next + kTiles * kStep);
+        }
 }
 
 template <int WARPS>
@@ -129,23 +168,41 @@ struct ChooseShared {
 
 // The `top` highest of keys 0 .. m - 1 (top < m; ties: the lower index): calls
 // emit(rank in order of index, index) for each.  Every thread of the block takes
-// part; the keys are in place before the call.
+// part; the keys are in place before the call.  A thread's run of neighbouring keys
+// is held in registers, K of them (m <= 32 WARPS K, K odd), or read again for every
+// pass (K = 0).
 //
 // Keys at or above `cut` are taken, and of those in [low, cut) the first `want`
 // (once they are all equal).  A pass counts a range's keys in bins and keeps the one
 // that the want-th highest lies in; the first spans the keys' own range, so that few
 // share a bin and one pass mostly does.
-template <int WARPS, typename K, typename F>
-__device__ __forceinline__ void choose_top(ChooseShared<WARPS>& sh, int m, int top, K&& key_at, F&& emit) {
+template <int K, int WARPS, typename G, typename F>
+__device__ __forceinline__ void choose_top(ChooseShared<WARPS>& sh, int m, int top, G&& key_at, F&& emit) {
     constexpr int T = WARPS * 32, kBinBits = WARPS == 8 ? 10 : 9;
     static_assert(4 * T == 1 << kBinBits, "four bins a thread");
+    static_assert(K == 0 || K % 2 == 1, "odd runs: no two lanes on one bank");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = ((m + T - 1) / T) | 1, r0 = min(tid * per, m), r1 = min(r0 + per, m);
+    uint32_t held[K > 0 ? K : 1];
+    if constexpr (K > 0) {
+        #pragma unroll
+        for (int i = 0; i < K; ++i) held[i] = r0 + i < r1 ? key_at(r0 + i) : 0u;
+    }
+    // f(key, index) for this thread's keys, in order
+    auto each = [&](auto&& f) {
+        if constexpr (K > 0) {
+            #pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (r0 + i < r1) f(held[i], r0 + i);
+        } else {
+            for (int c = r0; c < r1; ++c) f(key_at(c), c);
+        }
+    };
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    for (int c = tid; c < m; c += T) {
-        const uint32_t k = key_at(c);
+    each([&](uint32_t k, int) {
         lo = min(lo, k);
         hi = max(hi, k);
-    }
+    });
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) { sh.warp_min[warp] = lo; sh.warp_max[warp] = hi; }
@@ -156,10 +213,9 @@ __device__ __forceinline__ void choose_top(ChooseShared<WARPS>& sh, int m, int t
     uint32_t low = lo, wide = hi - lo, cut;           // the range is [low, low + wide]
     int want = top, shift = max(0, 32 - __clz(hi - lo) - kBinBits);
     while (true) {
-        for (int c = tid; c < m; c += T) {
-            const uint32_t k = key_at(c);
+        each([&](uint32_t k, int) {
             if (k >= low && k - low <= wide) atomicAdd(&sh.hist[(k - low) >> shift], 1);
-        }
+        });
         __syncthreads();
         const int4 f = *reinterpret_cast<const int4*>(&sh.hist[4 * tid]);
         int s = f.x + f.y + f.z + f.w;                // of this thread's bins and all above
@@ -200,16 +256,13 @@ __device__ __forceinline__ void choose_top(ChooseShared<WARPS>& sh, int m, int t
         wide = (1u << shift) - 1;
         shift = max(0, shift - kBinBits);
     }
-    // Thread t's run of keys (an odd number of them: no two lanes on one bank): how
-    // many are at or above the cut, how many below it; then all of the former and
-    // the first `want` of the latter, in order.
-    const int per = ((m + T - 1) / T) | 1, r0 = min(tid * per, m), r1 = min(r0 + per, m);
+    // How many keys of the run are at or above the cut, how many on the bin below it;
+    // then all of the former and the first `want` of the latter, in order.
     int above = 0, on = 0;
-    for (int c = r0; c < r1; ++c) {
-        const uint32_t k = key_at(c);
+    each([&](uint32_t k, int) {
         above += k >= cut;
         on += k >= low && k < cut;
-    }
+    });
     int sa = above, so = on;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -223,13 +276,12 @@ __device__ __forceinline__ void choose_top(ChooseShared<WARPS>& sh, int m, int t
         if (w < warp) { sa += sh.warp_sum[0][w]; so += sh.warp_sum[1][w]; }
     sa -= above;
     so -= on;
-    for (int c = r0; c < r1; ++c) {
-        const uint32_t k = key_at(c);
+    each([&](uint32_t k, int c) {
         const bool up = k >= cut, tie = !up && k >= low;
         if (up || (tie && so < want)) emit(sa + min(so, want), c);
         sa += up;
         so += tie;
-    }
+    });
 }
 
 }  // namespace

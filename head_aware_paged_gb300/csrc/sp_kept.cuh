@@ -3,15 +3,15 @@
 // A unit (sequence, KV head) reads a few dozen pages here, so what costs time is not
 // the stream but everything around it: a second launch, the look-ups, the merge.
 // A cluster of blocks therefore takes one unit from its query to its output:
-//   1. scores: the blocks share the candidates; every block reads the others' keys
-//      from their shared memory (one cluster barrier) and makes the same choice
+//   1. scores: the blocks share the candidates and write each key into every block's
+//      shared memory; after one cluster barrier all make the same choice
 //      (sp_choose.cuh), so no list has to travel back;
 //   2. attention: the unit's visible slots in groups of 16 (a group lies inside a page
 //      whatever the page size), a neighbouring run of them per warp.  There is no
 //      staging: a lane loads its operands' bytes of K and V straight into registers,
 //      the next step's K as soon as the scores are taken and its V after the products;
-//   3. merge: the warps' (o, m, l) in shared memory, the blocks' over the cluster, each
-//      block a part of the output.
+//   3. merge: the warps' (o, m, l) meet in shared memory, the blocks' sums are written
+//      to the block that finishes them (each a part of the output): one barrier.
 // LOCAL and RETRIEVAL heads, and GLOBAL ones that keep everything, skip the first step.
 //
 // Keys are the M side of m16n8k16 and the query heads the N side, as in
@@ -37,8 +37,12 @@ namespace {
 
 constexpr int kKeptWarps = 4;
 constexpr int kKeptThreads = kKeptWarps * 32;
+static_assert(kKeptCandidates <= 33 * kKeptThreads, "a block's registers hold the keys");
 
 enum { kRowsBf16, kRowsFp8, kRowsFp4 };
+
+template <int N>
+struct Count { static constexpr int value = N; };
 
 // What a lane holds of a step's NG groups, and the products' operands from it.
 // Lane (gl, j): slots gl and gl + 8 of K, slots 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of V.
@@ -235,34 +239,36 @@ struct Rows<kRowsFp4, 128> {
     __device__ static int slot_a(int gl) { return (gl >> 1) + 4 * (gl & 1); }
 };
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Shared-memory address `local` of block `rank` of the cluster.
+// A cluster's barrier; the first one only says that every block runs (its shared
+// memory may be written from then on).
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores to shared memory of block `rank` of the cluster, at this block's address.
 __device__ __forceinline__ uint32_t peer_smem(const void* local, int rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
-    uint32_t r;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-    return r;
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // One block of 128 threads a cluster rank.  Registers: three blocks an SM at NH = 1.
 template <int KV, int D, int NH, bool CAP>
 __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __grid_constant__ KeptParams p) {
     using R = Rows<KV, D>;
-    constexpr int NG = R::NG, MT = D / 16, KS = D / 16, HF = D + 4;   // groups a step, tiles, steps, a head's floats
-    extern __shared__ __align__(16) float parts[];    // [warps][group][HF], then [group][D] and the weights
+    constexpr int NG = R::NG, MT = D / 16, KS = D / 16, HF = D + 8;   // groups a step, tiles, steps, a head's floats
+    extern __shared__ __align__(16) float parts[];    // [warps][group][HF], then the blocks' sums and all (m, l)
     __shared__ QueryCodes<D, NH> qc;
     __shared__ ChooseShared<kKeptWarps> sh;
     __shared__ uint32_t list[kKeptCandidates];
     __shared__ int32_t kept[kKeptPages];
     __shared__ __align__(8) float score_scale[8 * NH];
+    __shared__ int32_t range_lo[3], range_hi[3], range_groups[3];    // visible slots, and the groups they touch
     const Geo& g = p.geo;
     const int group = g.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, j = lane & 3;
+    if (p.log_ranks > 0) cluster_started();
     const int u = (int)(blockIdx.x >> p.log_ranks), ranks = 1 << p.log_ranks, rank = blockIdx.x & (ranks - 1);
     const int b = u / g.hkv, h = u - b * g.hkv, seq = p.seq[b], lp = 31 - __clz(g.page);
     const int64_t row = g.unit_row(seq, p.layer, h);
@@ -271,35 +277,14 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     const __nv_bfloat16* q0 = p.q + ((int64_t)b * g.hq + h * group) * D;
     int32_t* pages = p.pages && rank == 0 ? p.pages + (int64_t)u * p.cap : nullptr;
     const int n = p.n[b], nb = (n + g.page - 1) >> lp;
+    // candidates (more than p.top), this block's share of them, and its first ones'
+    // pages, looked up before the head's class is known
+    const int m = nb - p.first - p.newest;
+    const int per = ((m + ranks - 1) / ranks + kTilePages - 1) & ~(kTilePages - 1);
+    const int c0 = min(rank * per, m), c1 = min(c0 + per, m);
+    int32_t id[kTiles] = {};
+    if (nb > p.cap && p.top > 0) first_pages<kKeptWarps>(tab, p.first, c0, c1, id);
     const bool chosen = pol.kind == kGlobal && nb > p.cap;
-
-    if (chosen) {
-        for (int i = tid; i < p.first + p.newest; i += kKeptThreads) {
-            const int at = i < p.first ? i : i + p.top, pg = i < p.first ? i : nb - p.newest + (i - p.first);
-            kept[at] = tab[pg];
-            if (pages) pages[at] = pg;
-        }
-        if (p.top > 0) {
-            const int m = nb - p.first - p.newest;    // candidates, more than p.top
-            const int per = ((m + ranks - 1) / ranks + kTilePages - 1) & ~(kTilePages - 1);
-            const int c0 = min(rank * per, m), c1 = min(c0 + per, m);
-            score_pages<D, NH, kKeptWarps>(p, qc, tab, q0, c0, c1, [&](int c, uint32_t k) { list[c] = k; });
-            if (ranks > 1) {
-                cluster_sync();
-                for (int c = tid; c < m; c += kKeptThreads) {
-                    const int owner = c / per;
-                    if (owner != rank) list[c] = ld_peer(peer_smem(&list[c], owner));
-                }
-            }
-            __syncthreads();
-            choose_top(sh, m, p.top, [&](int c) { return list[c]; }, [&](int at, int c) {
-                kept[p.first + at] = tab[p.first + c];
-                if (pages) pages[p.first + at] = p.first + c;
-            });
-        }
-    } else if (pages) {
-        for (int i = tid; i < p.cap; i += kKeptThreads) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
-    }
 
     // The query as the products' operand.  bf16 pages: as it is.  Others: f16, times a
     // power of two per head that takes the largest |q * channel scale| to 2^14 .. 2^15
@@ -353,22 +338,47 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
         // (this lane's query is head gl, its scores are heads 2 j and 2 j + 1's)
         if (warp == 0 && j == 0) score_scale[head] = factor * unit_scale;
     }
-    __syncthreads();
 
-    // The unit's visible slots, in groups of 16; this warp's run [w0, w1) of them.
-    int32_t lo[3], ng[3], hi[3];
-    int total = 0;
-    {
+    if (warp == kKeptWarps - 1 && lane == 0) {
         const int64_t t = chosen ? kept_slots(n, g.page, p.cap) - 1 : n - 1;
         const SlotRanges rg = decode_ranges(pol, p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off, t, g.page);
         #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            lo[i] = (int32_t)rg.lo[i];
-            hi[i] = (int32_t)rg.hi[i];
-            ng[i] = hi[i] > lo[i] ? ((hi[i] - 1) >> 4) - (lo[i] >> 4) + 1 : 0;
-            total += ng[i];
+            range_lo[i] = (int32_t)rg.lo[i];
+            range_hi[i] = (int32_t)rg.hi[i];
+            range_groups[i] = rg.hi[i] > rg.lo[i] ? (int32_t)(((rg.hi[i] - 1) >> 4) - (rg.lo[i] >> 4) + 1) : 0;
         }
     }
+    if (chosen) {
+        for (int i = tid; i < p.first + p.newest; i += kKeptThreads) {
+            const int at = i < p.first ? i : i + p.top, pg = i < p.first ? i : nb - p.newest + (i - p.first);
+            kept[at] = tab[pg];
+            if (pages) pages[at] = pg;
+        }
+        if (p.top > 0) {
+            score_pages<D, NH, kKeptWarps>(p, qc, tab, q0, c0, c1, id, [&] { if (ranks > 1) cluster_wait(); },
+                                           [&](int c, uint32_t k, int half) {
+                                               if (ranks == 1) list[c] = k;      // (both halves the same)
+                                               else for (int r = half; r < ranks; r += 2) st_peer(peer_smem(&list[c], r), k);
+                                           });
+            if (ranks > 1) { cluster_arrive(); cluster_wait(); } else __syncthreads();
+            auto take = [&](int at, int c) {
+                kept[p.first + at] = tab[p.first + c];
+                if (pages) pages[p.first + at] = p.first + c;
+            };
+            auto key_at = [&](int c) { return list[c]; };
+            if (m <= 5 * kKeptThreads) choose_top<5, kKeptWarps>(sh, m, p.top, key_at, take);
+            else if (m <= 17 * kKeptThreads) choose_top<17, kKeptWarps>(sh, m, p.top, key_at, take);
+            else choose_top<33, kKeptWarps>(sh, m, p.top, key_at, take);
+        }
+    } else if (pages) {
+        for (int i = tid; i < p.cap; i += kKeptThreads) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
+    }
+
+    __syncthreads();
+
+    // The unit's visible slots are read in groups of 16; this warp's run [w0, w1) of them.
+    const int total = range_groups[0] + range_groups[1] + range_groups[2];
     const int runs = ranks * kKeptWarps, run = rank * kKeptWarps + warp;
     const int w0 = (int)((int64_t)total * run / runs), w1 = (int)((int64_t)total * (run + 1) / runs);
     // Lane i of a batch of 32: group w0 + batch + i's place in the pool (in groups)
@@ -380,17 +390,17 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
         place = seen = 0;
         #pragma unroll
         for (int r = 0; r < 3; ++r) {
-            if (at >= 0 && at < ng[r]) {
-                const int32_t slot = ((lo[r] >> 4) + at) << 4, pg = slot >> lp;
+            if (at >= 0 && at < range_groups[r]) {
+                const int32_t lo = range_lo[r], slot = ((lo >> 4) + at) << 4, pg = slot >> lp;
                 const int32_t page = chosen ? kept[pg] : tab[pg];
                 if (page < 0 || page >= g.num_pages) {
                     atomicOr(p.meta.status, kStatusBadPage);
                 } else {
                     place = (((uint32_t)page << lp) + (uint32_t)(slot & (g.page - 1))) >> 4;
-                    seen = (uint32_t)max(lo[r] - slot, 0) | ((uint32_t)min(hi[r] - slot, 16) << 8);
+                    seen = (uint32_t)max(lo - slot, 0) | ((uint32_t)min(range_hi[r] - slot, 16) << 8);
                 }
             }
-            at -= ng[r];
+            at -= range_groups[r];
         }
     };
     R rows;
@@ -529,10 +539,11 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     }
 
     // ------------------------------- merge -------------------------------
+    // A head's sums lie in the tiles' order: dimension v_dim(t, i, gl) at 16 t + 2 gl + i.
     float* mine_o = parts + warp * group * HF;
-    float* block_o = parts + kKeptWarps * group * HF;               // [group][D]
-    float2* warp_ml = reinterpret_cast<float2*>(block_o + group * D);   // [warps][group]
-    float2* block_ml = warp_ml + kKeptWarps * group;                // [group]
+    float* sums = parts + kKeptWarps * group * HF;                  // [ranks][group * D / ranks]
+    float2* warp_ml = reinterpret_cast<float2*>(sums + group * D);  // [warps][group]
+    float2* rank_ml = warp_ml + kKeptWarps * group;                 // [ranks][group]
     const float* vscale = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
     #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
@@ -546,67 +557,92 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
             if (head >= group) continue;
             #pragma unroll
             for (int t = 0; t < MT; ++t)
-                *reinterpret_cast<float2*>(mine_o + head * HF + R::v_dim(t, 0, gl)) =
-                    make_float2(o[nh][t][e], o[nh][t][2 + e]);
+                *reinterpret_cast<float2*>(mine_o + head * HF + 16 * t + 2 * gl) = make_float2(o[nh][t][e], o[nh][t][2 + e]);
             if (gl == 0) warp_ml[warp * group + head] = make_float2(m_run[nh][e], l);
         }
+    if (ranks > 1 && !(chosen && p.top > 0)) cluster_wait();         // every block runs
     __syncthreads();
     __nv_bfloat16* out = p.out + ((int64_t)b * g.hq + h * group) * D;
     float* lse = p.lse ? p.lse + (int64_t)b * g.hq + h * group : nullptr;
     // a unit without a visible token: O = 0, LSE = -inf
-    auto finish = [&](int r, int c, float acc, float m, float l) {
+    auto finish = [&](int r, int at, float acc, float m, float l) {
+        const int c = R::v_dim(at >> 4, at & 1, (at >> 1) & 7);
         if (KV != kRowsBf16 && p.scaled) acc *= __ldg(vscale + c);
         out[r * D + c] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-        if (c == 0 && lse) lse[r] = (m + __log2f(l)) * 0.69314718055994531f;
+        if (at == 0 && lse) lse[r] = (m + __log2f(l)) * 0.69314718055994531f;
     };
+    const int part = (group * D) >> p.log_ranks;                    // outputs that a block finishes
     for (int e = tid; e < group * D; e += kKeptThreads) {
-        const int r = e / D, c = e % D;
+        const int r = e / D, at = e % D;
         float m = -INFINITY, l = 0.f, acc = 0.f;
+        float2 ml[kKeptWarps];
         #pragma unroll
-        for (int w = 0; w < kKeptWarps; ++w) m = fmaxf(m, warp_ml[w * group + r].x);
+        for (int w = 0; w < kKeptWarps; ++w) {
+            ml[w] = warp_ml[w * group + r];
+            m = fmaxf(m, ml[w].x);
+        }
         const float ref = m == -INFINITY ? 0.f : m;
         #pragma unroll
         for (int w = 0; w < kKeptWarps; ++w) {
-            const float2 ml = warp_ml[w * group + r];
-            const float f = fast_exp2(ml.x - ref);
-            l += f * ml.y;
-            acc += f * parts[(w * group + r) * HF + c];
+            const float f = fast_exp2(ml[w].x - ref);
+            l += f * ml[w].y;
+            acc += f * parts[(w * group + r) * HF + at];
         }
         if (ranks == 1) {
-            finish(r, c, acc, m, l);
+            finish(r, at, acc, m, l);
         } else {
-            block_o[e] = acc;
-            if (c == 0) block_ml[r] = make_float2(m, l);
+            const int owner = e / part;
+            st_peer(peer_smem(&sums[rank * part + (e - owner * part)], owner), __float_as_uint(acc));
+            if (at < ranks) {                                       // (D >= ranks) lanes share the blocks to tell
+                const uint32_t to = peer_smem(&rank_ml[rank * group + r], at);
+                st_peer(to, __float_as_uint(m));
+                st_peer(to + 4, __float_as_uint(l));
+            }
         }
     }
     if (ranks == 1) return;
-    cluster_sync();
-    for (int e = rank * kKeptThreads + tid; e < group * D; e += ranks * kKeptThreads) {
-        const int r = e / D, c = e % D;
-        float m = -INFINITY, l = 0.f, acc = 0.f;
-        for (int i = 0; i < ranks; ++i) m = fmaxf(m, __uint_as_float(ld_peer(peer_smem(&block_ml[r].x, i))));
-        const float ref = m == -INFINITY ? 0.f : m;
-        for (int i = 0; i < ranks; ++i) {
-            const float f = fast_exp2(__uint_as_float(ld_peer(peer_smem(&block_ml[r].x, i))) - ref);
-            l += f * __uint_as_float(ld_peer(peer_smem(&block_ml[r].y, i)));
-            acc += f * __uint_as_float(ld_peer(peer_smem(&block_o[e], i)));
+    cluster_arrive();
+    cluster_wait();
+    auto join = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        for (int e = tid; e < part; e += kKeptThreads) {
+            const int r = (rank * part + e) / D, at = (rank * part + e) % D;
+            float2 ml[N];
+            float x[N], m = -INFINITY, l = 0.f, acc = 0.f;
+            #pragma unroll
+            for (int i = 0; i < N; ++i) {
+                ml[i] = rank_ml[i * group + r];
+                x[i] = sums[i * part + e];
+            }
+            #pragma unroll
+            for (int i = 0; i < N; ++i) m = fmaxf(m, ml[i].x);
+            const float ref = m == -INFINITY ? 0.f : m;
+            #pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float f = fast_exp2(ml[i].x - ref);
+                l += f * ml[i].y;
+                acc += f * x[i];
+            }
+            finish(r, at, acc, m, l);
         }
-        finish(r, c, acc, m, l);
-    }
-    cluster_sync();                                   // no block leaves while another reads its parts
+    };
+    if (ranks == 2) join(Count<2>());
+    else if (ranks == 4) join(Count<4>());
+    else if (ranks == 8) join(Count<8>());
+    else join(Count<16>());
 }
 
 template <int KV, int D, int NH, bool CAP>
 cudaError_t launch_kept_t(const KeptParams& p, cudaStream_t s) {
     const int group = p.geo.group;
-    const int smem = (kKeptWarps * group * (D + 4) + group * D + 2 * (kKeptWarps + 1) * group) * 4;
+    const int smem = (kKeptWarps * group * (D + 8) + group * D + 2 * (kKeptWarps + 16) * group) * 4;
     auto kernel = k_kept<KV, D, NH, CAP>;
     static std::atomic<uint64_t> ready{0};            // devices on which the attributes are set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        constexpr int kMost = (kKeptWarps * 8 * NH * (D + 4) + 8 * NH * D + 2 * (kKeptWarps + 1) * 8 * NH) * 4;
+        constexpr int kMost = (kKeptWarps * 8 * NH * (D + 8) + 8 * NH * D + 2 * (kKeptWarps + 16) * 8 * NH) * 4;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
