@@ -217,31 +217,36 @@ def sp_rope_axes(q: Optional[torch.Tensor], k: Optional[torch.Tensor], axis_pos:
     (int64): pair i turns by the position on axis axis_of[i].  Returns (q_out, k_out)."""
     first = k if q is None else q
     rows, _, d = first.shape
-    index = first.get_device()
+    index, device = first.get_device(), first.device
+    axes, given = axis_pos.shape
+    per_axis, per_row = axis_pos.stride()
     assert len(axis_of) == d // 2 and (inv_freq is None or len(inv_freq) == d // 2)
-    assert axis_pos.dtype is torch.int64 and axis_pos.get_device() == index and axis_pos.dim() == 2 and \
-        axis_pos.shape[1] >= rows, "axis_pos: int64 [axes, rows] on the device of q and k"
+    assert axis_pos.dtype is torch.int64 and axis_pos.get_device() == index and given >= rows, \
+        "axis_pos: int64 [axes, rows] on the device of q and k"
+    args = []                                        # (address, row stride, heads) of q and of k
     outs = []
     for x, out in ((q, q_out), (k, k_out)):
         if x is None:
+            args += (0, 0, 0)
             outs.append(None)
             continue
-        _, per_head, per_element = x.stride()
-        assert x.dtype is torch.bfloat16 and x.get_device() == index and x.shape[0] == rows and x.shape[2] == d and \
-            (x.shape[1] == 1 or per_head == d) and per_element == 1, \
+        shape = x.shape
+        n, heads, dim = shape
+        stride, per_head, per_element = x.stride()
+        assert x.dtype is torch.bfloat16 and x.get_device() == index and n == rows and dim == d and \
+            (heads == 1 or per_head == d) and per_element == 1, \
             "q, k: bf16 [rows, heads, head_dim] on one device, heads contiguous"
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         else:
-            assert out.is_contiguous() and out.shape == x.shape and out.dtype is x.dtype and \
+            assert out.is_contiguous() and out.shape == shape and out.dtype is x.dtype and \
                 out.get_device() == index, "outputs: contiguous, of their input's shape, type and device"
+        args += (x.data_ptr(), stride if n > 1 else heads * d, heads)
         outs.append(out)
     of = i32_buffer(axis_of)
     check(load().sp_rope_axes(
-        _ptr(q), 0 if q is None else _row_stride(q), 0 if q is None else q.shape[1],
-        _ptr(k), 0 if k is None else _row_stride(k), 0 if k is None else k.shape[1], d, rows,
-        _ptr(axis_pos), axis_pos.stride(0), axis_pos.stride(1), axis_pos.shape[0], of.buffer_info()[0],
-        float(rope_theta), _frequencies(inv_freq), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)))
+        *args, d, rows, axis_pos.data_ptr(), per_axis, per_row, axes, of.buffer_info()[0], rope_theta,
+        _frequencies(inv_freq), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)))
     return tuple(outs)
 
 
@@ -607,19 +612,20 @@ class SegPagedCache:
         Returns (out, lse, pages): pages [sequences, kv_heads, sink + recent + top]
         int32, the kept pages in ascending order, -1 behind them."""
         c = self.cfg
+        n, heads, d = q.shape
         assert q.dtype is torch.bfloat16 and q.is_contiguous() and q.get_device() == self._index and \
-            tuple(q.shape) == (len(seq_ids), c.num_q_heads, c.head_dim), \
+            n == len(seq_ids) and heads == c.num_q_heads and d == c.head_dim, \
             "q: bf16 [sequences, heads, head_dim], contiguous, on the cache's device"
+        shape = (n, c.num_kv_heads, max(0, top_pages + sink_pages + recent_pages))
+        for x, s, t in ((out, (n, heads, d), torch.bfloat16), (lse, (n, heads), torch.float32), (pages, shape, torch.int32)):
+            assert x is None or (x.is_contiguous() and x.shape == s and x.dtype is t and
+                                 x.get_device() == self._index), "out, lse, pages: contiguous, on the cache's device"
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
-        shape = (q.shape[0], c.num_kv_heads, max(0, top_pages + sink_pages + recent_pages))
+            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
         if pages is None and want_pages:
             pages = torch.empty(shape, dtype=torch.int32, device=q.device)
-        for x, s, t in ((out, q.shape, torch.bfloat16), (lse, q.shape[:2], torch.float32), (pages, shape, torch.int32)):
-            assert x is None or (x.is_contiguous() and x.shape == s and x.dtype is t and
-                                 x.get_device() == self._index), "out, lse, pages: contiguous, on the cache's device"
         if score_cap is not None and not score_cap > 0:
             raise ValueError("score_cap must be positive")
         sp_attention_decode_select(self.handle, layer, seq_ids, q, top_pages, sink_pages, recent_pages, out, lse, pages,

@@ -180,7 +180,6 @@ k_write_rope(const __grid_constant__ PR p) {
     // angles, [token][pair of a chunk][chunk]: lanes read neighbouring chunks
     __shared__ float4 cs[kMaxTok * 32];
     __shared__ int32_t tok_b[kMaxTok], tok_t[kMaxTok], tok_n[kMaxTok];
-    __shared__ int64_t tok_p[AXES ? kMaxTok * kMaxAxes : 1];             // [token][axis]
     const int D = g.d, half = D / 2;
     const int r0 = (int)blockIdx.x * p.tok, nt = min(p.tok, p.rows - r0);
     // queries: two chunk pairs a pass (four 16-byte loads in flight a thread),
@@ -204,11 +203,12 @@ k_write_rope(const __grid_constant__ PR p) {
         }
     };
     fetch(first);
-    if constexpr (AXES) {
-        const int t = tid / kMaxAxes - 8, a = tid % kMaxAxes;            // (warp 0 looks up the sequences)
-        if (t >= 0 && t < nt && a < p.axes.n)
-            tok_p[t * kMaxAxes + a] = __ldg(p.axes.pos + a * p.axes.axis_stride + (int64_t)(r0 + t) * p.axes.row_stride);
-    }
+    // a thread takes one angle at most; its position travels while the tokens are looked up
+    static_assert(kMaxTok * 64 <= kWriteThreads, "an angle a thread");
+    uint64_t at = 0;
+    if (AXES && tid < nt * half)
+        at = (uint64_t)__ldg(p.axes.pos + p.axes.of[tid % half] * p.axes.axis_stride +
+                             (int64_t)(r0 + tid / half) * p.axes.row_stride);
     if (tid < nt) {
         int a = 0, z = p.n_seqs - 1;                     // sequence with row0[b] <= row < row0[b + 1]
         while (a < z) {
@@ -227,9 +227,9 @@ k_write_rope(const __grid_constant__ PR p) {
         }
     }
     __syncthreads();
-    for (int e = tid; e < nt * half; e += kWriteThreads) {
-        const int t = e / half, f = e % half;
-        const uint64_t at = AXES ? (uint64_t)tok_p[t * kMaxAxes + p.axes.of[f]] : (uint64_t)(uint32_t)tok_t[t];
+    if (tid < nt * half) {
+        const int t = tid / half, f = tid % half;
+        if (!AXES) at = (uint32_t)tok_t[t];
         reinterpret_cast<float2*>(cs + (t * 4 + ((f & 7) >> 1)) * nc + (f >> 3))[f & 1] = cos_sin(at * p.turn[f]);
     }
     __syncthreads();
