@@ -19,8 +19,8 @@ LIB = os.path.join(BUILD, "libsegpaged.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["sp_api.cu", "sp_storage.cu", "sp_decode.cu", "sp_prefill.cu", "sp_decode_static.cu",
            "sp_decode_capped.cu", "sp_decode4.cu", "sp_decode4_capped.cu", "sp_prefill_capped.cu", "sp_prefill_rows.cu",
-           "sp_dequant.cu", "sp_write.cu", "sp_rope_axes.cu", "sp_bounds.cu", "sp_choose.cu", "sp_kept.cu", "sp_kept_capped.cu", "sp_rope.cu",
-           "sp_transfer.cu", "sp_select.cu", "sp_selftest.cu"]
+           "sp_dequant.cu", "sp_write.cu", "sp_rope_axes.cu", "sp_bounds.cu", "sp_choose.cu", "sp_kept.cu", "sp_kept_capped.cu",
+           "sp_kept_coded.cu", "sp_kept_coded_capped.cu", "sp_rope.cu", "sp_transfer.cu", "sp_select.cu", "sp_selftest.cu"]
 
 
 def nvcc() -> str:

@@ -26,7 +26,7 @@
 // FP8 and 4-bit pages: f16, 2^-12), the query under channel scales to f16.
 #pragma once
 #include <algorithm>
-#include <atomic>
+#include <mutex>
 
 #include "sp_choose.cuh"
 #include "sp_decode4.cuh"
@@ -35,9 +35,9 @@ namespace sp {
 
 namespace {
 
-constexpr int kKeptWarps = 4;
-constexpr int kKeptThreads = kKeptWarps * 32;
-static_assert(kKeptCandidates <= 33 * kKeptThreads, "a block's registers hold the keys");
+static_assert(kKeptCandidates <= 33 * 128 && kKeptCandidates <= 17 * 256, "a block's registers hold the keys");
+
+constexpr int kMaxKeptDevices = 64;
 
 enum { kRowsBf16, kRowsFp8, kRowsFp4 };
 
@@ -254,14 +254,16 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// One block of 128 threads a cluster rank.  Registers: three blocks an SM at NH = 1.
-template <int KV, int D, int NH, bool CAP>
-__global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __grid_constant__ KeptParams p) {
+// A block of W warps a cluster rank.  Registers: three blocks of 4 warps an SM at
+// NH = 1 (two at NH = 2), or one of 8, for few units.
+template <int KV, int D, int NH, int W, bool CAP>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(const __grid_constant__ KeptParams p) {
     using R = Rows<KV, D>;
+    constexpr int T = W * 32;
     constexpr int NG = R::NG, MT = D / 16, KS = D / 16, HF = D + 8;   // groups a step, tiles, steps, a head's floats
     extern __shared__ __align__(16) float parts[];    // [warps][group][HF], then the blocks' sums and all (m, l)
     __shared__ QueryCodes<D, NH> qc;
-    __shared__ ChooseShared<kKeptWarps> sh;
+    __shared__ ChooseShared<W> sh;
     __shared__ uint32_t list[kKeptCandidates];
     __shared__ int32_t kept[kKeptPages];
     __shared__ __align__(8) float score_scale[8 * NH];
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     const int per = ((m + ranks - 1) / ranks + kTilePages - 1) & ~(kTilePages - 1);
     const int c0 = min(rank * per, m), c1 = min(c0 + per, m);
     int32_t id[kTiles] = {};
-    if (nb > p.cap && p.top > 0) first_pages<kKeptWarps>(tab, p.first, c0, c1, id);
+    if (nb > p.cap && p.top > 0) first_pages<W>(tab, p.first, c0, c1, id);
     const bool chosen = pol.kind == kGlobal && nb > p.cap;
 
     // The query as the products' operand.  bf16 pages: as it is.  Others: f16, times a
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
         if (warp == 0 && j == 0) score_scale[head] = factor * unit_scale;
     }
 
-    if (warp == kKeptWarps - 1 && lane == 0) {
+    if (warp == W - 1 && lane == 0) {
         const int64_t t = chosen ? kept_slots(n, g.page, p.cap) - 1 : n - 1;
         const SlotRanges rg = decode_ranges(pol, p.meta.idx + (int64_t)seq * g.max_idx_per_seq + pol.idx_off, t, g.page);
         #pragma unroll
@@ -350,13 +352,13 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
         }
     }
     if (chosen) {
-        for (int i = tid; i < p.first + p.newest; i += kKeptThreads) {
+        for (int i = tid; i < p.first + p.newest; i += T) {
             const int at = i < p.first ? i : i + p.top, pg = i < p.first ? i : nb - p.newest + (i - p.first);
             kept[at] = tab[pg];
             if (pages) pages[at] = pg;
         }
         if (p.top > 0) {
-            score_pages<D, NH, kKeptWarps>(p, qc, tab, q0, c0, c1, id, [&] { if (ranks > 1) cluster_wait(); },
+            score_pages<D, NH, W>(p, qc, tab, q0, c0, c1, id, [&] { if (ranks > 1) cluster_wait(); },
                                            [&](int c, uint32_t k, int half) {
                                                if (ranks == 1) list[c] = k;      // (both halves the same)
                                                else for (int r = half; r < ranks; r += 2) st_peer(peer_smem(&list[c], r), k);
@@ -367,19 +369,19 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
                 if (pages) pages[p.first + at] = p.first + c;
             };
             auto key_at = [&](int c) { return list[c]; };
-            if (m <= 5 * kKeptThreads) choose_top<5, kKeptWarps>(sh, m, p.top, key_at, take);
-            else if (m <= 17 * kKeptThreads) choose_top<17, kKeptWarps>(sh, m, p.top, key_at, take);
-            else choose_top<33, kKeptWarps>(sh, m, p.top, key_at, take);
+            if (m <= 5 * T) choose_top<5, W>(sh, m, p.top, key_at, take);
+            else if (m <= 17 * T) choose_top<17, W>(sh, m, p.top, key_at, take);
+            else if constexpr (W == 4) choose_top<33, W>(sh, m, p.top, key_at, take);
         }
     } else if (pages) {
-        for (int i = tid; i < p.cap; i += kKeptThreads) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
+        for (int i = tid; i < p.cap; i += T) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
     }
 
     __syncthreads();
 
     // The unit's visible slots are read in groups of 16; this warp's run [w0, w1) of them.
     const int total = range_groups[0] + range_groups[1] + range_groups[2];
-    const int runs = ranks * kKeptWarps, run = rank * kKeptWarps + warp;
+    const int runs = ranks * W, run = rank * W + warp;
     const int w0 = (int)((int64_t)total * run / runs), w1 = (int)((int64_t)total * (run + 1) / runs);
     // Lane i of a batch of 32: group w0 + batch + i's place in the pool (in groups)
     // and its visible slots, low | high << 8 (0: none).
@@ -541,9 +543,9 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     // ------------------------------- merge -------------------------------
     // A head's sums lie in the tiles' order: dimension v_dim(t, i, gl) at 16 t + 2 gl + i.
     float* mine_o = parts + warp * group * HF;
-    float* sums = parts + kKeptWarps * group * HF;                  // [ranks][group * D / ranks]
+    float* sums = parts + W * group * HF;                  // [ranks][group * D / ranks]
     float2* warp_ml = reinterpret_cast<float2*>(sums + group * D);  // [warps][group]
-    float2* rank_ml = warp_ml + kKeptWarps * group;                 // [ranks][group]
+    float2* rank_ml = warp_ml + W * group;                 // [ranks][group]
     const float* vscale = p.meta.vscale + ((int64_t)p.layer * g.hkv + h) * D;
     #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
@@ -572,18 +574,18 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
         if (at == 0 && lse) lse[r] = (m + __log2f(l)) * 0.69314718055994531f;
     };
     const int part = (group * D) >> p.log_ranks;                    // outputs that a block finishes
-    for (int e = tid; e < group * D; e += kKeptThreads) {
+    for (int e = tid; e < group * D; e += T) {
         const int r = e / D, at = e % D;
         float m = -INFINITY, l = 0.f, acc = 0.f;
-        float2 ml[kKeptWarps];
+        float2 ml[W];
         #pragma unroll
-        for (int w = 0; w < kKeptWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             ml[w] = warp_ml[w * group + r];
             m = fmaxf(m, ml[w].x);
         }
         const float ref = m == -INFINITY ? 0.f : m;
         #pragma unroll
-        for (int w = 0; w < kKeptWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = fast_exp2(ml[w].x - ref);
             l += f * ml[w].y;
             acc += f * parts[(w * group + r) * HF + at];
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     cluster_wait();
     auto join = [&](auto count) {
         constexpr int N = decltype(count)::value;
-        for (int e = tid; e < part; e += kKeptThreads) {
+        for (int e = tid; e < part; e += T) {
             const int r = (rank * part + e) / D, at = (rank * part + e) % D;
             float2 ml[N];
             float x[N], m = -INFINITY, l = 0.f, acc = 0.f;
@@ -632,44 +634,119 @@ __global__ void __launch_bounds__(kKeptThreads, NH == 1 ? 3 : 2) k_kept(const __
     else join(Count<16>());
 }
 
-template <int KV, int D, int NH, bool CAP>
-cudaError_t launch_kept_t(const KeptParams& p, cudaStream_t s) {
-    const int group = p.geo.group;
-    const int smem = (kKeptWarps * group * (D + 8) + group * D + 2 * (kKeptWarps + 16) * group) * 4;
-    auto kernel = k_kept<KV, D, NH, CAP>;
-    static std::atomic<uint64_t> ready{0};            // devices on which the attributes are set
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        constexpr int kMost = (kKeptWarps * 8 * NH * (D + 8) + 8 * NH * D + 2 * (kKeptWarps + 16) * 8 * NH) * 4;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+// An instance's launches, on the current device.
+template <int KV, int D, int NH, int W, bool CAP>
+struct KeptLaunch {
+    static int bytes(int heads) { return (W * heads * (D + 8) + heads * D + 2 * (W + 16) * heads) * 4; }
+    static void fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& at, int units, int log_ranks, int heads, cudaStream_t s) {
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 1u << log_ranks;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)units << log_ranks);
+        cfg.blockDim = dim3(W * 32);
+        cfg.dynamicSmemBytes = (size_t)bytes(heads);
+        cfg.stream = s;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
     }
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 1u << p.log_ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.n_seqs * p.geo.hkv) << p.log_ranks);
-    cfg.blockDim = dim3(kKeptThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    // Units of 1 << log_ranks blocks that run at once; asked for once per device.
+    struct Fit { bool known; int units[5]; };
+    static cudaError_t fit(Fit& f) {
+        static std::mutex mu;
+        static Fit of[kMaxKeptDevices];
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= kMaxKeptDevices) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!of[dev].known) {
+            auto kernel = k_kept<KV, D, NH, W, CAP>;
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(8 * NH));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            for (int r = 0; r < 5 && e == cudaSuccess; ++r) {
+                cudaLaunchConfig_t cfg{};
+                cudaLaunchAttribute at{};
+                fill(cfg, at, 1, r, 8 * NH, 0);
+                e = cudaOccupancyMaxActiveClusters(&of[dev].units[r], kernel, &cfg);
+            }
+            if (e != cudaSuccess) return e;
+            of[dev].known = true;
+        }
+        f = of[dev];
+        return cudaSuccess;
+    }
+    static cudaError_t run(KeptParams& p, int log_ranks, cudaStream_t s) {
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at{};
+        p.log_ranks = log_ranks;
+        fill(cfg, at, p.n_seqs * p.geo.hkv, log_ranks, p.geo.group, s);
+        return cudaLaunchKernelEx(&cfg, k_kept<KV, D, NH, W, CAP>, static_cast<const KeptParams&>(p));
+    }
+};
+
+// Microseconds until the last of the units ends, of which `at_once` run side by side
+// and the others in turn: a start and a merge, a choice where there is one, and the
+// steps of a unit's warps (measured: 6.5, 4 and 1.1 us).
+inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
+    float busy[kKeptLoads] = {};
+    const int n = at_once < kKeptLoads ? at_once : kKeptLoads;
+    float end = 0.f;
+    for (int u = 0; u < load.n; ++u) {
+        int first = 0;
+        for (int i = 1; i < n; ++i) first = busy[i] < busy[first] ? i : first;
+        const int steps = (load.groups[u] + groups_a_step - 1) / groups_a_step;
+        busy[first] += 6.5f + (load.chosen[u] ? 4.f : 0.f) + 1.1f * (float)steps;
+        end = std::max(end, busy[first]);
+    }
+    return end;
+}
+
+// Warps a block and blocks a unit: the most warps a unit with which all units still
+// run at once (three blocks of 4 warps an SM, or one of 8; clusters cannot use all SMs
+// of a group).  45 units of 64 pages, FP8, 4 warps: 8 blocks each 16.3 us, 4 each
+// 20.5, 16 each (more than run at once) 30.7; 128 units, 4-bit: 2 each 25.2, 4 each 40;
+// 32 units: 8 warps in 4 blocks each 15.3, 4 warps in 8 each 16.5.  A few units may
+// differ much (one sequence's GLOBAL heads and its LOCAL ones): then the largest
+// clusters can end first although some units wait (1 x 128K, two of eight heads
+// GLOBAL: 17.5 us against 22.3; 1 x 4K, all GLOBAL: 18 against 10).
+template <int KV, int D, int NH, bool CAP>
+cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+    typedef KeptLaunch<KV, D, NH, 8, CAP> Eight;
+    typedef KeptLaunch<KV, D, NH, 4, CAP> Four;
+    typename Eight::Fit eight;
+    typename Four::Fit four;
+    cudaError_t e = Eight::fit(eight);
+    if (e == cudaSuccess) e = Four::fit(four);
+    if (e != cudaSuccess) return e;
+    const int units = p.n_seqs * p.geo.hkv;
+    constexpr int NG = Rows<KV, D>::NG;
+    if (units <= eight.units[4]) return Eight::run(p, 4, s);
+    if (units <= eight.units[3]) {
+        const bool largest = load.n == units && eight.units[4] > 0 &&
+                             kept_span(load, eight.units[4], 128 * NG) < kept_span(load, eight.units[3], 64 * NG);
+        return Eight::run(p, largest ? 4 : 3, s);
+    }
+    if (units <= four.units[4]) return Four::run(p, 4, s);
+    if (units <= eight.units[2]) return Eight::run(p, 2, s);
+    for (int r = 3; r > 0; --r)
+        if (units <= four.units[r]) return Four::run(p, r, s);
+    return Four::run(p, 0, s);
+}
+
+template <int KV, int D, bool CAP>
+cudaError_t launch_kept_type(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+    return p.geo.group > 8 ? launch_kept_heads<KV, D, 2, CAP>(p, load, s) : launch_kept_heads<KV, D, 1, CAP>(p, load, s);
 }
 
 template <bool CAP>
-cudaError_t launch_kept_any(const KeptParams& p, cudaStream_t s) {
-    const bool wide = p.geo.group > 8;
-    if (p.geo.fp4) return wide ? launch_kept_t<kRowsFp4, 128, 2, CAP>(p, s) : launch_kept_t<kRowsFp4, 128, 1, CAP>(p, s);
-    if (p.geo.fp8) return wide ? launch_kept_t<kRowsFp8, 128, 2, CAP>(p, s) : launch_kept_t<kRowsFp8, 128, 1, CAP>(p, s);
-    if (p.geo.d == 128)
-        return wide ? launch_kept_t<kRowsBf16, 128, 2, CAP>(p, s) : launch_kept_t<kRowsBf16, 128, 1, CAP>(p, s);
-    return wide ? launch_kept_t<kRowsBf16, 64, 2, CAP>(p, s) : launch_kept_t<kRowsBf16, 64, 1, CAP>(p, s);
+cudaError_t launch_kept_bf16(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+    return p.geo.d == 128 ? launch_kept_type<kRowsBf16, 128, CAP>(p, load, s)
+                          : launch_kept_type<kRowsBf16, 64, CAP>(p, load, s);
+}
+template <bool CAP>
+cudaError_t launch_kept_coded(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+    return p.geo.fp4 ? launch_kept_type<kRowsFp4, 128, CAP>(p, load, s)
+                     : launch_kept_type<kRowsFp8, 128, CAP>(p, load, s);
 }
 
 }  // namespace

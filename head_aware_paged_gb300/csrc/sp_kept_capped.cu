@@ -1,9 +1,11 @@
-// sp_kept_capped.cu -- the instances of k_kept (sp_kept.cuh) for scores capped by a
-// tanh.
+// sp_kept_capped.cu -- the instances of k_kept (sp_kept.cuh) for bf16 pages and scores capped
+// by a tanh.
 #include "sp_kept.cuh"
 
 namespace sp {
 
-cudaError_t launch_kept_capped(const KeptParams& p, cudaStream_t s) { return launch_kept_any<true>(p, s); }
+cudaError_t launch_kept_bf16_capped(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+    return launch_kept_bf16<true>(p, load, s);
+}
 
 }  // namespace sp

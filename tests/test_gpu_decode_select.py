@@ -237,6 +237,29 @@ def test_long_unit_and_its_neighbours():
     assert c.status() == 0
 
 
+@pytest.mark.parametrize("kv,d,hq,hkv,cap", [("bf16", 64, 3, 1, None), ("bf16", 128, 12, 1, 30.0), ("fp8", 128, 4, 2, None),
+                                            ("fp8", 128, 16, 1, 30.0), ("fp4", 128, 8, 1, 30.0), ("fp4", 128, 24, 2, None)])
+def test_many_pages_kept(kv, d, hq, hkv, cap):
+    """More pages kept than a cluster's list holds: the choice in a launch of its own,
+    next to a sequence that keeps everything and LOCAL heads."""
+    gpu_ready()
+    P, lens = 16, [35000, 900, 1]
+    pols = [W.HeadPolicy(G), W.HeadPolicy(L, 4, 60)][:hkv]
+    c = _mk(hq, hkv, d, P, 3, 36000, pages=hkv * 2400, kv=kv)
+    scales = None
+    if kv != "bf16":
+        scales = np.exp2(np.random.default_rng(3).integers(-3, 3, (2, hkv, d))).astype(np.float32)
+        c.set_kv_scales(0, scales[0], scales[1])
+    for s, n in enumerate(lens):
+        c.set_policy(s, to_c_policies([pols]))
+        c.build(s, 0, _keys(n, hkv, d, 10 * s), W.normal((n, hkv, d), 10 * s + 5, device="cuda"))
+    q = W.normal((3, hq, d), 99, device="cuda")
+    _check_select(c, [1, 0, 2], pols, q, 2060, 1, 2, cap=cap, scales=scales)
+    again = c.decode_select(0, [1, 0, 2], q, 2060, 1, 2, score_cap=cap)
+    few = c.decode_select(0, [0], q[1:2].contiguous(), 2060, 1, 2, score_cap=cap)
+    assert torch.equal(again[2][1], few[2][0])
+
+
 @pytest.mark.parametrize("kv,d,P,hq,hkv", [("bf16", 64, 16, 4, 2), ("bf16", 128, 64, 9, 3), ("fp8", 128, 32, 9, 3),
                                            ("fp4", 128, 16, 9, 3)])
 def test_bounds_follow_every_write(kv, d, P, hq, hkv):
@@ -474,10 +497,10 @@ def test_a_serving_run():
     v = x[:, hq + hkv:].contiguous()
     out, lse = c.prefill(0, [0], [0, n], q, k, v)
     rows = [0, 63, 499]
-    ref = attend(q[rows].double(), k.double(), v.double(), rows, [(G, 0, 0, None), (L, 4, 60, None)])
-    check(out[rows], lse[rows], ref, 2.0 ** -8, 0.0, "prefill")
+    ref = attend(q[rows].double().cpu(), k.double().cpu(), v.double().cpu(), rows, [(G, 0, 0, None), (L, 4, 60, None)])
+    check(out[rows].cpu(), lse[rows].cpu(), ref, 2.0 ** -8, 0.0, "prefill")
     c.append_kv(0, [0], [0, n], k, v)
-    for t in range(n, n + 20):
+    for t in range(n, n + 17):
         y = W.normal((1, hq + 2 * hkv, d), t, device="cuda")
         at = torch.full((3, 1), 10 + t - n, device="cuda")
         qr = c.append_kv_rope_axes(0, [0], [0, 1], y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:], at, of)
