@@ -687,22 +687,24 @@ static sp_status decode_kept(sp_cache* c, int32_t layer, const int32_t* seq_ids,
     p.top = choice.top;
     p.cap = choice.first + choice.newest + choice.top;
     KeptLoad load;
+    load.total = load.longest = 0;
     load.n = n_seqs * H <= kKeptLoads ? n_seqs * H : 0;
     for (int b = 0; b < n_seqs; ++b) {
         const int64_t n = c->h_seqlen[(size_t)seq_ids[b] * c->cfg.num_layers + layer];
         if (n < 1) return fail(SP_ERR_INVALID_ARG, "decode needs the query's own token appended first");
         p.seq[b] = seq_ids[b];
         p.n[b] = (int32_t)n;
-        const int64_t nb = cdiv64(n, P);
+        const int64_t nb = cdiv64(n, P), kept = kept_slots(n, P, p.cap);
         const bool fits = nb <= p.cap || (p.cap <= kKeptPages && nb - choice.first - choice.newest <= kKeptCandidates);
-        if (fits && load.n == 0) continue;
         for (int h = 0; h < H; ++h) {
             const UnitPol& u = c->h_pol[unit_index(c, seq_ids[b], layer, h)];
             const bool global = u.kind == kGlobal;
             if (global && !fits) return SP_OK;
+            const int64_t groups = cdiv64(global ? kept : visible_count(u, host_idx(c, seq_ids[b], u), n - 1), 16);
+            load.total += groups;
+            load.longest = std::max(load.longest, groups);
             if (load.n == 0) continue;
-            const int64_t t = (global ? kept_slots(n, P, p.cap) : n) - 1;
-            load.groups[b * H + h] = (int32_t)decode_items(decode_ranges(u, host_idx(c, seq_ids[b], u), t, P), 16);
+            load.groups[b * H + h] = (int32_t)groups;
             load.chosen[b * H + h] = global && nb > p.cap;
         }
     }
@@ -722,10 +724,9 @@ static sp_status decode_kept(sp_cache* c, int32_t layer, const int32_t* seq_ids,
     p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->cfg.head_dim));
     p.score_cap = score_cap != 0.f ? make_cap(score_cap, c->cfg.head_dim) : Cap{};
     launch_mark_start(c, static_cast<cudaStream_t>(stream));
-    const cudaError_t e = launch_kept(p, load, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_kept(p, load, done, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-    launch_mark_end(c, static_cast<cudaStream_t>(stream));
-    done = true;
+    if (done) launch_mark_end(c, static_cast<cudaStream_t>(stream));
     return SP_OK;
 }
 

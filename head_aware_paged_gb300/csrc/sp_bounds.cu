@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kBoundThreads) k_bounds(const __grid_constant_
     const int seq = p.seq[a], h = blockIdx.y;
     const int32_t pg = p.page0[a] + ((int)blockIdx.x - p.off[a]);
     const int64_t row = g.unit_row(seq, p.layer, h);
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // the write is done
     if (p.meta.pol[row].kind != kGlobal || pg >= p.meta.npages[row] ||
         (int64_t)(pg + 1) * g.page > p.meta.seqlen[(int64_t)seq * g.layers + p.layer])
         return;
@@ -178,9 +179,9 @@ sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, i
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &capture);
     if (e != cudaSuccess) return cuda_fail(e, "stream query");
-    std::unique_ptr<BoundsParams> pp(new BoundsParams());
+    std::unique_ptr<BoundsParams> pp(new BoundsParams);      // (its lists are filled as far as they are used)
     BoundsParams& p = *pp;
-    p.off[0] = 0;
+    p.n_seqs = p.off[0] = 0;
     for (int b = 0; b < n_seqs; ++b) {
         if (hi[b] <= lo[b]) continue;
         const UnitPol* pol = &c->h_pol[((size_t)seqs[b] * L + layer) * H];
@@ -202,12 +203,21 @@ sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, i
     p.codes = c->bounds.codes;
     p.step = c->bounds.step;
     p.kpool = c->kpool;
-    const dim3 grid((unsigned)p.off[p.n_seqs], (unsigned)H);
-    if (c->geo.fp4) k_bounds<kFp4, 128><<<grid, kBoundThreads, 0, stream>>>(p);
-    else if (c->geo.fp8) k_bounds<kFp8, 128><<<grid, kBoundThreads, 0, stream>>>(p);
-    else if (c->geo.d == 128) k_bounds<kBf16, 128><<<grid, kBoundThreads, 0, stream>>>(p);
-    else k_bounds<kBf16, 64><<<grid, kBoundThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
+    // launched while the write's last blocks run
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.off[p.n_seqs], (unsigned)H);
+    cfg.blockDim = dim3(kBoundThreads);
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const BoundsParams& q = p;
+    if (c->geo.fp4) e = cudaLaunchKernelEx(&cfg, k_bounds<kFp4, 128>, q);
+    else if (c->geo.fp8) e = cudaLaunchKernelEx(&cfg, k_bounds<kFp8, 128>, q);
+    else if (c->geo.d == 128) e = cudaLaunchKernelEx(&cfg, k_bounds<kBf16, 128>, q);
+    else e = cudaLaunchKernelEx(&cfg, k_bounds<kBf16, 64>, q);
     return e == cudaSuccess ? SP_OK : cuda_fail(e, "page bounds launch");
 }
 

@@ -334,24 +334,27 @@ struct KeptParams {
     Cap score_cap;
     int32_t seq[kMaxCallSeqs], n[kMaxCallSeqs];
 };
-// What the units of a small call have to do (n = 0: a large call): groups of 16
-// slots that they read, and whether their pages are chosen.
+// What the call's units have to do: groups of 16 slots that they read (about), and
+// for a small call (n units, else n = 0) those of each and whether its pages are
+// chosen.
 constexpr int kKeptLoads = 16;
 struct KeptLoad {
+    int64_t total, longest;
     int32_t n;
     int32_t groups[kKeptLoads];
     bool chosen[kKeptLoads];
 };
 // bf16 pages (sp_kept.cu, sp_kept_capped.cu), FP8 and 4-bit pages (sp_kept_coded.cu,
-// sp_kept_coded_capped.cu).
-cudaError_t launch_kept_bf16_plain(KeptParams& p, const KeptLoad& load, cudaStream_t s);
-cudaError_t launch_kept_bf16_capped(KeptParams& p, const KeptLoad& load, cudaStream_t s);
-cudaError_t launch_kept_coded_plain(KeptParams& p, const KeptLoad& load, cudaStream_t s);
-cudaError_t launch_kept_coded_capped(KeptParams& p, const KeptLoad& load, cudaStream_t s);
-inline cudaError_t launch_kept(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+// sp_kept_coded_capped.cu).  `serves` is cleared, and nothing launched, where a
+// choice in a launch of its own is the better way.
+cudaError_t launch_kept_bf16_plain(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s);
+cudaError_t launch_kept_bf16_capped(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s);
+cudaError_t launch_kept_coded_plain(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s);
+cudaError_t launch_kept_coded_capped(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s);
+inline cudaError_t launch_kept(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
     if (p.geo.fp8 || p.geo.fp4)
-        return p.score_cap.on ? launch_kept_coded_capped(p, load, s) : launch_kept_coded_plain(p, load, s);
-    return p.score_cap.on ? launch_kept_bf16_capped(p, load, s) : launch_kept_bf16_plain(p, load, s);
+        return p.score_cap.on ? launch_kept_coded_capped(p, load, serves, s) : launch_kept_coded_plain(p, load, serves, s);
+    return p.score_cap.on ? launch_kept_bf16_capped(p, load, serves, s) : launch_kept_bf16_plain(p, load, serves, s);
 }
 // Bounds of the pages that a write of positions [lo[b], hi[b]) of sequence seqs[b]
 // touched, where the cache has them (sp_bounds.cu); the lengths are those after

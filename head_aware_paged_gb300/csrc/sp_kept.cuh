@@ -709,8 +709,19 @@ inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
 // differ much (one sequence's GLOBAL heads and its LOCAL ones): then the largest
 // clusters can end first although some units wait (1 x 128K, two of eight heads
 // GLOBAL: 17.5 us against 22.3; 1 x 4K, all GLOBAL: 18 against 10).
+//
+// A unit is one cluster's work, so many pages of few units, or of some among many
+// light ones, leave most of the GPU waiting for them, and k_decode, which shares all
+// pages out evenly, is ahead although it starts after the choice.  Up to 48 groups a
+// warp of the longest unit this way was never behind; units of about the same length
+// bear more (groups a warp, then microseconds in one launch / in two; 32K tokens a
+// sequence: bf16, 32 sequences, 64: 107 / 136, 128: 194 / 210, 256: 369 / 359; 16
+// sequences, 128: 192 / 190; FP8, 32 sequences, 64: 81 / 105, 128: 143 / 144; 4 bits,
+// 64: 64 / 82, 128: 109 / 105.  One GLOBAL head of eight, 32 sequences: bf16 32: 62 / 71,
+// 64: 98 / 75; FP8 78 / 60; 4 bits 63 / 47.  One sequence of 128K, blocks of 8 warps, 64:
+// bf16 89 / 75, FP8 75 / 71, 4 bits 64 / 54, 32: 53 / 55, 45 / 56, 41 / 47).
 template <int KV, int D, int NH, bool CAP>
-cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
+cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
     typedef KeptLaunch<KV, D, NH, 8, CAP> Eight;
     typedef KeptLaunch<KV, D, NH, 4, CAP> Four;
     typename Eight::Fit eight;
@@ -720,33 +731,45 @@ cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, cudaStream_t 
     if (e != cudaSuccess) return e;
     const int units = p.n_seqs * p.geo.hkv;
     constexpr int NG = Rows<KV, D>::NG;
-    if (units <= eight.units[4]) return Eight::run(p, 4, s);
-    if (units <= eight.units[3]) {
+    int ranks = 0, warps = 4;                         // (the former as a power of two)
+    if (units <= eight.units[4]) {
+        ranks = 4;
+        warps = 8;
+    } else if (units <= eight.units[3]) {
         const bool largest = load.n == units && eight.units[4] > 0 &&
                              kept_span(load, eight.units[4], 128 * NG) < kept_span(load, eight.units[3], 64 * NG);
-        return Eight::run(p, largest ? 4 : 3, s);
+        ranks = largest ? 4 : 3;
+        warps = 8;
+    } else if (units <= four.units[4]) {
+        ranks = 4;
+    } else if (units <= eight.units[2]) {
+        ranks = 2;
+        warps = 8;
+    } else {
+        for (int r = 3; r > 0 && ranks == 0; --r)
+            if (units <= four.units[r]) ranks = r;
     }
-    if (units <= four.units[4]) return Four::run(p, 4, s);
-    if (units <= eight.units[2]) return Eight::run(p, 2, s);
-    for (int r = 3; r > 0; --r)
-        if (units <= four.units[r]) return Four::run(p, r, s);
-    return Four::run(p, 0, s);
+    const int64_t per_warp = load.longest / (warps << ranks);
+    const bool even = 4 * load.total >= 3 * load.longest * units;
+    serves = per_warp <= 48 || (warps == 4 && even && per_warp <= (KV == kRowsBf16 ? 128 : 64));
+    if (!serves) return cudaSuccess;
+    return warps == 8 ? Eight::run(p, ranks, s) : Four::run(p, ranks, s);
 }
 
 template <int KV, int D, bool CAP>
-cudaError_t launch_kept_type(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
-    return p.geo.group > 8 ? launch_kept_heads<KV, D, 2, CAP>(p, load, s) : launch_kept_heads<KV, D, 1, CAP>(p, load, s);
-}
-
-template <bool CAP>
-cudaError_t launch_kept_bf16(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
-    return p.geo.d == 128 ? launch_kept_type<kRowsBf16, 128, CAP>(p, load, s)
-                          : launch_kept_type<kRowsBf16, 64, CAP>(p, load, s);
+cudaError_t launch_kept_type(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
+    return p.geo.group > 8 ? launch_kept_heads<KV, D, 2, CAP>(p, load, serves, s)
+                           : launch_kept_heads<KV, D, 1, CAP>(p, load, serves, s);
 }
 template <bool CAP>
-cudaError_t launch_kept_coded(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
-    return p.geo.fp4 ? launch_kept_type<kRowsFp4, 128, CAP>(p, load, s)
-                     : launch_kept_type<kRowsFp8, 128, CAP>(p, load, s);
+cudaError_t launch_kept_bf16(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
+    return p.geo.d == 128 ? launch_kept_type<kRowsBf16, 128, CAP>(p, load, serves, s)
+                          : launch_kept_type<kRowsBf16, 64, CAP>(p, load, serves, s);
+}
+template <bool CAP>
+cudaError_t launch_kept_coded(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
+    return p.geo.fp4 ? launch_kept_type<kRowsFp4, 128, CAP>(p, load, serves, s)
+                     : launch_kept_type<kRowsFp8, 128, CAP>(p, load, serves, s);
 }
 
 }  // namespace

@@ -3,8 +3,8 @@
 
 namespace sp {
 
-cudaError_t launch_kept_coded_plain(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
-    return launch_kept_coded<false>(p, load, s);
+cudaError_t launch_kept_coded_plain(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
+    return launch_kept_coded<false>(p, load, serves, s);
 }
 
 }  // namespace sp

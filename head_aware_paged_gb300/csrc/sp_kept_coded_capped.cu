@@ -4,8 +4,8 @@
 
 namespace sp {
 
-cudaError_t launch_kept_coded_capped(KeptParams& p, const KeptLoad& load, cudaStream_t s) {
-    return launch_kept_coded<true>(p, load, s);
+cudaError_t launch_kept_coded_capped(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
+    return launch_kept_coded<true>(p, load, serves, s);
 }
 
 }  // namespace sp

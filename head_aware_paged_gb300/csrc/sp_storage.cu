@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(256)
 k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict__ k,
           const __nv_bfloat16* __restrict__ v, int64_t row_stride,
           __nv_bfloat16* __restrict__ kpool, __nv_bfloat16* __restrict__ vpool) {
+    asm volatile("griddepcontrol.launch_dependents;");      // (page bounds may start when the last blocks have)
     const int u = blockIdx.y;
     const int b = u / g.hkv, h = u % g.hkv;
     const int seq = cs.seq[b];

@@ -169,6 +169,25 @@ def test_pages_and_outputs(kv, d, P, hq, hkv):
     _check_select(c, ids, pols, q, 5, 1, 2, cap=20.0, scales=scales, what="capped")
 
 
+@pytest.mark.parametrize("kv,seqs,hq,hkv", [("bf16", 1, 16, 8), ("bf16", 2, 5, 5), ("bf16", 5, 72, 8), ("bf16", 12, 16, 8),
+                                            ("bf16", 27, 8, 8), ("bf16", 40, 24, 8), ("fp8", 6, 8, 8), ("fp8", 31, 16, 8),
+                                            ("fp4", 3, 24, 8), ("fp4", 20, 16, 8), ("fp4", 33, 72, 8)])
+def test_batches(kv, seqs, hq, hkv):
+    """From one unit to hundreds (blocks and warps a unit differ), ragged."""
+    gpu_ready()
+    P, rng = 16, np.random.default_rng(seqs)
+    pols = _classes(hkv)
+    lens = [int(x) for x in rng.integers(1, 500, seqs)]
+    lens[0] = 1100
+    c = _mk(hq, hkv, 128, P, seqs, 1200, pages=seqs * hkv * 34 + hkv * 40, kv=kv)
+    for s, n in enumerate(lens):
+        c.set_policy(s, to_c_policies([pols]))
+        c.build(s, 0, _keys(n, hkv, 128, 10 * s), W.normal((n, hkv, 128), 10 * s + 5, device="cuda"))
+    ids = [int(x) for x in rng.permutation(seqs)]
+    q = W.normal((seqs, hq, 128), 99, device="cuda")
+    _check_select(c, ids, pols, q, 6, 1, 2, cap=30.0 if seqs % 3 == 0 else None)
+
+
 @pytest.mark.parametrize("kv,P", [("bf16", 64), ("fp8", 16), ("fp4", 32)])
 def test_all_pages_kept(kv, P):
     """More pages asked for than there are: plain attention over everything that
@@ -258,6 +277,24 @@ def test_many_pages_kept(kv, d, hq, hkv, cap):
     again = c.decode_select(0, [1, 0, 2], q, 2060, 1, 2, score_cap=cap)
     few = c.decode_select(0, [0], q[1:2].contiguous(), 2060, 1, 2, score_cap=cap)
     assert torch.equal(again[2][1], few[2][0])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_one_heavy_head_among_light_ones(kv):
+    """One GLOBAL head of each of 24 sequences keeps many pages, the others read a
+    few rows: shared out page by page instead of unit by unit."""
+    gpu_ready()
+    P, hkv, hq = 32, 8, 16
+    pols = [W.HeadPolicy(G) if h == 3 else W.HeadPolicy(L, 4, 60) for h in range(hkv)]
+    lens = [6000 + 10 * s for s in range(24)]
+    c = _mk(hq, hkv, 128, P, 24, 6400, pages=24 * 300, kv=kv)
+    for s, n in enumerate(lens):
+        c.set_policy(s, to_c_policies([pols]))
+        c.build(s, 0, _keys(n, hkv, 128, 10 * s), W.normal((n, hkv, 128), 10 * s + 5, device="cuda"))
+    q = W.normal((24, hq, 128), 99, device="cuda")
+    out, lse, pages = c.decode_select(0, list(range(24)), q, 160, 1, 2)
+    for s in (0, 11, 23):
+        _check_select(c, [s], pols, q[s:s + 1], 160, 1, 2, what=str(s), res=(out[s:s + 1], lse[s:s + 1], pages[s:s + 1]))
 
 
 @pytest.mark.parametrize("kv,d,P,hq,hkv", [("bf16", 64, 16, 4, 2), ("bf16", 128, 64, 9, 3), ("fp8", 128, 32, 9, 3),
