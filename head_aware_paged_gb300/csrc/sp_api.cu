@@ -208,12 +208,12 @@ sp_status write_tokens(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t 
     cudaError_t e = launch_scatter(c, cs, layer, k, v, row_stride, max_items, stream);
     if (e != cudaSuccess) return cuda_fail(e, "scatter launch");
     if (!c->bounds.codes) return SP_OK;
-    std::vector<int64_t> lo(n_seqs), hi(n_seqs);
+    int64_t lo[kMaxCallSeqs], hi[kMaxCallSeqs];
     for (int b = 0; b < n_seqs; ++b) {
         lo[b] = cs.n_old[b];
         hi[b] = lo[b] + counts[b];
     }
-    return update_bounds(c, layer, seqs, n_seqs, lo.data(), hi.data(), stream);
+    return update_bounds(c, layer, seqs, n_seqs, lo, hi, stream);
 }
 
 // Rows a unit holding n tokens keeps (the retained set of the slot rules):
@@ -995,10 +995,12 @@ sp_status sp_rope_realign(sp_cache* c, int32_t layer, const int32_t* seq_ids, in
     cudaError_t e = flush();
     if (e != cudaSuccess) return cuda_fail(e, "rope launch");
     if (!c->bounds.codes) return SP_OK;
-    std::vector<int64_t> lo(n_seqs, pos_lo), hi(n_seqs);
-    for (int b = 0; b < n_seqs; ++b)
+    int64_t lo[kMaxCallSeqs], hi[kMaxCallSeqs];
+    for (int b = 0; b < n_seqs; ++b) {
+        lo[b] = pos_lo;
         hi[b] = std::min<int64_t>(pos_hi, c->h_seqlen[(size_t)seq_ids[b] * c->cfg.num_layers + layer]);
-    return update_bounds(c, layer, seq_ids, n_seqs, lo.data(), hi.data(), st);
+    }
+    return update_bounds(c, layer, seq_ids, n_seqs, lo, hi, st);
 }
 
 sp_status sp_pack_seq(sp_cache* c, int32_t seq, void* dst, size_t dst_bytes, size_t* packed_bytes,

@@ -8,8 +8,6 @@
 // device's own length, page table and head class decide whether a page is
 // there and full, so a replayed write leaves them right whatever was appended
 // in between.
-#include <memory>
-
 #include "sp_bounds.cuh"
 #include "sp_device.cuh"
 #include "sp_internal.h"
@@ -179,8 +177,7 @@ sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, i
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &capture);
     if (e != cudaSuccess) return cuda_fail(e, "stream query");
-    std::unique_ptr<BoundsParams> pp(new BoundsParams);      // (its lists are filled as far as they are used)
-    BoundsParams& p = *pp;
+    BoundsParams p;                                           // (its lists are filled as far as they are used)
     p.n_seqs = p.off[0] = 0;
     for (int b = 0; b < n_seqs; ++b) {
         if (hi[b] <= lo[b]) continue;

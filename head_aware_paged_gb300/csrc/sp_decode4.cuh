@@ -78,7 +78,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 // slots [lo, hi) as lo | hi << 8.
 struct Item4 { uint32_t g[kD4Groups], visible; };
 
-// Item j of unit u (positions and slots are below 2^31).
+// Item j of unit u (positions and slots are below 2^31).  KEPT: pages are chosen for
+// the call.
+template <bool KEPT>
 __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_t j) {
     const Geo& g = p.geo;
     const uint32_t P = (uint32_t)g.page, lp = 31 - __clz(P);
@@ -87,7 +89,7 @@ __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_
     const int64_t row = g.unit_row(seq, p.layer, h);
     const UnitPol pol = p.meta.pol[row];
     // chosen pages lie end to end in a table of their own
-    const bool chosen = p.kept && pol.kind == kGlobal;
+    const bool chosen = KEPT && pol.kind == kGlobal;
     if (chosen) wait_for_choice();
     const int32_t t = chosen ? (int32_t)kept_slots((int64_t)p.tq[b] + 1, (int)P, p.kept_cap) - 1 : p.tq[b];
     // the visible ranges of decode_ranges (sp_rules.h), in 32 bits
@@ -143,7 +145,7 @@ __device__ __forceinline__ Item4 find_item4(const DecodeParams& p, int u, int32_
 // NH: 8-head steps (group <= 8 * NH).  Two CTAs of 8 warps share an SM at
 // NH = 1 (at most 128 registers a thread); NH = 2 holds twice the output and
 // runs one.
-template <int NH, bool CAP>
+template <int NH, bool CAP, bool KEPT>
 __global__ void __launch_bounds__(kD4Threads, NH == 1 ? 2 : 1)
 k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kpool,
           const uint8_t* __restrict__ vpool) {
@@ -220,7 +222,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
                 if (end > last) break;
                 if (end <= x) { u = u_batch + 1; start = end; }
             }
-            if (batch + lane < mine) held = find_item4(p, u, x - start);
+            if (batch + lane < mine) held = find_item4<KEPT>(p, u, x - start);
         }
         next.visible = __shfl_sync(0xffffffffu, held.visible, i - batch);
         next.g[0] = __shfl_sync(0xffffffffu, held.g[0], i - batch);
@@ -650,7 +652,7 @@ k_decode4(const __grid_constant__ DecodeParams p, const uint8_t* __restrict__ kp
     }
 }
 
-template <int NH, bool CAP>
+template <int NH, bool CAP, bool KEPT>
 cudaError_t launch_decode4_t(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s) {
     // merge buffer: the warps' first partials, or two [grid][group] arrays
     // for the merge across CTAs, whichever is larger (a multiple of 4)
@@ -663,18 +665,20 @@ cudaError_t launch_decode4_t(const sp_cache* c, DecodeParams& p, int grid, cudaS
     p.rem = (int32_t)(p.total_items % grid);
     const int smem = kD4Warps * kD4StageBytes + merge_bytes;
     if (smem > kCap) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap);
+    auto kernel = k_decode4<NH, CAP, KEPT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap);
     if (e == cudaSuccess && NH == 1)
-        e = cudaFuncSetAttribute(k_decode4<NH, CAP>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 (int)cudaSharedmemCarveoutMaxShared);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    return launch_after_choice(p, k_decode4<NH, CAP>, grid, kD4Threads, smem, s, p,
+    return launch_after_choice(p, kernel, grid, kD4Threads, smem, s, p,
                                reinterpret_cast<const uint8_t*>(c->kpool), reinterpret_cast<const uint8_t*>(c->vpool));
 }
 
 template <bool CAP>
 cudaError_t launch_decode4_any(const sp_cache* c, DecodeParams& p, int grid, cudaStream_t s) {
-    return c->geo.group <= 8 ? launch_decode4_t<1, CAP>(c, p, grid, s) : launch_decode4_t<2, CAP>(c, p, grid, s);
+    if (p.kept)
+        return c->geo.group <= 8 ? launch_decode4_t<1, CAP, true>(c, p, grid, s) : launch_decode4_t<2, CAP, true>(c, p, grid, s);
+    return c->geo.group <= 8 ? launch_decode4_t<1, CAP, false>(c, p, grid, s) : launch_decode4_t<2, CAP, false>(c, p, grid, s);
 }
 
 }  // namespace

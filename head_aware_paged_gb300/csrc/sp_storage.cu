@@ -168,7 +168,7 @@ k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict
         for (int i = 0; i < kAhead; ++i) {
             page[i] = -1;
             const int64_t e = e0 + i * step;
-            if (e >= total) break;
+            if (e >= total) continue;
             const int64_t j = e >> lv;
             const int32_t item = (int32_t)(j < n0 ? r.lo[0] + j : r.lo[1] + (j - n0));
             int32_t t = item, us = item;                  // unit_slot of sp_rules.h in 32 bits

@@ -35,7 +35,6 @@
 // (an instance of its own: 28.5 instead of 26.9 us replaying the 8,192 rows).
 #include <cstring>
 #include <memory>
-#include <vector>
 
 #include "sp_rotate.cuh"
 
@@ -418,9 +417,12 @@ sp_status write_rope(sp_cache* c, int32_t layer, const int32_t* seqs, int32_t n_
             c->h_npages[((size_t)seqs[b] * L + layer) * H + h] += p.off[b * H + h + 1] - p.off[b * H + h];
     }
     if (!c->bounds.codes) return SP_OK;
-    std::vector<int64_t> lo(p.pos, p.pos + n_seqs), hi(lo);
-    for (int b = 0; b < n_seqs; ++b) hi[b] += cu[b + 1] - cu[b];
-    return update_bounds(c, layer, seqs, n_seqs, lo.data(), hi.data(), stream);
+    int64_t lo[kMaxCallSeqs], hi[kMaxCallSeqs];
+    for (int b = 0; b < n_seqs; ++b) {
+        lo[b] = p.pos[b];
+        hi[b] = lo[b] + cu[b + 1] - cu[b];
+    }
+    return update_bounds(c, layer, seqs, n_seqs, lo, hi, stream);
 }
 
 }  // namespace

@@ -327,7 +327,7 @@ sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
  * The bounds live in a caller-owned device buffer (256-byte aligned, at least
  * sp_page_bounds_bytes bytes: 2 * head_dim + 4 per page, and scratch of the choice),
  * attached while no sequence holds tokens (SP_ERR_INVALID_ARG otherwise; null
- * detaches; synchronous).  From then on every call that writes keys (sp_build_cache,
+ * detaches; synchronous) and kept alive until it is detached or the cache destroyed.  From then on every call that writes keys (sp_build_cache,
  * sp_append_kv, the rope forms, sp_rope_realign, sp_unpack_seq) also computes the
  * bounds of the full pages that it touched, in one more launch; attach the buffer
  * before capturing such calls.  Two decodes of one cache share the scratch, as they share the
@@ -539,8 +539,8 @@ sp_status sp_selftest_bounded_wait(sp_cache* cache, int64_t limit_cycles, int32_
 /* Instrumentation for profilers and benchmarks (the pages have no
  * counterpart).  Arms one pair of caller-created CUDA events (cudaEvent_t
  * handles passed as void*) for the next attention call on this cache
- * (sp_attention_prefill, sp_attention_decode or
- * sp_attention_decode_static_scratch): that call records start_event on its
+ * (sp_attention_prefill, sp_attention_decode, their capped forms,
+ * sp_attention_decode_select or sp_attention_decode_static_scratch): that call records start_event on its
  * stream immediately before its first kernel launch and end_event
  * immediately after its last one (the prefill's merge included), so the
  * interval between them is the device time of the call's kernels without
