@@ -7,6 +7,11 @@
 // kept pages' places in the pool end to end for the decode, which then streams them
 // as if they were the whole unit.  The decode is launched early and waits for the
 // table where it needs it (its start costs as much as the choice).
+//
+// Bound by the bounds' bytes (2 d + 4 a candidate) when there are many units, by its
+// chain of look-ups, barriers and passes when there are few.  Scores by dp4a, one
+// 16-byte piece a lane and five shuffles a head: 24.1 us for 256 units of 504
+// candidates (33 MB), 9.3 us for 8 units of 61; by integer products 18.9 and 7 us.
 #include <algorithm>
 
 #include "sp_choose.cuh"

@@ -22,8 +22,21 @@
 // key's row serve as they come; V's rows of two keys are interleaved by byte
 // permutations.  P^T goes through two 8 x 8 register transposes.
 //
-// Scores, maxima, sums and partials are fp32; P is rounded to bf16 (2^-9 of a weight;
-// FP8 and 4-bit pages: f16, 2^-12), the query under channel scales to f16.
+// Scores, maxima, sums and partials are fp32; P is rounded to bf16 (2^-8 of a weight;
+// FP8 and 4-bit pages: f16, 2^-11), the query under channel scales to f16.
+//
+// What it takes (8 KV heads of 4 query heads, d 128, page 64; with a launch for the
+// choice in brackets): 1 x 4K, 16 of 64 pages 8.5 us (23); 1 x 128K, two heads GLOBAL,
+// 128 of 2,048 pages 17.2 (40); 32 x 32K, all GLOBAL, 32 of 512 pages 61 (72): 8.5 us of
+// it reading 34 MB of bounds, 2.5 choosing, 43 streaming 268 MB at 6.2 TB/s.  Small
+// calls are bound by their chain: look-ups, three barriers and about 1.1 us a step of
+// 16 bf16 keys a warp.
+//
+// Measured and not kept: three tiles of bounds in flight (spills: 32 x 32K 63 us); the
+// other blocks' keys read after the barrier instead of pushed before it (1 x 128K 3 us
+// more); the choice by every warp alone, bisecting keys in registers (504 keys: 7 to 17
+// us against 2.5); at 8 warps a block two steps in flight, or twice the keys a step (no
+// change: a step's own chain of products, votes and exponentials decides).
 #pragma once
 #include <algorithm>
 #include <mutex>
@@ -359,10 +372,10 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(c
         }
         if (p.top > 0) {
             score_pages<D, NH, W>(p, qc, tab, q0, c0, c1, id, [&] { if (ranks > 1) cluster_wait(); },
-                                           [&](int c, uint32_t k, int half) {
-                                               if (ranks == 1) list[c] = k;      // (both halves the same)
-                                               else for (int r = half; r < ranks; r += 2) st_peer(peer_smem(&list[c], r), k);
-                                           });
+                                  [&](int c, uint32_t k, int half) {
+                                      if (ranks == 1) list[c] = k;               // (both halves the same)
+                                      else for (int r = half; r < ranks; r += 2) st_peer(peer_smem(&list[c], r), k);
+                                  });
             if (ranks > 1) { cluster_arrive(); cluster_wait(); } else __syncthreads();
             auto take = [&](int at, int c) {
                 kept[p.first + at] = tab[p.first + c];

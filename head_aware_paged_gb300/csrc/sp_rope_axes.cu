@@ -7,7 +7,10 @@
 // in fp32, rounded once to bf16.  Angles as for the writes into the pages
 // (sp_rotate.cuh): one (cos, sin) per row and pair serves every head of q and k.
 //
-// Bound by memory: 2 bytes an element read and as much written.
+// Bound by memory: 2 bytes an element read and as much written.  32,768 rows of 32
+// query and 8 KV heads (671 MB) 103 us, 6.5 TB/s, 0.96 of the copy rate; 777 rows of
+// 28 and 4 heads 4.0 us, launch and two dependent loads.  Four rows a block share its
+// start from 2,048 rows on; fewer rows take a block each, for more of them.
 #include "sp_rotate.cuh"
 
 namespace sp {
