@@ -589,3 +589,106 @@ def test_refusals():
     with pytest.raises(H.SegPagedError):
         c.decode_select(0, [0], q, 2)
     assert c.status() == 0
+
+
+def test_two_caches_on_two_streams():
+    """Each cache has its own bounds and scratch: calls on both may run at once."""
+    gpu_ready()
+    caches, want, qs = [], [], []
+    pols = [W.HeadPolicy(G)] * 4
+    for i, kv in enumerate(("bf16", "fp4")):
+        c = _mk(16, 4, 128, 16, 2, 40000, kv=kv)
+        for s in range(2):
+            c.set_policy(s, to_c_policies([pols]))
+            n = 38000 if s == 0 else 3000
+            c.build(s, 0, _keys(n, 4, 128, 10 * i + s), W.normal((n, 4, 128), s + 5, device="cuda"))
+        q = W.normal((2, 16, 128), 9 + i, device="cuda")
+        caches.append(c)
+        qs.append(q)
+        want.append([c.decode_select(0, [0, 1], q, top, 1, 2) for top in (40, 2100)])      # one launch, two launches
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in caches]
+    got = [[], []]
+    for _ in range(5):
+        for i, c in enumerate(caches):
+            for top in (40, 2100):
+                with torch.cuda.stream(streams[i]):
+                    got[i].append(c.decode_select(0, [0, 1], qs[i], top, 1, 2))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for k, res in enumerate(got[i]):
+            for a, b in zip(res, want[i][k % 2]):
+                assert torch.equal(a, b), (i, k)
+        assert caches[i].status() == 0
+
+
+@pytest.mark.parametrize("top", [3, 2100])
+def test_stream_argument_and_launch_events(top):
+    gpu_ready()
+    c = _mk(4, 1, 64, 16, 1, 40000)
+    c.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = _keys(39000, 1, 64, 1)
+    c.build(0, 0, k, k)
+    q = W.normal((1, 4, 64), 9, device="cuda")
+    want = c.decode_select(0, [0], q, top)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for x in e:
+        x.record(s)
+    c.set_launch_events(*e)
+    got = c.decode_select(0, [0], q, top, stream=s)
+    s.synchronize()
+    assert 0.0 < e[0].elapsed_time(e[1]) < 1000.0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_the_largest_batch():
+    """512 sequences of 8 KV heads, a few tokens to a few pages each."""
+    gpu_ready()
+    hkv, P = 8, 16
+    pols = [W.HeadPolicy(G) if h % 2 == 0 else W.HeadPolicy(L, 2, 9) for h in range(hkv)]
+    lens = [1 + (37 * s) % 150 for s in range(512)]
+    c = _mk(hkv, hkv, 64, P, 512, 160, batch=512)
+    x, y = _keys(150, hkv, 64, 1), W.normal((150, hkv, 64), 2, device="cuda")
+    for s, n in enumerate(lens):
+        c.set_policy(s, to_c_policies([pols]))
+        c.build(s, 0, x[150 - n:], y[150 - n:])
+    q = W.normal((512, hkv, 64), 3, device="cuda")
+    out, lse, pages = c.decode_select(0, list(range(512)), q, 2, 1, 1)
+    for s in (0, 1, 4, 100, 255, 256, 511):
+        _check_select(c, [s], pols, q[s:s + 1], 2, 1, 1, what=str(s), res=(out[s:s + 1], lse[s:s + 1], pages[s:s + 1]))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_pools_past_4_gib(kv):
+    """The same sequence at the start of a pool and behind 4 GiB of keys: the same
+    pages, the same bits."""
+    gpu_ready()
+    hkv, P, n = 8, 128, 262144
+    per = hkv * n // P                                        # pages a filler takes
+    fill = -(-(1 << 32) // (per * P * 128 * (2 if kv == "bf16" else 1)))
+    k = torch.randn(n, hkv, 128, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    m = 9000
+    ks, vs = _keys(m, hkv, 128, 1), W.normal((m, hkv, 128), 2, device="cuda")
+    q = W.normal((1, 16, 128), 3, device="cuda")
+    res = []
+    for fillers in (0, fill):
+        c = _mk(16, hkv, 128, P, fill + 1, n, pages=fillers * per + hkv * (m // P + 1), kv=kv)
+        pol = to_c_policies([[W.HeadPolicy(G)] * hkv])
+        for s in range(fillers):
+            c.set_policy(s, pol)
+            c.build(s, 0, k, k)
+        c.set_policy(fill, pol)
+        c.build(fill, 0, ks, vs)
+        if fillers:
+            assert min(c.export_table(fill, 0, 7)[0]) * P * 128 * (2 if kv == "bf16" else 1) >= 1 << 32
+        res.append([c.decode_select(0, [fill], q, t, 1, 2) for t in (5, 60)])
+        torch.cuda.synchronize()
+        assert c.status() == 0
+        c.close()
+        del c
+    for a, b in zip(*res):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)

@@ -50,7 +50,7 @@ def _of(d, n, seed):
 
 @pytest.mark.parametrize("n,hq,hkv,d,axes", [(1, 32, 8, 128, 3), (3, 14, 2, 64, 3), (777, 28, 4, 128, 3), (257, 1, 1, 64, 1),
                                              (2049, 5, 5, 128, 4), (5000, 35, 5, 64, 2), (64, 0, 8, 128, 3),
-                                             (9, 16, 0, 64, 3)])
+                                             (9, 16, 0, 64, 3), (5, 1024, 3, 64, 3)])
 def test_rows_against_64_bits(n, hq, hkv, d, axes):
     import head_aware_paged_gb300 as H
     gpu_ready()
@@ -82,7 +82,7 @@ def test_far_negative_and_shared_positions():
     pos = np.stack([np.arange(n) * 100003 - 2000000, np.full(n, -1), np.arange(n) + (1 << 33)])
     qo, _ = H.sp_rope_axes(q, None, torch.from_numpy(pos).cuda(), of)
     _close(qo, _turned(q, pos, of), "far")
-    # a turn's 64-bit reduction takes any int64: p and p + 2^62 times a frequency of 4 / 2^64 turns... agree
+    # positions near 2^62: whole turns away from small ones
     freq = [2 * np.pi / 8.0] * 64                                            # an eighth of a turn a position
     big = torch.tensor([[(1 << 62) + 8 * i + i % 8 for i in range(n)]], device="cuda")
     small = torch.tensor([[i % 8 for i in range(n)]], device="cuda")
