@@ -18,6 +18,13 @@ and scores capped by a tanh:
 
     q1 = cache.append_kv_rope(layer, [seq], [0, 1], q1, k1, v1)
     out, lse = cache.decode(layer, [seq], q1, score_cap=50.0)
+
+or, with positions on several axes and GLOBAL heads that read only the pages
+that promise the largest scores for the query:
+
+    cache.attach_page_bounds()                        # before tokens are held
+    q1 = cache.append_kv_rope_axes(layer, [seq], [0, 1], q1, k1, v1, positions, axis_of)
+    out, lse, pages = cache.decode_select(layer, [seq], q1, top_pages=24)
 """
 from __future__ import annotations
 
