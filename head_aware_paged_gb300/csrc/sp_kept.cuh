@@ -23,7 +23,10 @@
 // permutations.  P^T goes through two 8 x 8 register transposes.
 //
 // Scores, maxima, sums and partials are fp32; P is rounded to bf16 (2^-8 of a weight;
-// FP8 and 4-bit pages: f16, 2^-11), the query under channel scales to f16.
+// FP8 and 4-bit pages: f16, 2^-11), the query under channel scales to f16.  A score's
+// tanh is CUDA's (relative to the score it is exact to fp32; the difference of two
+// numbers of the cap's size that k_decode takes, which is shorter, was 9e-6 off at a cap
+// of 50 and showed in the lse of few keys; no difference in time).
 //
 // What it takes (8 KV heads of 4 query heads, d 128, page 64; with a launch for the
 // choice in brackets): 1 x 4K, 16 of 64 pages 8.5 us (23); 1 x 128K, two heads GLOBAL,
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(c
     // power of two per head that takes the largest |q * channel scale| to 2^14 .. 2^15
     // (sp_decode4.cuh says why); the scores are multiplied back in fp32.
     const float* kscale = p.meta.kscale + ((int64_t)p.layer * g.hkv + h) * D;
-    const float unit_scale = CAP ? p.score_cap.k1 : p.scale_log2;
+    const float unit_scale = CAP ? p.scale_log2 / p.score_cap.a : p.scale_log2;      // (to score / cap, or to log2 units)
     uint32_t qb[NH][KS][2];
     #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(c
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float x = sc[q][nh][e] * ((e & 1) ? f.y : f.x);
-                    if constexpr (CAP) x = capped_log2(x, p.score_cap);
+                    if constexpr (CAP) x = p.score_cap.a * tanhf(x);
                     x = (e < 2 ? in_a : in_b) ? x : -INFINITY;
                     sc[q][nh][e] = x;
                     mx[nh][e & 1] = fmaxf(mx[nh][e & 1], x);

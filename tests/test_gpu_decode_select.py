@@ -692,3 +692,27 @@ def test_pools_past_4_gib(kv):
     for a, b in zip(*res):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("cap", [1.5, 50.0, 64.0])
+def test_capped_lse_of_one_key(kv, cap):
+    """One key and one product a head, so lse = cap tanh(s / cap) with nothing summed:
+    s and s / cap three roundings of 2^-24, tanh two steps of 2^-23, times the cap
+    and back to e one each (2^-20.5 of it in all); the weight's exp2 and the sum's
+    log2 2^-22 each, absolute, with their constants' roundings 2^-20."""
+    gpu_ready()
+    hq = 16
+    c = _mk(hq, 1, 128, 16, 1, 64, kv=kv)
+    c.set_policy(0, to_c_policies([[W.HeadPolicy(G)]]))
+    k = torch.zeros(1, 1, 128, device="cuda", dtype=torch.bfloat16)
+    k[0, 0, 77] = 1.5                                           # exact in every page type
+    c.build(0, 0, k, k)
+    q = torch.zeros(1, hq, 128, device="cuda", dtype=torch.bfloat16)
+    q[0, :, 77] = torch.tensor([0.0, 1e-4, -1e-3, 0.01, 0.1, -0.5, 1.0, 3.0, -7.0, 20.0, 60.0, -150.0, 300.0, 900.0, -2000.0, 1e4])
+    out, lse, _ = c.decode_select(0, [0], q, 1, score_cap=cap)
+    s = q[0, :, 77].double().cpu() * 1.5 / np.sqrt(128.0)
+    want = cap * torch.tanh(s / cap)
+    err = (lse[0].double().cpu() - want).abs()
+    assert (err <= 2.0 ** -20.5 * want.abs() + 2.0 ** -20).all(), (err / (2.0 ** -20.5 * want.abs() + 2.0 ** -20)).max()
+    assert torch.equal(out[0, :, 77].cpu(), torch.full((hq,), 1.5, dtype=torch.bfloat16))
