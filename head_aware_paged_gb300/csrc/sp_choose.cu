@@ -83,12 +83,15 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose(const __grid_constant
             for (int c = tid; c < m; c += kChooseThreads) list[c] = __ldcg(key + c);
     }
     __syncthreads();
-    auto take = [&](int at, int c) {
-        kept[p.first + at] = tab[p.first + c];
-        if (pages) pages[p.first + at] = p.first + c;
-    };
+    auto take = [&](int at, int c) { kept[p.first + at] = p.first + c; };
     if (listed) choose_top<17, kChooseWarps>(sh, m, p.top, [&](int c) { return list[c]; }, take);
     else choose_top<0, kChooseWarps>(sh, m, p.top, [&](int c) { return __ldcg(key + c); }, take);
+    __syncthreads();
+    for (int i = p.first + tid; i < p.first + p.top; i += kChooseThreads) {      // page numbers to places
+        const int pg = kept[i];
+        kept[i] = tab[pg];
+        if (pages) pages[i] = pg;
+    }
 }
 
 }  // namespace

@@ -380,14 +380,19 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(c
                                       else for (int r = half; r < ranks; r += 2) st_peer(peer_smem(&list[c], r), k);
                                   });
             if (ranks > 1) { cluster_arrive(); cluster_wait(); } else __syncthreads();
-            auto take = [&](int at, int c) {
-                kept[p.first + at] = tab[p.first + c];
-                if (pages) pages[p.first + at] = p.first + c;
-            };
+            auto take = [&](int at, int c) { kept[p.first + at] = p.first + c; };
             auto key_at = [&](int c) { return list[c]; };
             if (m <= 5 * T) choose_top<5, W>(sh, m, p.top, key_at, take);
             else if (m <= 17 * T) choose_top<17, W>(sh, m, p.top, key_at, take);
             else if constexpr (W == 4) choose_top<33, W>(sh, m, p.top, key_at, take);
+            // page numbers to places: one look-up a thread, not one after another where
+            // a thread's run holds several
+            __syncthreads();
+            for (int i = p.first + tid; i < p.first + p.top; i += T) {
+                const int pg = kept[i];
+                kept[i] = tab[pg];
+                if (pages) pages[i] = pg;
+            }
         }
     } else if (pages) {
         for (int i = tid; i < p.cap; i += T) pages[i] = pol.kind == kGlobal && i < nb ? i : -1;
