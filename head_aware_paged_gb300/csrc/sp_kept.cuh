@@ -30,15 +30,15 @@
 //
 // What it takes (8 KV heads of 4 query heads, d 128, page 64; with a launch for the
 // choice in brackets): 1 x 4K, 16 of 64 pages 8.5 us (23); 1 x 128K, two heads GLOBAL,
-// 128 of 2,048 pages 17.2 (40); 32 x 32K, all GLOBAL, 32 of 512 pages 61 (72): 8.5 us of
-// it reading 34 MB of bounds, 2.5 choosing, 43 streaming 268 MB at 6.2 TB/s.  Small
+// 128 of 2,048 pages 15.4 (40); 32 x 32K, all GLOBAL, 32 of 512 pages 61 (72): 8.5 us of
+// it reading 34 MB of bounds, 2 choosing, 43 streaming 268 MB at 6.2 TB/s.  Small
 // calls are bound by their chain: look-ups, three barriers and about 1.1 us a step of
 // 16 bf16 keys a warp.
 //
 // Measured and not kept: three tiles of bounds in flight (spills: 32 x 32K 63 us); the
 // other blocks' keys read after the barrier instead of pushed before it (1 x 128K 3 us
 // more); the choice by every warp alone, bisecting keys in registers (504 keys: 7 to 17
-// us against 2.5); at 8 warps a block two steps in flight, or twice the keys a step (no
+// us against 2); at 8 warps a block two steps in flight, or twice the keys a step (no
 // change: a step's own chain of products, votes and exponentials decides).
 #pragma once
 #include <algorithm>
@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NH == 1 ? 3 : 2) k_kept(c
             auto take = [&](int at, int c) { kept[p.first + at] = p.first + c; };
             auto key_at = [&](int c) { return list[c]; };
             if (m <= 5 * T) choose_top<5, W>(sh, m, p.top, key_at, take);
+            else if (m <= 9 * T) choose_top<9, W>(sh, m, p.top, key_at, take);
             else if (m <= 17 * T) choose_top<17, W>(sh, m, p.top, key_at, take);
             else if constexpr (W == 4) choose_top<33, W>(sh, m, p.top, key_at, take);
             // page numbers to places: one look-up a thread, not one after another where
@@ -729,7 +730,8 @@ inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
 // 32 units: 8 warps in 4 blocks each 15.3, 4 warps in 8 each 16.5.  A few units may
 // differ much (one sequence's GLOBAL heads and its LOCAL ones): then the largest
 // clusters can end first although some units wait (1 x 128K, two of eight heads
-// GLOBAL: 17.5 us against 22.3; 1 x 4K, all GLOBAL: 18 against 10).
+// GLOBAL, while a choice took longer: 17.5 us against 22.3; 1 x 4K, all GLOBAL: 18
+// against 10).
 //
 // A unit is one cluster's work, so many pages of few units, or of some among many
 // light ones, leave most of the GPU waiting for them, and k_decode, which shares all
