@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kAllocThreads)
 k_alloc(Meta m, Geo g, CallSeqs cs, int layer, int32_t top) {
     extern __shared__ int32_t sm[];
     __shared__ int32_t warp_sums[32];
+    asm volatile("griddepcontrol.launch_dependents;");      // (the scatter's blocks may come and wait)
     const int n_units = cs.n * g.hkv;
     int32_t* dem = sm;             // demand, then offsets
     int32_t* onp = sm + n_units;   // pages held before the call
@@ -142,6 +143,7 @@ k_scatter(Meta m, Geo g, CallSeqs cs, int layer, const __nv_bfloat16* __restrict
           const __nv_bfloat16* __restrict__ v, int64_t row_stride,
           __nv_bfloat16* __restrict__ kpool, __nv_bfloat16* __restrict__ vpool) {
     asm volatile("griddepcontrol.launch_dependents;");      // (page bounds may start when the last blocks have)
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the pages are there
     const int u = blockIdx.y;
     const int b = u / g.hkv, h = u % g.hkv;
     const int seq = cs.seq[b];
@@ -322,13 +324,18 @@ cudaError_t launch_scatter(const sp_cache* c, const CallSeqs& cs, int layer,
     if (gx * cs.n * c->geo.hkv > (int64_t)16 * c->num_sms) gx = (gx + 1) / 2;
     if (gx > 4096) gx = 4096;
     dim3 grid((unsigned)gx, (unsigned)(cs.n * c->geo.hkv));
-    if (c->geo.fp4)
-        k_scatter<true><<<grid, 256, 0, s>>>(c->meta, c->geo, cs, layer, k, v, row_stride,
-                                             c->kpool, c->vpool);
-    else
-        k_scatter<false><<<grid, 256, 0, s>>>(c->meta, c->geo, cs, layer, k, v, row_stride,
-                                              c->kpool, c->vpool);
-    return cudaGetLastError();
+    // launched while the allocator runs
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, c->geo.fp4 ? k_scatter<true> : k_scatter<false>, c->meta, c->geo, cs, layer, k, v,
+                              row_stride, c->kpool, c->vpool);
 }
 
 cudaError_t launch_release(const sp_cache* c, int seq, int32_t top, cudaStream_t s) {
