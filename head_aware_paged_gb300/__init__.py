@@ -225,6 +225,8 @@ def sp_rope_axes(q: Optional[torch.Tensor], k: Optional[torch.Tensor], axis_pos:
     first = k if q is None else q
     rows, _, d = first.shape
     index, device = first.get_device(), first.device
+    # (the launch goes to the current device, on a stream of its own)
+    assert index >= 0 and index == torch.cuda.current_device(), "q, k: on the current CUDA device"
     axes, given = axis_pos.shape
     per_axis, per_row = axis_pos.stride()
     assert len(axis_of) == d // 2 and (inv_freq is None or len(inv_freq) == d // 2)
