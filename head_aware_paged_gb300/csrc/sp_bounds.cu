@@ -182,6 +182,7 @@ sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, i
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &capture);
     if (e != cudaSuccess) return cuda_fail(e, "stream query");
+    const bool graph = capture != cudaStreamCaptureStatusNone;
     BoundsParams p;                                           // (its lists are filled as far as they are used)
     p.n_seqs = p.off[0] = 0;
     for (int b = 0; b < n_seqs; ++b) {
@@ -189,10 +190,12 @@ sp_status update_bounds(const sp_cache* c, int32_t layer, const int32_t* seqs, i
         const UnitPol* pol = &c->h_pol[((size_t)seqs[b] * L + layer) * H];
         bool global = false;
         for (int h = 0; h < H; ++h) global = global || pol[h].kind == kGlobal;
-        // full pages; in a graph also the last one, which may be full by a replay
+        // Full pages of sequences with GLOBAL heads.  A replay may meet other heads and
+        // lengths than the capture (the kernel asks the device what is there by then):
+        // in a graph every page that the write touches.
         const int64_t first = lo[b] / P, n = c->h_seqlen[(size_t)seqs[b] * L + layer];
-        const int64_t end = capture != cudaStreamCaptureStatusNone ? cdiv64(hi[b], P) : min64(cdiv64(hi[b], P), n / P);
-        if (!global || end <= first) continue;
+        const int64_t end = graph ? cdiv64(hi[b], P) : min64(cdiv64(hi[b], P), n / P);
+        if (!(global || graph) || end <= first) continue;
         p.seq[p.n_seqs] = seqs[b];
         p.page0[p.n_seqs] = (int32_t)first;
         p.off[p.n_seqs + 1] = p.off[p.n_seqs] + (int32_t)(end - first);
