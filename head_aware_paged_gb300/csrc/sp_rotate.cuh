@@ -2,13 +2,15 @@
 // writes into the pages (sp_write.cu) and the rotation of plain rows
 // (sp_rope_axes.cu).
 //
-// A frequency is a 64-bit fraction of a turn, so position * frequency modulo
-// 2^64 is the angle modulo a turn, whatever the position's size or sign.
+// A frequency is a 64-bit fraction of a turn (sp_turns.h), so position * frequency
+// modulo 2^64 is the angle modulo a turn, whatever the position's size or sign: off
+// by |position| times the fraction's own error.
 #pragma once
 #include <cmath>
 
 #include "sp_device.cuh"
 #include "sp_internal.h"
+#include "sp_turns.h"
 
 namespace sp {
 
@@ -17,12 +19,10 @@ namespace sp {
 inline sp_status turns_of(double rope_theta, const double* inv_freq, int d, uint64_t (&turn)[64]) {
     if (!inv_freq && (!(rope_theta > 0.0) || !std::isfinite(rope_theta)))
         return fail(SP_ERR_INVALID_ARG, "rope_theta must be positive and finite");
-    const double two_pi = 6.283185307179586476925286766559;
     for (int i = 0; i < d / 2; ++i) {
         const double w = inv_freq ? inv_freq[i] : std::pow(rope_theta, -2.0 * i / d);
         if (!(std::fabs(w) <= 65536.0)) return fail(SP_ERR_INVALID_ARG, "frequencies must be finite, at most 2^16");
-        const double f = w / two_pi, frac = f - std::floor(f);      // [0, 1]
-        turn[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
+        turn[i] = turn_of(w);
     }
     return SP_OK;
 }

@@ -228,7 +228,8 @@ sp_status sp_append_kv_rope(sp_cache* cache, int32_t layer, const int32_t* seq_i
  *   axis_pos: DEVICE array of int64 positions, element (axis, row) at axis *
  *     axis_stride + row * row_stride (strides in elements, >= 0; 8-byte aligned;
  *     rows are those of q, k and v).  Any int64 is a position: p * w is reduced
- *     modulo a turn in 64-bit fixed point (off by |p w| 2^-53 turns at most).
+ *     modulo a turn in 64-bit fixed point, off by |p| (2^-65 + |w| 2^-53) turns at
+ *     most (inv_freq: 2^-55 for 2^-53), and the angle is rounded to 2^-32 turns.
  *   n_axes: 1 .. 4; axis_of: host array [head_dim / 2] of axes in [0, n_axes).
  * q_out may not overlap the positions.  A call captured into a graph reads the
  * positions when it is replayed. */
