@@ -244,15 +244,19 @@ extern "C" sp_status sp_attach_page_bounds(sp_cache* c, void* buffer) {
     if (reinterpret_cast<uintptr_t>(buffer) & 255) return fail(SP_ERR_INVALID_ARG, "buffer must be 256-byte aligned");
     for (const int32_t n : c->h_seqlen)
         if (n != 0) return fail(SP_ERR_INVALID_ARG, "the cache holds tokens; release them first");
+    const sp_status s = check_device(c);
+    if (s != SP_OK) return s;
+    // Released sequences may still have writes and decodes on their way: they end before
+    // a buffer is let go or cleared.
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_fail(e, "waiting for the device");
     if (!buffer) {
         c->bounds = PageBounds{};
         return SP_OK;
     }
-    const sp_status s = check_device(c);
-    if (s != SP_OK) return s;
     PageBounds b;
     const size_t bytes = place(c->cfg, c->geo.max_pages_unit, static_cast<uint8_t*>(buffer), &b);
-    cudaError_t e = cudaMemset(buffer, 0, bytes);
+    e = cudaMemset(buffer, 0, bytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "page bounds initialisation");
     c->bounds = b;

@@ -326,13 +326,17 @@ sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
  *   >= 0; each at most 2^20.
  *
  * The bounds live in a caller-owned device buffer (256-byte aligned, at least
- * sp_page_bounds_bytes bytes: 2 * head_dim + 4 per page, and scratch of the choice),
- * attached while no sequence holds tokens (SP_ERR_INVALID_ARG otherwise; null
- * detaches; synchronous) and kept alive until it is detached or the cache destroyed.  From then on every call that writes keys (sp_build_cache,
- * sp_append_kv, the rope forms, sp_rope_realign, sp_unpack_seq) also computes the
- * bounds of the full pages that it touched, in one more launch; attach the buffer
- * before capturing such calls.  Two decodes of one cache share the scratch, as they share the
- * workspace: stream order. */
+ * sp_page_bounds_bytes bytes: 2 * head_dim + 4 per page, and as scratch of the choice
+ * 8 bytes for every page that max_batch sequences of max_seq_len tokens have in one
+ * layer), attached while no sequence holds tokens (SP_ERR_INVALID_ARG otherwise; null
+ * detaches).  Both wait for the device first, so that no earlier call still uses a
+ * buffer that is detached or replaced; keep it alive until then, or until the cache is
+ * destroyed, and replay no graph captured with it afterwards.  While it is attached,
+ * every call that writes keys (sp_build_cache, sp_append_kv, the rope forms,
+ * sp_rope_realign, sp_unpack_seq) also computes the bounds of the full pages that it
+ * touched, in one more launch a layer; attach the buffer before capturing such calls.
+ * Two decodes of one cache share the scratch, as they share the workspace: stream
+ * order. */
 sp_status sp_page_bounds_bytes(const sp_config* cfg, size_t* bytes);
 sp_status sp_attach_page_bounds(sp_cache* cache, void* buffer);
 sp_status sp_attention_decode_select(sp_cache* cache, int32_t layer, const int32_t* seq_ids,
