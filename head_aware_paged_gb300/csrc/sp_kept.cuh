@@ -708,7 +708,9 @@ struct KeptLaunch {
 
 // Microseconds until the last of the units ends, of which `at_once` run side by side
 // and the others in turn: a start and a merge, a choice where there is one, and the
-// steps of a unit's warps (measured: 6.5, 4 and 1.1 us).
+// steps of a unit's warps (measured on bf16 pages of d 128: 6.5, 4 and 1.1 us; for
+// other types only the comparison of two spans is used, in which all terms are larger
+// or smaller together).
 inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
     float busy[kKeptLoads] = {};
     const int n = at_once < kKeptLoads ? at_once : kKeptLoads;
@@ -735,14 +737,29 @@ inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
 //
 // A unit is one cluster's work, so many pages of few units, or of some among many
 // light ones, leave most of the GPU waiting for them, and k_decode, which shares all
-// pages out evenly, is ahead although it starts after the choice.  Up to 48 groups a
-// warp of the longest unit this way was never behind; units of about the same length
-// bear more (groups a warp, then microseconds in one launch / in two; 32K tokens a
-// sequence: bf16, 32 sequences, 64: 107 / 136, 128: 194 / 210, 256: 369 / 359; 16
-// sequences, 128: 192 / 190; FP8, 32 sequences, 64: 81 / 105, 128: 143 / 144; 4 bits,
-// 64: 64 / 82, 128: 109 / 105.  One GLOBAL head of eight, 32 sequences: bf16 32: 62 / 71,
-// 64: 98 / 75; FP8 78 / 60; 4 bits 63 / 47.  One sequence of 128K, blocks of 8 warps, 64:
-// bf16 89 / 75, FP8 75 / 71, 4 bits 64 / 54, 32: 53 / 55, 45 / 56, 41 / 47).
+// pages out evenly, is ahead although it starts after the choice.  What decides is the
+// groups a warp of the longest unit, and how much of the work is the longest units'
+// kind.  Microseconds in one launch / in two, L2 flushed, 8 KV heads of 4 query heads,
+// d 128, at that many groups a warp:
+//   largest clusters (16 blocks a unit, a few units), whatever the other units are: of 8
+//     warps to 64, of 4 to 48.  1 x 128K, one head of eight GLOBAL, 56: bf16 81 / 116, FP8
+//     68 / 153, 4 bits 60 / 70, bf16 of d 64 capped 66 / 81; two heads 81 / 98, 67 / 143,
+//     60 / 92, 66 / 75; 2 x 64K, one head (4 warps), 40: 60 / 63, 52 / 77, 42 / 44,
+//     50 / 47, 48: 69 / 65, 58 / 85, 48 / 47, 56 / 50, 56: 78 / 67, 66 / 94, 52 / 50, 62 / 51.
+//   the longest units' kind is half of the work or more: to 48.  Four heads of eight
+//     GLOBAL, 48: 4 x 64K 76 / 73, 62 / 69, 56 / 49; 16 x 32K 76 / 79, 64 / 67, 52 / 49;
+//     32 x 32K 85 / 94, 72 / 78, 60 / 59.  All eight, 1 x 128K 76 / 76, 64 / 71, 56 / 55.
+//   less: to 24.  One head of eight, 4 x 64K 24: 46 / 43, 40 / 43, 36 / 36, 32: 55 / 49,
+//     47 / 51, 42 / 37; 8 x 64K 16: 40 / 39, 37 / 47, 31 / 35, 24: 49 / 40, 44 / 50, 36 / 36;
+//     32 x 32K 24: 56 / 59, 48 / 51, 42 / 42, 48: 83 / 65, 70 / 54, 58 / 44.
+// d 64 and capped scores cross a little earlier (bf16, d 64, capped, four heads of eight, 40:
+// 16 x 32K 54 / 52, 32 x 32K 58 / 57; 8 x 64K one head 16: 33 / 34, 24: 41 / 33); they
+// take the same limits.  Of 400 calls around the limits (15 shapes, these types) the way
+// taken was 2 % behind the better one on average, 22 % at most.
+// Units of about the same length on blocks of 4 warps bear more (32K tokens a sequence:
+// bf16, 32 sequences, 64: 107 / 136, 128: 194 / 210, 256: 369 / 359; 16 sequences, 128:
+// 192 / 190; FP8, 32 sequences, 64: 81 / 105, 128: 143 / 144; 4 bits, 64: 64 / 82, 128:
+// 109 / 105).
 template <int KV, int D, int NH, bool CAP>
 cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, bool& serves, cudaStream_t s) {
     typedef KeptLaunch<KV, D, NH, 8, CAP> Eight;
@@ -772,9 +789,10 @@ cudaError_t launch_kept_heads(KeptParams& p, const KeptLoad& load, bool& serves,
         for (int r = 3; r > 0 && ranks == 0; --r)
             if (units <= four.units[r]) ranks = r;
     }
-    const int64_t per_warp = load.longest / (warps << ranks);
-    const bool even = 4 * load.total >= 3 * load.longest * units;
-    serves = per_warp <= 48 || (warps == 4 && even && per_warp <= (KV == kRowsBf16 ? 128 : 64));
+    const int64_t per_warp = cdiv64(load.longest, warps << ranks), full = load.longest * units;
+    const bool half = 2 * load.total >= full, even = 4 * load.total >= 3 * full;
+    const int limit = ranks == 4 ? (warps == 8 ? 64 : 48) : half ? 48 : 24;
+    serves = per_warp <= limit || (warps == 4 && even && per_warp <= (KV == kRowsBf16 ? 128 : 64));
     if (!serves) return cudaSuccess;
     return warps == 8 ? Eight::run(p, ranks, s) : Four::run(p, ranks, s);
 }
