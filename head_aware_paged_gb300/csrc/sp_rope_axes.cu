@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(kRotThreads) k_rope_axes(const __grid_constant
         reinterpret_cast<float2*>(cs + (t * 4 + ((f & 7) >> 1)) * nc + (f >> 3))[f & 1] = cos_sin(at * p.turn[f]);
     }
     __syncthreads();
-    const int heads = p.hq + p.hkv, all = (n * heads) << lc, step = kRotThreads * gridDim.y;
-    for (int e = blockIdx.y * kRotThreads + tid; e < all; e += step) {
+    const int heads = p.hq + p.hkv, all = (n * heads) << lc;
+    for (int e = tid; e < all; e += kRotThreads) {
         const int c = e & (nc - 1), th = e >> lc, t = th / heads, h = th - t * heads;
         const bool is_q = h < p.hq;
         const int hh = is_q ? h : h - p.hq;
@@ -115,8 +115,8 @@ extern "C" sp_status sp_rope_axes(const void* q, int64_t q_stride, int32_t num_q
     p.hkv = num_kv_heads;
     p.d = head_dim;
     p.per = rows >= 2048 ? kRotRows : 1;
-    const dim3 grid((unsigned)((rows + p.per - 1) / p.per), 1);
-    k_rope_axes<<<grid, kRotThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const unsigned blocks = (unsigned)((rows + p.per - 1) / p.per);
+    k_rope_axes<<<blocks, kRotThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SP_OK : cuda_fail(e, "rotation launch");
 }
