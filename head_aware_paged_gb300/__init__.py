@@ -275,6 +275,9 @@ def sp_attention_decode_select(handle, layer: int, seq_ids: Sequence[int], q: to
                                score_cap: float = 0.0, stream=None) -> None:
     """sp_attention_decode in which GLOBAL heads read their first sink_pages, their
     newest recent_pages and the top_pages others with the highest scores."""
+    for n in (top_pages, sink_pages, recent_pages):       # (the call's integers have 32 bits)
+        if not -(1 << 31) <= n < 1 << 31:
+            raise OverflowError("page counts must fit 32 bits")
     ids = i32_buffer(seq_ids)
     check(load().sp_attention_decode_select(handle, layer, ids.buffer_info()[0], len(seq_ids), _ptr(q), top_pages,
                                             sink_pages, recent_pages, float(score_cap), _ptr(out), _ptr(lse),
