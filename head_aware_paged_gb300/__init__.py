@@ -466,6 +466,7 @@ class SegPagedCache:
         self._meta_raw, self.meta = self._aligned(meta_b, device)
         self._ws_raw, self.ws = self._aligned(ws_b, device)
         self._halves = None          # K and V views of the pool
+        self._bounds_raw = self._bounds = None
         self._index = self.pool.get_device()
         self.handle = sp_cache_create(cfg, self.pool, self.meta, self.ws)
 
@@ -607,10 +608,17 @@ class SegPagedCache:
         sp_attach_page_bounds(self.handle, buf)
         self._bounds_raw, self._bounds = raw, buf
 
+    def detach_page_bounds(self) -> None:
+        """Keep no bounds any more; the cache must hold no tokens."""
+        sp_attach_page_bounds(self.handle, None)
+        self._bounds_raw = self._bounds = None
+
     def page_bounds(self):
         """Views of the attached bounds: codes [num_pages, 2, head_dim] int8 (upper,
         lower) and their steps [num_pages] fp32, by physical page; what a page that
         is not a full one of a GLOBAL head holds means nothing."""
+        if self._bounds is None:
+            raise RuntimeError("no page bounds: call attach_page_bounds first")
         n, d = self.cfg.num_pages, self.cfg.head_dim
         at = (n * 2 * d + 255) // 256 * 256
         return self._bounds[:n * 2 * d].view(torch.int8).view(n, 2, d), self._bounds[at:at + 4 * n].view(torch.float32)

@@ -61,3 +61,28 @@ def test_the_same_buffer_again():
     torch.cuda.synchronize()
     codes, step = c.page_bounds()
     assert not codes.any() and not step.any()
+
+
+def test_without_bounds():
+    """Before they are attached and after they are detached: refused, and writes go on."""
+    import head_aware_paged_gb300 as H
+    gpu_ready()
+    c = _mk(4, 2, 64, 16, 1, 300, attach=False)
+    c.set_policy(0, to_c_policies([POLS]))
+    k, q = _keys(200, 2, 64, 1), W.normal((1, 4, 64), 9, device="cuda")
+    for _ in range(2):
+        with pytest.raises(RuntimeError):
+            c.page_bounds()
+        c.build(0, 0, k, k)
+        with pytest.raises(H.SegPagedError):
+            c.decode_select(0, [0], q, 2)
+        c.release(0)
+        c.attach_page_bounds()
+        c.build(0, 0, k, k)
+        _check_bounds(c, [0], [0, 1])
+        with pytest.raises(H.SegPagedError):                    # tokens held
+            c.detach_page_bounds()
+        c.page_bounds()
+        c.release(0)
+        c.detach_page_bounds()
+    assert c.status() == 0
