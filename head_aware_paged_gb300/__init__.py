@@ -255,7 +255,8 @@ def sp_rope_axes(q: Optional[torch.Tensor], k: Optional[torch.Tensor], axis_pos:
     of = i32_buffer(axis_of)
     check(load().sp_rope_axes(
         *args, d, rows, axis_pos.data_ptr(), per_axis, per_row, axes, of.buffer_info()[0], rope_theta,
-        _frequencies(inv_freq), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)))
+        _frequencies(inv_freq), _ptr(outs[0]), _ptr(outs[1]),
+        torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)))
     return tuple(outs)
 
 
@@ -275,9 +276,9 @@ def sp_attention_decode_select(handle, layer: int, seq_ids: Sequence[int], q: to
                                score_cap: float = 0.0, stream=None) -> None:
     """sp_attention_decode in which GLOBAL heads read their first sink_pages, their
     newest recent_pages and the top_pages others with the highest scores."""
-    for n in (top_pages, sink_pages, recent_pages):       # (the call's integers have 32 bits)
-        if not -(1 << 31) <= n < 1 << 31:
-            raise OverflowError("page counts must fit 32 bits")
+    # (the call's integers have 32 bits; a negative one is the library's to refuse)
+    if (top_pages | sink_pages | recent_pages) >> 31 not in (0, -1):
+        raise OverflowError("page counts must fit 32 bits")
     ids = i32_buffer(seq_ids)
     check(load().sp_attention_decode_select(handle, layer, ids.buffer_info()[0], len(seq_ids), _ptr(q), top_pages,
                                             sink_pages, recent_pages, float(score_cap), _ptr(out), _ptr(lse),
