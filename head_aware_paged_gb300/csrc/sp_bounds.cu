@@ -7,7 +7,7 @@
 // from L2 then), so nothing else has to remember which bounds are stale.  The
 // device's own length, page table and head class decide whether a page is
 // there and full, so a replayed write leaves them right whatever was appended
-// in between.
+// or released in between.
 //
 // Bound by latency: 2 P d bytes of keys a page come from L2, and a block looks up one
 // page.  An 8,192-token prompt of 8 GLOBAL heads (1,024 pages, 17 MB) 7.3 us; launched

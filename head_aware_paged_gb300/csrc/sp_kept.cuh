@@ -22,16 +22,18 @@
 // key's row serve as they come; V's rows of two keys are interleaved by byte
 // permutations.  P^T goes through two 8 x 8 register transposes.
 //
-// Scores, maxima, sums and partials are fp32; P is rounded to bf16 (2^-8 of a weight;
-// FP8 and 4-bit pages: f16, 2^-11), the query under channel scales to f16.  A score's
+// Scores, maxima, sums and partials are fp32.  P is rounded to V's type, for a product
+// takes both operands in one: bf16 (2^-8 of a weight; it brings a row's error against 64
+// bits from 0.0017, the output's own rounding, to 0.0019 .. 0.0023 of its norm), or f16 for
+// FP8 and 4-bit pages (2^-11, nothing to see); the query under channel scales to f16.  A score's
 // tanh is CUDA's (relative to the score it is exact to fp32; the difference of two
 // numbers of the cap's size that k_decode takes, which is shorter, was 9e-6 off at a cap
 // of 50 and showed in the lse of few keys; no difference in time).
 //
 // What it takes (8 KV heads of 4 query heads, d 128, page 64; with a launch for the
 // choice in brackets): 1 x 4K, 16 of 64 pages 8.5 us (23); 1 x 128K, two heads GLOBAL,
-// 128 of 2,048 pages 15.4 (40); 32 x 32K, all GLOBAL, 32 of 512 pages 61 (72): 8.5 us of
-// it reading 34 MB of bounds, 2 choosing, 43 streaming 268 MB at 6.2 TB/s.  Small
+// 128 of 2,048 pages 15.4 (40); 32 x 32K, all GLOBAL, 32 of 512 pages 61 (72): 9 us of
+// it reading 34 MB of bounds, 2.5 until the stream starts, 43 streaming 268 MB at 6.2 TB/s.  Small
 // calls are bound by their chain: look-ups, three barriers and about 1.1 us a step of
 // 16 bf16 keys a warp.
 //
