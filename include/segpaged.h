@@ -329,9 +329,9 @@ sp_status sp_attention_decode_capped(sp_cache* cache, int32_t layer,
  * sp_page_bounds_bytes bytes: 2 * head_dim + 4 per page, and as scratch of the choice
  * 8 bytes for every page that max_batch sequences of max_seq_len tokens have in one
  * layer), attached while no sequence holds tokens (SP_ERR_INVALID_ARG otherwise; null
- * detaches).  Both wait for the device first, so that no earlier call still uses a
- * buffer that is detached or replaced; keep it alive until then, or until the cache is
- * destroyed, and replay no graph captured with it afterwards.  While it is attached,
+ * detaches).  Both want the cache's device to be current and wait for it first, so that
+ * no earlier call still uses a buffer that is detached or replaced; keep it alive until
+ * then, or until the cache is destroyed, and replay no graph captured with it afterwards.  While it is attached,
  * every call that writes keys (sp_build_cache, sp_append_kv, the rope forms,
  * sp_rope_realign, sp_unpack_seq) also computes the bounds of the full pages that it
  * touched, in one more launch a layer; attach the buffer before capturing such calls.
