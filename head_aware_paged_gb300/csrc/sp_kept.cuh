@@ -710,9 +710,8 @@ struct KeptLaunch {
 
 // Microseconds until the last of the units ends, of which `at_once` run side by side
 // and the others in turn: a start and a merge, a choice where there is one, and the
-// steps of a unit's warps (measured on bf16 pages of d 128: 6.5, 4 and 1.1 us; for
-// other types only the comparison of two spans is used, in which all terms are larger
-// or smaller together).
+// steps of a unit's warps (measured on bf16 pages of d 128: 6.5, 4 and 1.1 us; other
+// types take the same numbers).
 inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
     float busy[kKeptLoads] = {};
     const int n = at_once < kKeptLoads ? at_once : kKeptLoads;
@@ -756,8 +755,9 @@ inline float kept_span(const KeptLoad& load, int at_once, int groups_a_step) {
 //     32 x 32K 24: 56 / 59, 48 / 51, 42 / 42, 48: 83 / 65, 70 / 54, 58 / 44.
 // d 64 and capped scores cross a little earlier (bf16, d 64, capped, four heads of eight, 40:
 // 16 x 32K 54 / 52, 32 x 32K 58 / 57; 8 x 64K one head 16: 33 / 34, 24: 41 / 33); they
-// take the same limits.  Of 400 calls around the limits (15 shapes, these types) the way
-// taken was 2 % behind the better one on average, 22 % at most.
+// take the same limits.  Of 630 calls around the limits (15 shapes, 16 to 62 groups, six
+// types) the way taken was 1.6 % behind the better one on average; to 48 groups 26 % at
+// most (capped scores on 4-bit pages), above 41 % (FP8, largest clusters of 4 warps).
 // Units of about the same length on blocks of 4 warps bear more (32K tokens a sequence:
 // bf16, 32 sequences, 64: 107 / 136, 128: 194 / 210, 256: 369 / 359; 16 sequences, 128:
 // 192 / 190; FP8, 32 sequences, 64: 81 / 105, 128: 143 / 144; 4 bits, 64: 64 / 82, 128:
